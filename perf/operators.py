@@ -232,7 +232,7 @@ def prepare(case, seed):
             st["plan"] = p = T.Plan(T.make_desc(1, 1, 64, 1, 8, 8, [], [(4, 4, 4)], [1]))
             new = lambda *s, t=BF16: torch.empty(*s, dtype=t, device="cuda")
             bwd = c["op"] == "linear_bwd"
-            st["ws"] = new(p.linear_workspace_bytes(M, K, N, backward=bwd), t=torch.uint8)
+            st["ws"] = new(p.linear_workspace_bytes(M, K, N, backward=bwd, samples=S if c["gate"] else 0), t=torch.uint8)
             if bwd:
                 st.update(dx=new(M, K), dw=new(N, K), dbias=new(N, t=F32) if c["bias"] else None,
                           dgate=new(S, N, t=F32) if c["gate"] else None)
