@@ -389,6 +389,175 @@ VSA_API vsa_status vsa_layer_forward(vsa_plan* plan, const void* q, const void* 
                              void* qp, void* kp, void* vp, float* scores, int32_t* idx,
                              void* op, float* lse, void* workspace, void* o, void* stream);
 
+/* ---- Around the layer: norm + rotation, linear, and the gradients ------------
+ *
+ * The operators that a transformer block runs next to the layer, on the same
+ * plan (its device, its error word, its wait limit), and what training it
+ * needs. They follow the conventions at the top of this file: bf16 tensors,
+ * fp32 parameters and statistics, asynchronous calls, caller-owned buffers and
+ * workspaces. A workspace is scratch of one call: calls that may overlap on the
+ * GPU (other streams, captured graphs replayed at the same time) need one each. */
+
+/* Element strides of a [B, N, heads, head_dim] view: heads and channels are
+ * contiguous, tokens `token` and batches `batch` elements apart. token >=
+ * heads * head_dim, both multiples of 8, batch >= 0. So q, k and v may be slices of one
+ * projection's [B, N, 3, heads, head_dim] output. */
+typedef struct {
+  int64_t batch, token;
+} vsa_strides;
+
+typedef enum {
+  VSA_ROPE_INTERLEAVED = 0,   /* pairs of channels (2i, 2i + 1) */
+  VSA_ROPE_HALVES = 1         /* pairs of channels (i, i + head_dim / 2) */
+} vsa_rope_layout;
+
+/* RMS norm per head row and rotary position embedding. For a row x of head_dim
+ * channels: n = x * rsqrt(mean(x^2) + eps) * w, then pair i of n turns by the
+ * token's angle i: (a, b) -> (a cos - b sin, a sin + b cos). */
+typedef struct {
+  const float* w_q;           /* [head_dim], or [heads][head_dim] with per_head; NULL: ones */
+  const float* w_k;
+  const float* cos_table;     /* [n_tokens][head_dim / 2], shared by batches and heads; both */
+  const float* sin_table;     /* NULL: no rotation */
+  int32_t per_head;           /* 0 or 1 */
+  int32_t layout;             /* vsa_rope_layout */
+  float eps;                  /* finite, >= 0 */
+} vsa_norm_rope;
+
+/* q_out, k_out = norm and rotation of q and k ([B, N, heads, head_dim] bf16).
+ * strides: a host array of four (q, k, q_out, k_out), or NULL: all contiguous.
+ * An output may be its own input (same pointer and strides); otherwise outputs
+ * overlap nothing. Statistics and rotation in fp32, one rounding. */
+VSA_API vsa_status vsa_qk_norm_rope(vsa_plan* plan, const vsa_norm_rope* norm, const void* q, const void* k,
+                                    void* q_out, void* k_out, const vsa_strides* strides, void* stream);
+
+/* vsa_qk_norm_rope followed by vsa_tile_pack_pool in one pass, bit for bit:
+ * packed tiles of the normed and turned q and k and of v, and the descriptors
+ * in `workspace` (follow with vsa_tile_score_pooled). strides: a host array of
+ * three (q, k, v), or NULL: contiguous. Descriptors of video tiles past a
+ * head's own are zero. */
+VSA_API vsa_status vsa_tile_norm_rope_pack_pool(vsa_plan* plan, const vsa_norm_rope* norm, const void* q,
+                                                const void* k, const void* v, const vsa_strides* strides, void* qp,
+                                                void* kp, void* vp, void* workspace, void* stream);
+
+/* Where the pooling calls (vsa_tile_pack_pool, vsa_tile_norm_rope_pack_pool,
+ * vsa_tile_pool) leave the descriptors in `workspace`: fp32 [B, heads, ntv_max,
+ * w] of Q and of K, w = head_dim (TripPool: 3 head_dim, mean, max, min). */
+VSA_API vsa_status vsa_pooled_descriptors(const vsa_plan* plan, void* workspace, float** pooled_q, float** pooled_k);
+
+/* Workspace of the two gradient calls below, in bytes. */
+VSA_API vsa_status vsa_norm_bwd_workspace(const vsa_plan* plan, int64_t* bytes);
+
+/* Gradient of vsa_qk_norm_rope: from dq_out, dk_out (gradients of its results)
+ * and its inputs q, k, the gradients dq, dk (bf16) and those of the weights, dw_q and dw_k
+ * (fp32, the weights' shape; either may be NULL). With dn = dy turned back, r
+ * the row's rsqrt, xr = x r and g = dn w: dx = r (g - xr mean(g xr)), dw = sum
+ * over the rows of dn xr (fixed order, the same result on every call).
+ * strides: a host array of six (dq_out, dk_out, q, k, dq, dk), or NULL. dq may be
+ * dq_out or q, dk likewise (same pointer and strides). workspace: 256-byte aligned. */
+VSA_API vsa_status vsa_qk_norm_rope_bwd(vsa_plan* plan, const vsa_norm_rope* norm, const void* dq_out,
+                                        const void* dk_out, const void* q, const void* k, void* dq, void* dk,
+                                        const vsa_strides* strides, float* dw_q, float* dw_k, void* workspace,
+                                        void* stream);
+
+/* Gradient of vsa_tile_norm_rope_pack_pool (the descriptors carry none: they
+ * only choose tiles): dqp, dkp, dvp packed as vsa_sparse_attn_bwd writes them,
+ * q and k the forward's inputs, dq, dk, dv token-major. strides: a host array
+ * of five (q, k, dq, dk, dv), or NULL. Otherwise as vsa_qk_norm_rope_bwd. */
+VSA_API vsa_status vsa_tile_norm_rope_bwd(vsa_plan* plan, const vsa_norm_rope* norm, const void* dqp,
+                                          const void* dkp, const void* dvp, const void* q, const void* k, void* dq,
+                                          void* dk, void* dv, const vsa_strides* strides, float* dw_q, float* dw_k,
+                                          void* workspace, void* stream);
+
+/* Gradient of vsa_sparse_attn (the index lists are taken as given): with P =
+ * exp(scale q k^T - lse) over the keys each query row keeps and delta =
+ * rowsum(do o), dV = P^T dO, dS = P (dO V^T - delta), dQ = scale dS K,
+ * dK = scale dS^T Q. qp, kp, vp, idx and k_per_head are the forward's inputs, op
+ * and lse its outputs, dop the packed gradient of op (vsa_tile_pack of the
+ * token-major gradient: rows of unused slots must be finite, as the pack
+ * leaves them). dqp, dkp, dvp (packed bf16) are written in full: zero in
+ * unused slots and in tiles past a head's own count. P and dS are rounded to
+ * bf16 for their products, sums are fp32 in a fixed order: no atomics, the
+ * same result on every call. A list that is out of range or not ascending
+ * latches VSA_ERR_BAD_INDEX and its query tile takes no part. workspace:
+ * vsa_attn_bwd_workspace bytes, 256-byte aligned. */
+VSA_API vsa_status vsa_attn_bwd_workspace(const vsa_plan* plan, int64_t* bytes);
+VSA_API vsa_status vsa_sparse_attn_bwd(vsa_plan* plan, const void* qp, const void* kp, const void* vp, const void* op,
+                                       const float* lse, const void* dop, const int32_t* idx,
+                                       const int32_t* k_per_head, void* dqp, void* dkp, void* dvp, void* workspace,
+                                       void* stream);
+
+/* Gradient of vsa_sparse_attn_ref: the same with the reference tiles' lists. */
+VSA_API vsa_status vsa_sparse_attn_ref_bwd(vsa_plan* plan, const void* qp, const void* kp, const void* vp,
+                                           const void* op, const float* lse, const void* dop, const int32_t* idx,
+                                           const int32_t* idx_ref, const int32_t* k_per_head, void* dqp, void* dkp,
+                                           void* dvp, void* workspace, void* stream);
+
+typedef enum {
+  VSA_ACT_NONE = 0,
+  VSA_ACT_GELU_TANH = 1,      /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  VSA_ACT_SILU = 2            /* z / (1 + e^-z) */
+} vsa_act;
+
+/* y = residual + gate * act(x w^T + bias). x [rows, n_in], w [n_out, n_in]
+ * (contiguous), y, residual and pre [rows, n_out] bf16, bias [n_out] fp32, gate
+ * [rows / rows_per_gate, n_out] fp32: row r uses gate row r / rows_per_gate (a
+ * sample's rows share one). n_in and n_out are multiples of 8, rows < 2^31, any
+ * rows >= 0; leading dimensions (row strides in elements) are multiples of 8.
+ * NULL bias, gate, residual: left out. pre, if given, gets x w^T + bias for the
+ * gradient. y may be residual (same pointer and stride); otherwise outputs
+ * overlap nothing. fp32 accumulation and epilogue, one rounding. */
+typedef struct {
+  int64_t rows;
+  int32_t n_in, n_out;
+  const void* x;
+  int64_t ld_x;
+  const void* w;
+  const float* bias;
+  int32_t act;                /* vsa_act */
+  const float* gate;
+  int64_t rows_per_gate;      /* divides rows; read only with a gate */
+  const void* residual;
+  int64_t ld_residual;
+  void* y;
+  int64_t ld_y;
+  void* pre;
+  int64_t ld_pre;
+} vsa_linear_args;
+
+/* Workspace of vsa_linear (backward 0) or vsa_linear_bwd (1) in bytes (0: none
+ * is needed); with a gate, rows_per_gate as in the call, else 0. Sizes that the
+ * calls refuse are refused. */
+VSA_API vsa_status vsa_linear_workspace(const vsa_plan* plan, int64_t rows, int32_t n_in, int32_t n_out,
+                                        int32_t backward, int64_t rows_per_gate, int64_t* bytes);
+VSA_API vsa_status vsa_linear(vsa_plan* plan, const vsa_linear_args* args, void* workspace, void* stream);
+
+/* Gradient of vsa_linear (that of the residual is dy itself): with dz = gate *
+ * dy * act'(pre), dx = dz w (bf16), dw = dz^T x (bf16), dbias = sum of dz,
+ * dgate = per sample the sum of dy act(pre) (fp32). Any of the four may be NULL.
+ * pre is needed with an activation or for dgate. dz is rounded to bf16 for the
+ * two products; dbias and dgate are summed unrounded, in a fixed order. */
+typedef struct {
+  int64_t rows;
+  int32_t n_in, n_out;
+  const void* dy;
+  int64_t ld_dy;
+  const void* x;
+  int64_t ld_x;
+  const void* w;
+  int32_t act;
+  const void* pre;
+  int64_t ld_pre;
+  const float* gate;
+  int64_t rows_per_gate;
+  void* dx;
+  int64_t ld_dx;
+  void* dw;
+  float* dbias;
+  float* dgate;
+} vsa_linear_grad_args;
+VSA_API vsa_status vsa_linear_bwd(vsa_plan* plan, const vsa_linear_grad_args* args, void* workspace, void* stream);
+
 /* Bound of every device-side wait of the plan's tcgen05 kernels (attention,
  * teacher map), in nanoseconds: 1,000 .. 60,000,000,000; 0 restores the
  * default of two seconds. A kernel whose wait runs past it stops: it latches

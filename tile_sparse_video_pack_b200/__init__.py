@@ -7,6 +7,7 @@ attention, tile unpack. This package is the thin Python binding.
 from .vsa import (  # noqa: F401
     EXPORTS,
     LIB_PATH,
+    NormRope,
     Plan,
     VsaError,
     k_from_sparsity,

@@ -13,8 +13,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libvsa.so")
-SOURCES = ["vsa_api.cu", "pack.cu", "score.cu", "topk.cu", "attn.cu", "teacher.cu"]
-HEADERS = ["vsa_internal.h", "tc_sm100.h"]
+SOURCES = ["vsa_api.cu", "pack.cu", "score.cu", "topk.cu", "attn.cu", "teacher.cu", "norm_rope.cu", "linear.cu",
+           "attn_bwd.cu"]
+HEADERS = ["vsa_internal.h", "tc_sm100.h", "tile_map.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

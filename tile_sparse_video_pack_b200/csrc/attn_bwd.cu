@@ -1,0 +1,684 @@
+// Gradient of the tile-sparse attention (TMA + tcgen05/TMEM).
+//
+// With P = exp(scale q k^T - lse) over the key tiles each query tile keeps,
+// o = P v and delta = rowsum(do o):
+//   dV = P^T dO,   dS = P (dO V^T - delta),   dQ = scale dS K,   dK = scale dS^T Q.
+// P is rebuilt from the forward's log-sum-exp, so nothing of size rows x keys
+// is stored.
+//
+// Two passes of one kernel, each with its own stationary 64-row tile whose
+// gradient stays in tensor memory from its first to its last partner, so that
+// no sum is spread over CTAs and no atomics decide its order:
+//   key pass    stationary key tile (K, V), streamed query tiles (Q, dO): dK, dV
+//   query pass  stationary query tile (Q, dO), streamed key tiles (K, V): dQ
+// Write X, Y for the streamed pair (Q, dO or K, V) and Xs, Ys for the
+// stationary one (K, V or Q, dO). Two streamed tiles make 128 rows, so every
+// product has M = 128 without merging two tiles' lists:
+//   S = X Xs^T, dP = Y Ys^T           128 x 64, rows = streamed tokens (TMEM lanes)
+//   acc1^T += X^T dS (dK or dQ)       d x 64, and in the key pass acc0^T += Y^T P (dV)
+// The accumulators are transposed (lanes = channels) so that M is 128 for them
+// too; the streamed tile serves its first product K-major and its second
+// MN-major from the same shared-memory image. P and dS go through shared
+// memory as bf16, the operand type of the forward's P (half a step, 2^-9,
+// of each term).
+// The two passes cost 14 d operations per (query, key) pair where one pass
+// with a summed dQ would cost 10 d, but that sum would go through global
+// atomics, 32 KB per tile pair.
+//
+// Which tiles meet is a bit matrix per (batch, head), [query tile][key tile]:
+// built from the index lists (validated on the way), its transpose by 32 x 32
+// ballots. The producer walks the stationary tile's row of it.
+//
+// Warp roles (320 threads): warp 0 producer (item, bit row, TMA), warp 1 MMA,
+// warps 2-9 two warpgroups that turn S and dP of alternate streamed pairs into
+// P and dS and write the finished gradients. Every wait is bounded as in the
+// forward.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "tc_sm100.h"
+#include "tile_map.h"
+#include "vsa_internal.h"
+
+namespace vsa {
+namespace {
+
+using namespace tc;
+
+constexpr int kBThreads = 320;
+constexpr uint32_t kBox = 64 * 64 * 2;           // one 64 x 64 bf16 TMA box
+
+// ------------------------------------------------------------ preparation ----
+
+// Per packed row: log-sum-exp in log2 units, and delta = sum of do * o. Rows of
+// unused slots (and of tiles past a head's own) get +inf, so that P is 0.
+template <int CPR>
+__global__ void __launch_bounds__(256) bwd_rows_kernel(Geometry g, const uint4* __restrict__ o,
+                                                       const uint4* __restrict__ dO, const float* __restrict__ lse,
+                                                       const int32_t* __restrict__ counts, float* __restrict__ lse2,
+                                                       float* __restrict__ delta) {
+  const int64_t rows = int64_t(g.B) * g.Hh * g.nt_max * VSA_TILE;
+  const int c = threadIdx.x % CPR;
+  constexpr int R = 256 / CPR;
+  for (int64_t r0 = int64_t(blockIdx.x) * R; r0 < rows; r0 += int64_t(gridDim.x) * R) {
+    const int64_t row = r0 + threadIdx.x / CPR;  // rows is a multiple of R: every lane has one
+    const int64_t tile = row / VSA_TILE;
+    const int h = int((tile / g.nt_max) % g.Hh);
+    const bool valid = int(row % VSA_TILE) < counts[int64_t(h) * g.nt_max + tile % g.nt_max];
+    float s = 0.f;
+    if (valid) {
+      float a[8], b[8];
+      bf16x8_to_f32(o[row * CPR + c], a);
+      bf16x8_to_f32(dO[row * CPR + c], b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+    }
+#pragma unroll
+    for (int x = CPR / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    if (c == 0) {
+      lse2[row] = valid ? lse[row] * 1.4426950408889634f : INFINITY;
+      delta[row] = s;
+    }
+  }
+}
+
+struct BitParams {
+  const int32_t *idx, *idx_ref, *ref_tiles, *prefix_ref;
+  uint32_t *bits, *bits_t;   // [B * heads][words * 32][words]: query-major and its transpose
+  uint32_t* state;
+  int32_t heads, nt_max, ntv_max, k_max, n_pre, n_ref, k_ref_max, words;
+  int32_t ntv[VSA_MAX_HEADS], k[VSA_MAX_HEADS], k_ref[VSA_MAX_HEADS];
+};
+
+// One warp per (batch, head, query tile): its row of the bit matrix. A list out
+// of range or not ascending latches the error and leaves the row empty.
+__global__ void __launch_bounds__(128) bwd_bits_kernel(const __grid_constant__ BitParams p) {
+  extern __shared__ uint32_t sm[];
+  const int lane = threadIdx.x & 31;
+  uint32_t* row = sm + (threadIdx.x >> 5) * p.words;
+  const int rows = p.words * 32;
+  const int i = int(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int bh = blockIdx.y, h = bh % p.heads;
+  if (i >= rows) return;
+  const int nt = p.n_pre + p.ntv[h];
+  for (int w = lane; w < p.words; w += 32) row[w] = 0u;
+  __syncwarp();
+  bool bad = false;
+  if (i < p.n_pre) {
+    for (int t = lane; t < nt; t += 32) atomicOr(row + (t >> 5), 1u << (t & 31));
+  } else if (i < nt) {
+    for (int t = lane; t < p.n_pre; t += 32)
+      if (!p.idx_ref || p.prefix_ref[t] < 0) atomicOr(row + (t >> 5), 1u << (t & 31));
+    const int64_t vrow = int64_t(bh) * p.ntv_max + (i - p.n_pre);
+    auto add = [&](const int32_t* list, int n, int limit, bool ref) {
+      for (int e = lane; e < n; e += 32) {
+        const int j = list[e], before = e > 0 ? list[e - 1] : -1;
+        if (j < 0 || j >= limit || j <= before) {
+          bad = true;
+        } else {
+          const int t = ref ? p.ref_tiles[j] : p.n_pre + j;
+          atomicOr(row + (t >> 5), 1u << (t & 31));
+        }
+      }
+    };
+    if (p.idx_ref) add(p.idx_ref + vrow * p.k_ref_max, p.k_ref[h], p.n_ref, true);
+    add(p.idx + vrow * p.k_max, p.k[h], p.ntv[h], false);
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  if (bad && lane == 0) atomicOr(p.state, kErrBadIndex);
+  __syncwarp();
+  uint32_t* out = p.bits + (int64_t(bh) * rows + i) * p.words;
+  for (int w = lane; w < p.words; w += 32) out[w] = bad ? 0u : row[w];
+}
+
+// Transpose by 32 x 32 blocks: one warp per block.
+__global__ void __launch_bounds__(256) bwd_transpose_kernel(const uint32_t* __restrict__ bits,
+                                                            uint32_t* __restrict__ bits_t, int words, int64_t blocks) {
+  const int lane = threadIdx.x & 31;
+  const int64_t blk = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (blk >= blocks) return;
+  const int64_t bh = blk / (int64_t(words) * words);
+  const int in = int(blk - bh * words * words);
+  const int wi = in / words, wj = in % words;
+  const int64_t base = bh * words * 32;
+  const uint32_t x = bits[(base + wi * 32 + lane) * words + wj];
+  uint32_t mine = 0u;
+#pragma unroll
+  for (int b = 0; b < 32; ++b) {
+    const uint32_t v = __ballot_sync(0xffffffffu, (x >> b) & 1u);
+    if (lane == b) mine = v;
+  }
+  bits_t[(base + wj * 32 + lane) * words + wi] = mine;
+}
+
+// ------------------------------------------------------------------ kernel ----
+
+struct BwdItem {
+  int32_t bh, tile, pairs, count;   // pairs: streamed pairs; count: valid rows of the stationary tile
+  int32_t end, pad[3];
+};
+struct BwdPair {
+  int32_t ta, tb;                   // streamed tiles (tb < 0: none)
+};
+
+template <int D, bool KEY>
+struct BSmem {
+  static constexpr uint32_t kHalf = 128 * 128;                 // 128 rows x 64 channels
+  static constexpr uint32_t kTensor = (D / 64) * kHalf;        // one streamed tensor's pair
+  static constexpr uint32_t kStage = 2 * kTensor;              // Y, then X
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr uint32_t kStat = (D / 64) * kBox;           // one stationary tile
+  static constexpr uint32_t kPd = 128 * 128;                   // P or dS of a pair: 128 rows x 64 bf16
+  static constexpr uint32_t oStage = 0;
+  static constexpr uint32_t oStat = oStage + kStages * kStage;               // Xs, Ys
+  static constexpr uint32_t oDs = oStat + 2 * kStat;                         // two buffers
+  static constexpr uint32_t oP = oDs + 2 * kPd;                              // two buffers (key pass)
+  static constexpr uint32_t oBar = oP + (KEY ? 2 : 0) * kPd;
+  static constexpr uint32_t oMisc = oBar + 32 * 8;
+  static constexpr uint32_t oItem = oMisc + 16;
+  static constexpr uint32_t oPair = oItem + 2 * sizeof(BwdItem);
+  static constexpr uint32_t oCol = oPair + 4 * sizeof(BwdPair);              // query pass: lse2, delta of the tile
+  static constexpr uint32_t oEnd = oCol + (KEY ? 0 : 2 * 2 * 64 * 4);        // per warpgroup
+};
+
+enum {
+  Q_FULL = 0, Q_EMPTY = 4, Q_SFULL = 8, Q_PREADY = 10, Q_PFREE = 12, Q_IFULL = 14, Q_IEMPTY = 16, Q_STATFULL = 18,
+  Q_STATEMPTY, Q_ACCFULL, Q_ACCFREE, Q_DRAIN
+};
+
+struct BwdParams {
+  const uint32_t* bits;             // this pass's bit matrix (rows = stationary tiles)
+  const float *lse2, *delta;        // [B * heads][nt_max][64]
+  const int32_t* counts;            // [heads][nt_max]
+  __nv_bfloat16 *out0, *out1;       // key pass: dV, dK; query pass: out1 = dQ
+  uint32_t* state;                  // [0] error word
+  uint32_t* counter;                // work counter of this pass
+  uint64_t wait_ns;
+  int64_t n_items;
+  int32_t heads, bh_total, nt_max, words;
+  float scale_log2, scale;
+};
+
+template <int D, bool KEY>
+__global__ void __launch_bounds__(kBThreads, 1)
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
+                    const __grid_constant__ CUtensorMap txs, const __grid_constant__ CUtensorMap tys,
+                    const __grid_constant__ BwdParams prm) {
+  using L = BSmem<D, KEY>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + L::oBar + 8u * uint32_t(i); };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::oMisc);
+  volatile uint32_t* abort_flag = misc + 1;
+  BwdItem* items = reinterpret_cast<BwdItem*>(smem + L::oItem);
+  BwdPair* pairs = reinterpret_cast<BwdPair*>(smem + L::oPair);
+  uint32_t* gerr = prm.state;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kH = D / 64;                     // 64-channel halves
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(bar(Q_FULL + i), 1);
+      mbar_init(bar(Q_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(Q_SFULL + i), 1);
+      mbar_init(bar(Q_PREADY + i), 4);           // one arrival per warp of the warpgroup
+      mbar_init(bar(Q_PFREE + i), 1);
+      mbar_init(bar(Q_IFULL + i), 1);
+      mbar_init(bar(Q_IEMPTY + i), 9);           // MMA thread, eight warps
+    }
+    mbar_init(bar(Q_STATFULL), 1);
+    mbar_init(bar(Q_STATEMPTY), 1);
+    mbar_init(bar(Q_ACCFULL), 1);
+    mbar_init(bar(Q_ACCFREE), 8);
+    mbar_init(bar(Q_DRAIN), 1);
+    misc[1] = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sbase + L::oMisc));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  // TMEM: buffer b at columns 128 b: S [0, 64), dP [64, 128); acc0 (dV^T) at 256, acc1 (dK^T / dQ^T) at 320
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer ---
+    uint32_t g = 0;                              // streamed pairs issued
+    int stat_it = -1;                            // item of the last stationary load
+    bool ok = true;
+    for (uint32_t it = 0; ok; ++it) {
+      const int slot = it & 1;
+      if (lane == 0) ok = wait_bar(bar(Q_IEMPTY + slot), ((it >> 1) & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      uint32_t item = 0;
+      if (lane == 0) item = atomicAdd(prm.counter, 1u);
+      item = __shfl_sync(0xffffffffu, item, 0);
+      if (int64_t(item) >= prm.n_items) {
+        if (lane == 0) {
+          items[slot].end = 1;
+          mbar_arrive(bar(Q_IFULL + slot));
+        }
+        break;
+      }
+      // tile-major order: prefix tiles, which meet every tile, come first
+      const int tile = int(item / uint32_t(prm.bh_total)), bh = int(item % uint32_t(prm.bh_total));
+      const int h = bh % prm.heads;
+      const uint32_t* row = prm.bits + (int64_t(bh) * prm.words * 32 + tile) * prm.words;
+      int n = 0;
+      for (int w = lane; w < prm.words; w += 32) n += __popc(row[w]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      const int npairs = (n + 1) >> 1;
+      if (lane == 0) {
+        BwdItem& b = items[slot];
+        b.bh = bh;
+        b.tile = tile;
+        b.pairs = npairs;
+        b.count = prm.counts[int64_t(h) * prm.nt_max + tile];
+        b.end = 0;
+        mbar_arrive(bar(Q_IFULL + slot));
+        if (npairs > 0) {
+          ok = wait_bar(bar(Q_STATEMPTY), (it & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
+          if (ok) {
+            mbar_expect_tx(bar(Q_STATFULL), 2 * L::kStat);
+            const int y = (bh * prm.nt_max + tile) * 64;
+            for (int c = 0; c < kH; ++c) {
+              tma_load_2d(sbase + L::oStat + c * kBox, &txs, 64 * c, y, bar(Q_STATFULL));
+              tma_load_2d(sbase + L::oStat + L::kStat + c * kBox, &tys, 64 * c, y, bar(Q_STATFULL));
+            }
+            stat_it = int(it);
+          }
+        } else {                                 // nothing to load: keep the barrier's phases in step with the items
+          ok = wait_bar(bar(Q_STATEMPTY), (it & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
+          if (ok) mbar_arrive(bar(Q_STATFULL));
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      // the streamed tiles, two at a time, in ascending order
+      int first = -1;
+      for (int w0 = 0; w0 < prm.words && ok; w0 += 32) {
+        const uint32_t mine = w0 + lane < prm.words ? row[w0 + lane] : 0u;
+        const int wn = min(32, prm.words - w0);
+        for (int w = 0; w <= wn && ok; ++w) {
+          uint32_t bitsw = w < wn ? __shfl_sync(0xffffffffu, mine, w) : 0u;
+          const bool last = w == wn && w0 + 32 >= prm.words;   // after the last word: a tile left over
+          if (w == wn && !last) break;
+          while ((bitsw || (last && first >= 0)) && ok) {
+            int t = -1;
+            if (bitsw) {
+              t = (w0 + w) * 32 + __ffs(bitsw) - 1;
+              bitsw &= bitsw - 1;
+              if (first < 0) {
+                first = t;
+                continue;
+              }
+            }
+            if (lane == 0) {
+              const int st = int(g % L::kStages);
+              ok = wait_bar(bar(Q_EMPTY + st), ((g / L::kStages) & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
+              if (ok) {
+                pairs[st].ta = first;
+                pairs[st].tb = t;
+                const uint32_t fb = bar(Q_FULL + st);
+                mbar_expect_tx(fb, L::kStage);
+                const int ya = (bh * prm.nt_max + first) * 64, yb = t >= 0 ? (bh * prm.nt_max + t) * 64 : ya;
+                const uint32_t sy = sbase + L::oStage + st * L::kStage, sx = sy + L::kTensor;
+                for (int c = 0; c < kH; ++c) {
+                  tma_load_2d(sx + c * L::kHalf, &tx, 64 * c, ya, fb);
+                  tma_load_2d(sx + c * L::kHalf + kBox, &tx, 64 * c, yb, fb);
+                }
+                for (int c = 0; c < kH; ++c) {
+                  tma_load_2d(sy + c * L::kHalf, &ty, 64 * c, ya, fb);
+                  tma_load_2d(sy + c * L::kHalf + kBox, &ty, 64 * c, yb, fb);
+                }
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (ok) ++g;
+            first = -1;
+          }
+        }
+      }
+    }
+    if (lane == 0 && *abort_flag) {              // let the copies land before shared memory is released
+      if (stat_it >= 0) drain_wait(bar(Q_STATFULL), uint32_t(stat_it) & 1);
+      for (uint32_t j = g >= uint32_t(L::kStages) ? g - L::kStages : 0; j < g; ++j)
+        drain_wait(bar(Q_FULL + int(j % L::kStages)), (j / L::kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMA ---
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0);
+      constexpr uint32_t idA = idesc_bf16(128, 64, 1, 1);
+      const uint64_t dxs = sw128_desc(sbase + L::oStat, 16, 1024);
+      const uint64_t dys = sw128_desc(sbase + L::oStat + L::kStat, 16, 1024);
+      uint32_t g = 0;                            // streamed pairs of earlier items
+      bool ok = true;
+      // S and dP of pair p into buffer p & 1
+      auto scores = [&](uint32_t p) {
+        const int st = int(p % L::kStages);
+        if (!wait_bar(bar(Q_FULL + st), (p / L::kStages) & 1, abort_flag, gerr, prm.wait_ns)) return false;
+        tc_fence_after();
+        const uint32_t sy = sbase + L::oStage + st * L::kStage, sx = sy + L::kTensor;
+        const uint64_t dx = sw128_desc(sx, 16, 1024), dy = sw128_desc(sy, 16, 1024);
+        const uint32_t tS = tmem + (p & 1) * 128;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma(tS, dx + (((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4), dxs + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
+                 idS, kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma(tS + 64, dy + (((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4),
+                 dys + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+        tc_commit(bar(Q_SFULL + int(p & 1)));
+        return true;
+      };
+      for (uint32_t it = 0; ok; ++it) {
+        const int slot = it & 1;
+        if (!(ok = wait_bar(bar(Q_IFULL + slot), (it >> 1) & 1, abort_flag, gerr, prm.wait_ns))) break;
+        const int npairs = items[slot].pairs;
+        const bool end = items[slot].end != 0;
+        mbar_arrive(bar(Q_IEMPTY + slot));
+        if (end) break;
+        if (!(ok = wait_bar(bar(Q_STATFULL), it & 1, abort_flag, gerr, prm.wait_ns))) break;
+        // the accumulators are free once the previous item's gradients are read
+        if (!(ok = wait_bar(bar(Q_ACCFREE), (it & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
+        tc_fence_after();
+        if (npairs > 0 && !(ok = scores(g))) break;
+        if (npairs <= 1) tc_commit(bar(Q_STATEMPTY));
+        for (int j = 0; j < npairs; ++j, ++g) {
+          if (j + 1 < npairs) {
+            // buffer (g + 1) & 1 was read before PREADY of pair g - 1, which was waited for
+            if (!(ok = scores(g + 1))) break;
+            if (j + 2 == npairs) tc_commit(bar(Q_STATEMPTY));
+          }
+          const int b = g & 1;
+          if (!(ok = wait_bar(bar(Q_PREADY + b), (g >> 1) & 1, abort_flag, gerr, prm.wait_ns))) break;
+          tc_fence_after();
+          const int st = int(g % L::kStages);
+          const uint32_t sy = sbase + L::oStage + st * L::kStage;
+          // A = Y^T and X^T, MN-major: 64-channel chunks kHalf apart. For d = 64 both
+          // are one operand of 128 channels, [Y; X]: dV^T is in lanes 0-63 of acc0,
+          // dK^T / dQ^T in lanes 64-127 of acc1, and the other halves are not used.
+          const uint64_t day = sw128_desc(sy, L::kHalf, 1024);
+          const uint64_t dax = D == 128 ? sw128_desc(sy + L::kTensor, L::kHalf, 1024) : day;
+          const uint64_t dds = sw128_desc(sbase + L::oDs + b * L::kPd, 8192, 1024);
+          const uint64_t dp = sw128_desc(sbase + L::oP + b * L::kPd, 8192, 1024);
+          if constexpr (KEY) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)       // 16 streamed rows per step
+              tc_mma(tmem + 256, day + ((kk * 2048) >> 4), dp + ((kk * 2048) >> 4), idA, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma(tmem + 320, dax + ((kk * 2048) >> 4), dds + ((kk * 2048) >> 4), idA, (j > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(bar(Q_EMPTY + st));
+          tc_commit(bar(Q_PFREE + b));
+        }
+        if (!ok) break;
+        tc_commit(bar(Q_ACCFULL));
+      }
+      tc_commit(bar(Q_DRAIN));
+      drain_wait(bar(Q_DRAIN), 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------- P, dS, output ---
+    const int wg = (warp - 2) >> 2;
+    const int q4 = warp & 3;                     // TMEM lane quarter this warp may read
+    const int r = q4 * 32 + lane;                // streamed row, TMEM lane
+    const uint32_t lane_off = uint32_t(q4 * 32) << 16;
+    float* col = reinterpret_cast<float*>(smem + L::oCol) + wg * 128;   // query pass: lse2 [64], delta [64]
+    uint32_t g = 0;
+    bool ok = true;
+    for (uint32_t it = 0; ok; ++it) {
+      const int slot = it & 1;
+      ok = wait_bar(bar(Q_IFULL + slot), (it >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const BwdItem inf = items[slot];
+      warp_arrive(bar(Q_IEMPTY + slot));
+      if (inf.end) break;
+      const int h = inf.bh % prm.heads;
+      const int64_t base = int64_t(inf.bh) * prm.nt_max;
+      if constexpr (!KEY) {
+        // this warpgroup's copy of the stationary queries' lse2 and delta; its warps meet
+        // before the write (the previous item's reads) and after it
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+        const int x = (warp - 2 - 4 * wg) * 32 + lane;
+        col[x] = x < 64 ? prm.lse2[(base + inf.tile) * 64 + x] : prm.delta[(base + inf.tile) * 64 + x - 64];
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+      }
+      for (int j = 0; j < inf.pairs; ++j, ++g) {
+        if (int(g & 1) != wg) continue;
+        const int st = int(g % L::kStages);
+        ok = wait_bar(bar(Q_FULL + st), (g / L::kStages) & 1, abort_flag, gerr, prm.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        const int tile = r < 64 ? pairs[st].ta : pairs[st].tb;
+        float rl = 0.f, rd = 0.f;                // key pass: lse2, delta of my query row
+        bool live = tile >= 0;
+        if (live) {
+          if constexpr (KEY) {
+            rl = prm.lse2[(base + tile) * 64 + (r & 63)];
+            rd = prm.delta[(base + tile) * 64 + (r & 63)];
+            live = rl < INFINITY;
+          } else {
+            live = (r & 63) < prm.counts[int64_t(h) * prm.nt_max + tile];
+          }
+        }
+        ok = wait_bar(bar(Q_SFULL + wg), (g >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t pk[KEY ? 32 : 1], dk[32];
+        const uint32_t tS = tmem + wg * 128 + lane_off;
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t s[32], dp[32];
+          tmem_ld32(tS + c, s);
+          tmem_ld32(tS + 64 + c, dp);
+          tmem_wait_ld(s);
+          reg_fence(dp);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float p[2], ds[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float l2 = KEY ? rl : col[c + i + e], dl = KEY ? rd : col[64 + c + i + e];
+              const float x = ex2(fmaf(__uint_as_float(s[i + e]), prm.scale_log2, -l2));
+              p[e] = live ? x : 0.f;
+              ds[e] = live ? x * (__uint_as_float(dp[i + e]) - dl) : 0.f;
+            }
+            if constexpr (KEY) pk[(c + i) / 2] = bf16x2(p[0], p[1]);
+            dk[(c + i) / 2] = bf16x2(ds[0], ds[1]);
+          }
+        }
+        tc_fence_before();
+        // the buffer's previous pair has been consumed by its products
+        if (g >= 2) {
+          ok = wait_bar(bar(Q_PFREE + wg), ((g >> 1) - 1) & 1, abort_flag, gerr, prm.wait_ns);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        }
+        // row r, 64 columns: 128 bytes, 16-byte chunks swizzled by the row
+        uint8_t* drow = smem + L::oDs + wg * L::kPd + r * 128;
+        uint8_t* prow = smem + L::oP + wg * L::kPd + r * 128;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int at = (i ^ (r & 7)) * 16;
+          *reinterpret_cast<uint4*>(drow + at) = make_uint4(dk[4 * i], dk[4 * i + 1], dk[4 * i + 2], dk[4 * i + 3]);
+          if constexpr (KEY)
+            *reinterpret_cast<uint4*>(prow + at) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        warp_arrive(bar(Q_PREADY + wg));
+      }
+      if (!ok) break;
+      // the finished gradients: lanes = channels, columns = the tile's rows. Key pass:
+      // warpgroup 0 writes dV, 1 writes dK; query pass: 32 rows of dQ each.
+      ok = wait_bar(bar(Q_ACCFULL), it & 1, abort_flag, gerr, prm.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const bool is_v = KEY && wg == 0;
+      const int ch = D == 128 ? r : (is_v ? r : r - 64);
+      const bool mine = ch >= 0 && ch < D;
+      __nv_bfloat16* out = (is_v ? prm.out0 : prm.out1) + (base + inf.tile) * 64 * D + (mine ? ch : 0);
+      const float f = is_v ? 1.f : prm.scale;
+      constexpr int kCols = KEY ? 64 : 32;
+      const int c0 = KEY ? 0 : 32 * wg;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + (is_v ? 256 : 320) + lane_off + c0 + c, v);
+        tmem_wait_ld(v);
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int row = c0 + c + i;
+            const float x = (row < inf.count && inf.pairs > 0) ? __uint_as_float(v[i]) * f : 0.f;
+            out[int64_t(row) * D] = __float2bfloat16_rn(x);
+          }
+        }
+      }
+      tc_fence_before();
+      warp_arrive(bar(Q_ACCFREE));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// -------------------------------------------------------------------- host ----
+
+inline int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
+
+struct BwdLayout {
+  int words;
+  int64_t rows_bytes, bits_bytes;
+  int64_t oLse, oDelta, oBits, oBitsT, total;
+};
+BwdLayout bwd_layout(const Geometry& g) {
+  BwdLayout l;
+  l.words = (g.nt_max + 31) / 32;
+  l.rows_bytes = round256(int64_t(g.B) * g.Hh * g.nt_max * VSA_TILE * 4);
+  l.bits_bytes = round256(int64_t(g.B) * g.Hh * l.words * 32 * l.words * 4);
+  l.oLse = 256;                                  // the two work counters first
+  l.oDelta = l.oLse + l.rows_bytes;
+  l.oBits = l.oDelta + l.rows_bytes;
+  l.oBitsT = l.oBits + l.bits_bytes;
+  l.total = l.oBitsT + l.bits_bytes;
+  return l;
+}
+
+template <int D, bool KEY>
+cudaError_t bwd_pass(const vsa_plan* p, const CUtensorMap& tx, const CUtensorMap& ty, const CUtensorMap& txs,
+                     const CUtensorMap& tys, const BwdParams& prm, cudaStream_t s) {
+  using L = BSmem<D, KEY>;
+  const int smem = 1024 + int(L::oEnd);
+  static_assert(1024 + L::oEnd <= 227 * 1024, "shared memory of one CTA");
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_kernel<D, KEY>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = int(prm.n_items < p->num_sms ? prm.n_items : p->num_sms);
+  attn_bwd_kernel<D, KEY><<<grid, kBThreads, smem, s>>>(tx, ty, txs, tys, prm);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t attn_bwd_workspace_bytes(const vsa_plan* p) { return bwd_layout(p->geo).total; }
+
+cudaError_t launch_attn_bwd(const vsa_plan* p, const void* qp, const void* kp, const void* vp, const void* op,
+                            const float* lse, const void* dop, const int32_t* idx, const int32_t* idx_ref,
+                            const int32_t* k, void* dqp, void* dkp, void* dvp, void* workspace, cudaStream_t s) {
+  const Geometry& g = p->geo;
+  const BwdLayout l = bwd_layout(g);
+  char* ws = static_cast<char*>(workspace);
+  const int64_t rows = int64_t(g.B) * g.Hh * g.nt_max * VSA_TILE;
+  CUtensorMap tq, tk, tv, tdo;
+  if (!make_map(&tq, qp, rows, g.d) || !make_map(&tk, kp, rows, g.d) || !make_map(&tv, vp, rows, g.d) ||
+      !make_map(&tdo, dop, rows, g.d))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaMemsetAsync(ws, 0, 256, s);
+  if (e != cudaSuccess) return e;
+
+  float* lse2 = reinterpret_cast<float*>(ws + l.oLse);
+  float* delta = reinterpret_cast<float*>(ws + l.oDelta);
+  const int rpb = 256 / (g.d / 8);
+  const int64_t want = (rows + rpb - 1) / rpb, cap = int64_t(p->num_sms) * 8;
+  const unsigned grid = unsigned(want < cap ? want : cap);
+  auto* o4 = static_cast<const uint4*>(op);
+  auto* do4 = static_cast<const uint4*>(dop);
+  if (g.d == 128)
+    bwd_rows_kernel<16><<<grid, 256, 0, s>>>(g, o4, do4, lse, p->d_tile_count, lse2, delta);
+  else
+    bwd_rows_kernel<8><<<grid, 256, 0, s>>>(g, o4, do4, lse, p->d_tile_count, lse2, delta);
+
+  BitParams bp;
+  bp.idx = idx;
+  bp.idx_ref = idx_ref;
+  bp.ref_tiles = p->d_ref_tiles;
+  bp.prefix_ref = p->d_prefix_ref;
+  bp.bits = reinterpret_cast<uint32_t*>(ws + l.oBits);
+  bp.bits_t = reinterpret_cast<uint32_t*>(ws + l.oBitsT);
+  bp.state = p->d_state;
+  bp.heads = g.Hh;
+  bp.nt_max = g.nt_max;
+  bp.ntv_max = g.ntv_max;
+  bp.k_max = g.k_max;
+  bp.n_pre = g.n_pre_tiles;
+  bp.n_ref = g.n_ref;
+  bp.k_ref_max = g.k_ref_max;
+  bp.words = l.words;
+  for (int h = 0; h < VSA_MAX_HEADS; ++h) {
+    bp.ntv[h] = h < g.Hh ? g.ntv[h] : 0;
+    bp.k[h] = h < g.Hh ? k[h] : 0;
+    bp.k_ref[h] = h < g.Hh ? g.k_ref[h] : 0;
+  }
+  const int bh = g.B * g.Hh;
+  bwd_bits_kernel<<<dim3(unsigned(l.words) * 8, unsigned(bh)), 128, size_t(4) * l.words * 4, s>>>(bp);
+  const int64_t blocks = int64_t(bh) * l.words * l.words;
+  bwd_transpose_kernel<<<unsigned((blocks + 7) / 8), 256, 0, s>>>(bp.bits, bp.bits_t, l.words, blocks);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  BwdParams prm;
+  prm.lse2 = lse2;
+  prm.delta = delta;
+  prm.counts = p->d_tile_count;
+  prm.state = p->d_state;
+  prm.wait_ns = p->wait_ns;
+  prm.n_items = int64_t(bh) * g.nt_max;
+  prm.heads = g.Hh;
+  prm.bh_total = bh;
+  prm.nt_max = g.nt_max;
+  prm.words = l.words;
+  prm.scale = p->desc.softmax_scale;
+  prm.scale_log2 = p->desc.softmax_scale * 1.4426950408889634f;
+
+  BwdParams key = prm, qry = prm;
+  key.bits = bp.bits_t;
+  key.counter = reinterpret_cast<uint32_t*>(ws);
+  key.out0 = static_cast<__nv_bfloat16*>(dvp);
+  key.out1 = static_cast<__nv_bfloat16*>(dkp);
+  qry.bits = bp.bits;
+  qry.counter = reinterpret_cast<uint32_t*>(ws) + 1;
+  qry.out0 = nullptr;
+  qry.out1 = static_cast<__nv_bfloat16*>(dqp);
+  if (g.d == 128) {
+    e = bwd_pass<128, true>(p, tq, tdo, tk, tv, key, s);
+    return e != cudaSuccess ? e : bwd_pass<128, false>(p, tk, tv, tq, tdo, qry, s);
+  }
+  e = bwd_pass<64, true>(p, tq, tdo, tk, tv, key, s);
+  return e != cudaSuccess ? e : bwd_pass<64, false>(p, tk, tv, tq, tdo, qry, s);
+}
+
+}  // namespace vsa

@@ -1,0 +1,566 @@
+// RMS norm of every head's query and key row and the rotary position embedding
+// in one pass, before the layer: token-major to token-major, or fused with the
+// tile pack and the score stage's pooling; and the gradient of both.
+//
+// Forward, for a row x of head_dim d with weights w:
+//   r = 1 / sqrt(mean(x^2) + eps),  n = x r w,
+//   every channel pair (a, b) of n turns by the token's angle of that pair:
+//   (a, b) -> (a cos - b sin, a sin + b cos).
+// Backward, for the gradient dy of the result: dn turns back,
+//   dn = (da cos + db sin, -da sin + db cos),  xr = x r,  g = dn w,
+//   dx = r (g - xr mean(g xr)),  dw = sum over the rows of dn xr.
+// Statistics, rotation and sums are fp32; each output is rounded to bf16 once.
+//
+// A row is held by d / 8 lanes, eight channels each, as four rotation pairs:
+// lane c owns pairs 4c .. 4c + 3, which are channels 8c .. 8c + 7 of the
+// interleaved layout (one 16-byte load) and channels 4c .. 4c + 3 and
+// d/2 + 4c .. + 3 of the halves layout (two 8-byte loads that fill their
+// sectors across the lanes). So both members of a pair are in one lane, the
+// table rows are one float4 of cosines and one of sines per lane in either
+// layout, and the only shuffles are those of the mean.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "tile_map.h"
+#include "vsa_internal.h"
+
+namespace vsa {
+namespace {
+
+__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// One lane's eight channels of a row as loaded: four words of two channels.
+// Interleaved: word j is pair j. Halves: words 0, 1 hold the first members of
+// pairs 0 .. 3, words 2, 3 the second.
+template <bool HALVES>
+__device__ __forceinline__ uint4 load_row(const __nv_bfloat16* row, int d, int c) {
+  if (HALVES) {
+    const uint2 a = __ldcs(reinterpret_cast<const uint2*>(row + 4 * c));
+    const uint2 b = __ldcs(reinterpret_cast<const uint2*>(row + d / 2 + 4 * c));
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+  return __ldcs(reinterpret_cast<const uint4*>(row) + c);
+}
+template <bool HALVES>
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int d, int c, uint4 v) {
+  if (HALVES) {
+    *reinterpret_cast<uint2*>(row + 4 * c) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(row + d / 2 + 4 * c) = make_uint2(v.z, v.w);
+  } else {
+    reinterpret_cast<uint4*>(row)[c] = v;
+  }
+}
+template <bool HALVES>
+__device__ __forceinline__ void to_pairs(uint4 v, float (&a)[4], float (&b)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (HALVES) {
+      a[j] = (j & 1) ? hi_f32(w[j >> 1]) : lo_f32(w[j >> 1]);
+      b[j] = (j & 1) ? hi_f32(w[2 + (j >> 1)]) : lo_f32(w[2 + (j >> 1)]);
+    } else {
+      a[j] = lo_f32(w[j]);
+      b[j] = hi_f32(w[j]);
+    }
+  }
+}
+template <bool HALVES>
+__device__ __forceinline__ uint4 from_pairs(const float (&a)[4], const float (&b)[4]) {
+  if (HALVES)
+    return make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3]));
+  return make_uint4(pack_bf16(a[0], b[0]), pack_bf16(a[1], b[1]), pack_bf16(a[2], b[2]), pack_bf16(a[3], b[3]));
+}
+// The channel of member m (0: a, 1: b) of the lane's pair j.
+template <bool HALVES>
+__device__ __forceinline__ int channel_of(int d, int c, int j, int m) {
+  return HALVES ? m * (d / 2) + 4 * c + j : 8 * c + 2 * j + m;
+}
+
+struct Weights {
+  float a[4], b[4];
+};
+// The lane's weights of one head (ones for a null table).
+template <bool HALVES>
+__device__ __forceinline__ Weights load_weights(const float* w, int d, int c) {
+  Weights r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r.a[j] = w ? __ldg(w + channel_of<HALVES>(d, c, j, 0)) : 1.f;
+    r.b[j] = w ? __ldg(w + channel_of<HALVES>(d, c, j, 1)) : 1.f;
+  }
+  return r;
+}
+
+struct Turn {
+  float c[4], s[4];
+};
+__device__ __forceinline__ Turn load_turn(const NormRopeArgs& n, int tok, int d, int c) {
+  Turn t;
+  if (n.cos) {
+    const float4 cs = __ldg(reinterpret_cast<const float4*>(n.cos + int64_t(tok) * (d / 2)) + c);
+    const float4 sn = __ldg(reinterpret_cast<const float4*>(n.sin + int64_t(tok) * (d / 2)) + c);
+    t.c[0] = cs.x; t.c[1] = cs.y; t.c[2] = cs.z; t.c[3] = cs.w;
+    t.s[0] = sn.x; t.s[1] = sn.y; t.s[2] = sn.z; t.s[3] = sn.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      t.c[j] = 1.f;
+      t.s[j] = 0.f;
+    }
+  }
+  return t;
+}
+
+// Sum over the CPR lanes of a row (aligned groups of the warp).
+template <int CPR>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = CPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// The normed and turned row as stored (bf16 words).
+template <int CPR, bool HALVES>
+__device__ __forceinline__ uint4 norm_rope_row(uint4 v, const Weights& w, const Turn& t, float eps) {
+  float a[4], b[4];
+  to_pairs<HALVES>(v, a, b);
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
+  const float r = rsqrtf(row_sum<CPR>(ss) * (1.f / (CPR * 8)) + eps);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float na = a[j] * r * w.a[j], nb = b[j] * r * w.b[j];
+    a[j] = fmaf(na, t.c[j], -nb * t.s[j]);
+    b[j] = fmaf(na, t.s[j], nb * t.c[j]);
+  }
+  return from_pairs<HALVES>(a, b);
+}
+
+// Token-major to token-major. One warp per token; its 32 / CPR lane groups
+// walk the heads, so the token's table row is loaded once for all heads.
+// Results may overwrite their inputs: a row is read before it is written, by
+// the lanes that write it.
+template <int CPR, bool HALVES>
+__global__ void __launch_bounds__(256) norm_rope_kernel(NormRopeArgs n, int B, int n_tok, int heads,
+                                                        const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                                        __nv_bfloat16* qo, __nv_bfloat16* ko) {
+  constexpr int D = CPR * 8, G = 32 / CPR;
+  const int lane = threadIdx.x & 31, c = lane % CPR, grp = lane / CPR;
+  Weights wq = load_weights<HALVES>(n.w_q, D, c), wk = load_weights<HALVES>(n.w_k, D, c);
+  const int64_t total = int64_t(B) * n_tok;
+  for (int64_t tk = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); tk < total; tk += int64_t(gridDim.x) * 8) {
+    const int b = int(tk / n_tok), tok = int(tk - int64_t(b) * n_tok);
+    const Turn t = load_turn(n, tok, D, c);
+    const __nv_bfloat16* qr = q + b * n.st[0].batch + tok * n.st[0].token;
+    const __nv_bfloat16* kr = k + b * n.st[1].batch + tok * n.st[1].token;
+    __nv_bfloat16* qw = qo + b * n.st[2].batch + tok * n.st[2].token;
+    __nv_bfloat16* kw = ko + b * n.st[3].batch + tok * n.st[3].token;
+    for (int h0 = 0; h0 < heads; h0 += G) {      // the same trip count in every lane: the sums are warp-wide
+      const int h = h0 + grp;
+      const bool on = h < heads;
+      uint4 vq = make_uint4(0, 0, 0, 0), vk = vq;
+      if (on) {
+        vq = load_row<HALVES>(qr + h * D, D, c);
+        vk = load_row<HALVES>(kr + h * D, D, c);
+        if (n.per_head) {
+          wq = load_weights<HALVES>(n.w_q ? n.w_q + h * D : nullptr, D, c);
+          wk = load_weights<HALVES>(n.w_k ? n.w_k + h * D : nullptr, D, c);
+        }
+      }
+      vq = norm_rope_row<CPR, HALVES>(vq, wq, t, n.eps);
+      vk = norm_rope_row<CPR, HALVES>(vk, wk, t, n.eps);
+      if (on) {
+        store_row<HALVES>(qw + h * D, D, c, vq);
+        store_row<HALVES>(kw + h * D, D, c, vk);
+      }
+    }
+  }
+}
+
+// Fused with the pack and the pooling: one CTA of 256 threads per (batch, tile,
+// head), the heads of a tile next to one another so that they find its table
+// rows in L2. Lanes and rows as in the pack kernel; the descriptors are pooled
+// from the rounded rows in the same order as there, so packed tiles and
+// descriptors equal, bit for bit, those of the token-major pass followed by
+// the pack. Tiles past a head's own are zero, their descriptors too.
+template <int CPR, bool HALVES, bool TRIP>
+__global__ void __launch_bounds__(256) norm_rope_pack_kernel(NormRopeArgs n, Geometry g, const __nv_bfloat16* q,
+                                                             const __nv_bfloat16* k, const __nv_bfloat16* v,
+                                                             __nv_bfloat16* qp, __nv_bfloat16* kp, __nv_bfloat16* vp,
+                                                             const int32_t* __restrict__ counts, float* pq, float* pk) {
+  constexpr int D = CPR * 8;
+  constexpr int KD = TRIP ? 3 * D : D;
+  constexpr int RG = 256 / CPR, RPT = 64 / RG;
+  constexpr int NS = TRIP ? 3 : 1;
+  __shared__ float part[NS][2][8][D];
+  const int h = int(blockIdx.x % g.Hh);
+  const int64_t bn = blockIdx.x / g.Hh;
+  const int tile_n = int(bn % g.nt_max), b = int(bn / g.nt_max);
+  const int bh = b * g.Hh + h;
+  const int64_t tile = int64_t(bh) * g.nt_max + tile_n;
+  const int c = threadIdx.x % CPR, rg = threadIdx.x / CPR;
+  const int vt = tile_n - g.n_pre_tiles;
+  const bool pool = vt >= 0 && vt < g.ntv[h];   // uniform over the CTA
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+
+  int tok[RPT];
+  uint4 xq[RPT], xk[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    tok[i] = src_token(g, h, tile_n, rg + RG * i);
+    xq[i] = xk[i] = zero;
+    uint4 xv = zero;
+    if (tok[i] >= 0) {
+      xq[i] = load_row<HALVES>(q + b * n.st[0].batch + tok[i] * n.st[0].token + h * D, D, c);
+      xk[i] = load_row<HALVES>(k + b * n.st[1].batch + tok[i] * n.st[1].token + h * D, D, c);
+      xv = __ldcs(reinterpret_cast<const uint4*>(v + b * n.st[2].batch + tok[i] * n.st[2].token + h * D) + c);
+    }
+    reinterpret_cast<uint4*>(vp + (tile * VSA_TILE + rg + RG * i) * D)[c] = xv;
+  }
+  const int64_t woff = n.per_head ? int64_t(h) * D : 0;
+  const Weights wq = load_weights<HALVES>(n.w_q ? n.w_q + woff : nullptr, D, c);
+  const Weights wk = load_weights<HALVES>(n.w_k ? n.w_k + woff : nullptr, D, c);
+  float st[NS][2][8];                            // [statistic][q, k][pair j: a, then b]
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      st[0][t][e] = 0.f;
+      if (TRIP) {
+        st[NS - 2][t][e] = -INFINITY;
+        st[NS - 1][t][e] = INFINITY;
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const Turn t = load_turn(n, tok[i] >= 0 ? tok[i] : 0, D, c);
+    uint4 y[2];
+    y[0] = norm_rope_row<CPR, HALVES>(xq[i], wq, t, n.eps);
+    y[1] = norm_rope_row<CPR, HALVES>(xk[i], wk, t, n.eps);
+    if (tok[i] < 0) y[0] = y[1] = zero;
+    const int64_t row = (tile * VSA_TILE + rg + RG * i) * D;
+    store_row<HALVES>(qp + row, D, c, y[0]);
+    store_row<HALVES>(kp + row, D, c, y[1]);
+    if (pool && tok[i] >= 0) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        float a[4], bb[4];
+        to_pairs<HALVES>(y[z], a, bb);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          st[0][z][j] += a[j];
+          st[0][z][4 + j] += bb[j];
+          if (TRIP) {
+            st[NS - 2][z][j] = fmaxf(st[NS - 2][z][j], a[j]);
+            st[NS - 2][z][4 + j] = fmaxf(st[NS - 2][z][4 + j], bb[j]);
+            st[NS - 1][z][j] = fminf(st[NS - 1][z][j], a[j]);
+            st[NS - 1][z][4 + j] = fminf(st[NS - 1][z][4 + j], bb[j]);
+          }
+        }
+      }
+    }
+  }
+  if (vt < 0) return;
+  if (!pool) {                                   // no such tile in this head
+    if (threadIdx.x < 2 * D)
+      for (int z = 0; z < NS; ++z)
+        (threadIdx.x / D ? pk : pq)[(int64_t(bh) * g.ntv_max + vt) * KD + z * D + threadIdx.x % D] = 0.f;
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = CPR; o < 32; o <<= 1)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        st[0][t][e] += __shfl_xor_sync(0xffffffffu, st[0][t][e], o);
+        if (TRIP) {
+          st[NS - 2][t][e] = fmaxf(st[NS - 2][t][e], __shfl_xor_sync(0xffffffffu, st[NS - 2][t][e], o));
+          st[NS - 1][t][e] = fminf(st[NS - 1][t][e], __shfl_xor_sync(0xffffffffu, st[NS - 1][t][e], o));
+        }
+      }
+  if (lane < CPR) {
+#pragma unroll
+    for (int z = 0; z < NS; ++z)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[z][t][warp][channel_of<HALVES>(D, c, e & 3, e >> 2)] = st[z][t][e];
+  }
+  __syncthreads();
+  if (threadIdx.x < 2 * D) {
+    const int t = threadIdx.x / D, ch = threadIdx.x % D;
+    float sum = 0.f, mx = -INFINITY, mn = INFINITY;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      sum += part[0][t][w][ch];
+      if (TRIP) {
+        mx = fmaxf(mx, part[NS - 2][t][w][ch]);
+        mn = fminf(mn, part[NS - 1][t][w][ch]);
+      }
+    }
+    const float cnt = float(counts[h * g.nt_max + tile_n]);
+    float* out = (t ? pk : pq) + (int64_t(bh) * g.ntv_max + vt) * KD;
+    out[ch] = sum / cnt;
+    if (TRIP) {
+      out[D + ch] = mx;
+      out[2 * D + ch] = mn;
+    }
+  }
+}
+
+// Gradient rows: dx from dy and x, and the row's share of dw.
+template <int CPR, bool HALVES>
+__device__ __forceinline__ uint4 norm_rope_grad_row(uint4 vy, uint4 vx, const Weights& w, const Turn& t, float eps,
+                                                    float (&dwa)[4], float (&dwb)[4]) {
+  float xa[4], xb[4], ya[4], yb[4];
+  to_pairs<HALVES>(vx, xa, xb);
+  to_pairs<HALVES>(vy, ya, yb);
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) ss = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], ss));
+  const float r = rsqrtf(row_sum<CPR>(ss) * (1.f / (CPR * 8)) + eps);
+  float dot = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float da = fmaf(ya[j], t.c[j], yb[j] * t.s[j]);
+    const float db = fmaf(yb[j], t.c[j], -ya[j] * t.s[j]);
+    xa[j] *= r;
+    xb[j] *= r;
+    dwa[j] = fmaf(da, xa[j], dwa[j]);
+    dwb[j] = fmaf(db, xb[j], dwb[j]);
+    ya[j] = da * w.a[j];
+    yb[j] = db * w.b[j];
+    dot = fmaf(ya[j], xa[j], fmaf(yb[j], xb[j], dot));
+  }
+  const float m = row_sum<CPR>(dot) * (1.f / (CPR * 8));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    ya[j] = r * fmaf(-xa[j], m, ya[j]);
+    yb[j] = r * fmaf(-xb[j], m, yb[j]);
+  }
+  return from_pairs<HALVES>(ya, yb);
+}
+
+// One warp per token and all heads (weights shared by the heads), or with
+// PER_HEAD one lane group per token of the block's own head (blockIdx.y), so
+// that the lanes' weight-gradient sums belong to one weight row in both.
+// PACKED: dy (and dv, which is only moved) come from packed tiles. The blocks'
+// partial sums of dw go to `part` [blockIdx.y][blockIdx.x][q, k][d], summed in
+// block order by the kernel below: no atomics, the same result every time.
+template <int CPR, bool HALVES, bool PACKED, bool PER_HEAD>
+__global__ void __launch_bounds__(256) norm_rope_bwd_kernel(NormRopeArgs n, Geometry g, const __nv_bfloat16* dyq,
+                                                            const __nv_bfloat16* dyk, const __nv_bfloat16* dyv,
+                                                            const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                                            __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv,
+                                                            float* part) {
+  constexpr int D = CPR * 8, G = 32 / CPR;
+  __shared__ float red[8][2][D];
+  __shared__ int32_t prow[PACKED && !PER_HEAD ? 8 : 1][VSA_MAX_HEADS];
+  const int lane = threadIdx.x & 31, c = lane % CPR, grp = lane / CPR, warp = threadIdx.x >> 5;
+  const int64_t woff = PER_HEAD && n.per_head ? int64_t(blockIdx.y) * D : 0;
+  const Weights wq = load_weights<HALVES>(n.w_q ? n.w_q + woff : nullptr, D, c);
+  const Weights wk = load_weights<HALVES>(n.w_k ? n.w_k + woff : nullptr, D, c);
+  float acc[2][2][4] = {};                       // [q, k][a, b][pair]
+  const int64_t total = int64_t(g.B) * g.n_tokens;
+  constexpr int TPW = PER_HEAD ? G : 1;          // tokens per warp and step
+  for (int64_t t0 = (int64_t(blockIdx.x) * 8 + warp) * TPW; t0 < total; t0 += int64_t(gridDim.x) * 8 * TPW) {
+    const int64_t tk = PER_HEAD ? t0 + grp : t0;
+    const bool real = tk < total;
+    const int b = int((real ? tk : 0) / g.n_tokens), tok = int((real ? tk : 0) - int64_t(b) * g.n_tokens);
+    const Turn t = load_turn(n, tok, D, c);
+    if constexpr (PACKED && !PER_HEAD) {
+      __syncwarp();                              // the previous token's rows are read
+      for (int h = lane; h < g.Hh; h += 32) prow[warp][h] = packed_row(g, h, tok);
+      __syncwarp();
+    }
+    float tok_acc[2][2][4] = {};                 // the token's own sum first: shorter fp32 chains
+    for (int h0 = 0; h0 < (PER_HEAD ? 1 : g.Hh); h0 += G) {
+      const int h = PER_HEAD ? int(blockIdx.y) : h0 + grp;
+      const bool on = real && h < g.Hh;
+      uint4 yq = make_uint4(0, 0, 0, 0), yk = yq, yv = yq, xq = yq, xk = yq;
+      if (on) {
+        if constexpr (PACKED) {
+          const int pr = PER_HEAD ? packed_row(g, h, tok) : prow[PER_HEAD ? 0 : warp][h];
+          const int64_t row = (int64_t(b * g.Hh + h) * g.nt_max * VSA_TILE + pr) * D;
+          yq = load_row<HALVES>(dyq + row, D, c);
+          yk = load_row<HALVES>(dyk + row, D, c);
+          yv = __ldcs(reinterpret_cast<const uint4*>(dyv + row) + c);
+        } else {
+          yq = load_row<HALVES>(dyq + b * n.st[5].batch + tok * n.st[5].token + h * D, D, c);
+          yk = load_row<HALVES>(dyk + b * n.st[6].batch + tok * n.st[6].token + h * D, D, c);
+        }
+        xq = load_row<HALVES>(q + b * n.st[0].batch + tok * n.st[0].token + h * D, D, c);
+        xk = load_row<HALVES>(k + b * n.st[1].batch + tok * n.st[1].token + h * D, D, c);
+      }
+      yq = norm_rope_grad_row<CPR, HALVES>(yq, xq, wq, t, n.eps, tok_acc[0][0], tok_acc[0][1]);
+      yk = norm_rope_grad_row<CPR, HALVES>(yk, xk, wk, t, n.eps, tok_acc[1][0], tok_acc[1][1]);
+      if (on) {
+        store_row<HALVES>(dq + b * n.st[2].batch + tok * n.st[2].token + h * D, D, c, yq);
+        store_row<HALVES>(dk + b * n.st[3].batch + tok * n.st[3].token + h * D, D, c, yk);
+        if constexpr (PACKED)
+          reinterpret_cast<uint4*>(dv + b * n.st[4].batch + tok * n.st[4].token + h * D)[c] = yv;
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[z][m][j] += tok_acc[z][m][j];
+  }
+#pragma unroll
+  for (int z = 0; z < 2; ++z)
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int o = CPR; o < 32; o <<= 1) acc[z][m][j] += __shfl_xor_sync(0xffffffffu, acc[z][m][j], o);
+        if (lane < CPR) red[warp][z][channel_of<HALVES>(D, c, j, m)] = acc[z][m][j];
+      }
+  __syncthreads();
+  if (threadIdx.x < 2 * D) {
+    const int z = threadIdx.x / D, ch = threadIdx.x % D;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += red[w][z][ch];
+    part[((int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * 2 + z) * D + ch] = s;
+  }
+}
+
+// dw[row][z][ch] = sum over the nb partials of that row: eight interleaved
+// chains per channel in fp64, joined in a fixed order. Grid (rows, 2).
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int nb, int D, float* dw_q,
+                                                       float* dw_k) {
+  __shared__ double red[8][128];
+  const int ch = threadIdx.x & 127, sl = threadIdx.x >> 7, z = blockIdx.y;
+  double s = 0.0;
+  if (ch < D)
+    for (int i = sl; i < nb; i += 8) s += double(part[((int64_t(blockIdx.x) * nb + i) * 2 + z) * D + ch]);
+  red[sl][ch] = s;
+  __syncthreads();
+  if (sl == 0 && ch < D) {
+    for (int i = 1; i < 8; ++i) s += red[i][ch];
+    float* out = z ? dw_k : dw_q;
+    if (out) out[int64_t(blockIdx.x) * D + ch] = float(s);
+  }
+}
+
+// Blocks along x of the gradient kernel: one step of eight warps at least, four
+// blocks per SM at most (weights per head: shared among the heads).
+int bwd_blocks(const vsa_plan* p, bool per_head) {
+  const Geometry& g = p->geo;
+  const int64_t tokens = int64_t(g.B) * g.n_tokens;
+  const int tpb = per_head ? 8 * (32 / (g.d / 8)) : 8;
+  const int64_t want = (tokens + tpb - 1) / tpb;
+  const int64_t cap = per_head ? (int64_t(p->num_sms) * 4 + g.Hh - 1) / g.Hh : int64_t(p->num_sms) * 4;
+  return int(want < cap ? want : cap);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const vsa_plan* p, const NormRopeArgs& n, const void* q, const void* k, void* qo, void* ko,
+                             cudaStream_t s) {
+  const Geometry& g = p->geo;
+  const int64_t want = (int64_t(g.B) * g.n_tokens + 7) / 8, cap = int64_t(p->num_sms) * 8;
+  const unsigned grid = unsigned(want < cap ? want : cap);
+  auto* q2 = static_cast<const __nv_bfloat16*>(q);
+  auto* k2 = static_cast<const __nv_bfloat16*>(k);
+  auto* qo2 = static_cast<__nv_bfloat16*>(qo);
+  auto* ko2 = static_cast<__nv_bfloat16*>(ko);
+#define VSA_RUN(CPR, HV) norm_rope_kernel<CPR, HV><<<grid, 256, 0, s>>>(n, g.B, g.n_tokens, g.Hh, q2, k2, qo2, ko2)
+  if (g.d == 128) {
+    if (n.halves) VSA_RUN(16, true);
+    else VSA_RUN(16, false);
+  } else {
+    if (n.halves) VSA_RUN(8, true);
+    else VSA_RUN(8, false);
+  }
+#undef VSA_RUN
+  return cudaGetLastError();
+}
+
+cudaError_t launch_norm_rope_pack(const vsa_plan* p, const NormRopeArgs& n, const void* q, const void* k, const void* v,
+                                  void* qp, void* kp, void* vp, float* pooled_q, float* pooled_k, cudaStream_t s) {
+  const Geometry& g = p->geo;
+  const unsigned grid = unsigned(int64_t(g.B) * g.Hh * g.nt_max);
+  const bool trip = p->desc.score_mode == VSA_SCORE_TRIPPOOL;
+#define VSA_RUN(CPR, HV, TR)                                                                                       \
+  norm_rope_pack_kernel<CPR, HV, TR><<<grid, 256, 0, s>>>(                                                          \
+      n, g, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),                            \
+      static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(qp), static_cast<__nv_bfloat16*>(kp),      \
+      static_cast<__nv_bfloat16*>(vp), p->d_tile_count, pooled_q, pooled_k)
+  if (g.d == 128) {
+    if (n.halves) {
+      if (trip) VSA_RUN(16, true, true);
+      else VSA_RUN(16, true, false);
+    } else {
+      if (trip) VSA_RUN(16, false, true);
+      else VSA_RUN(16, false, false);
+    }
+  } else {
+    if (n.halves) {
+      if (trip) VSA_RUN(8, true, true);
+      else VSA_RUN(8, true, false);
+    } else {
+      if (trip) VSA_RUN(8, false, true);
+      else VSA_RUN(8, false, false);
+    }
+  }
+#undef VSA_RUN
+  return cudaGetLastError();
+}
+
+int64_t norm_bwd_workspace_bytes(const vsa_plan* p) {
+  const int64_t shared = bwd_blocks(p, false), per_head = int64_t(bwd_blocks(p, true)) * p->geo.Hh;
+  return (shared > per_head ? shared : per_head) * 2 * p->geo.d * int64_t(sizeof(float));
+}
+
+cudaError_t launch_norm_rope_bwd(const vsa_plan* p, const NormRopeArgs& n, bool packed, const void* dyq, const void* dyk,
+                                 const void* dyv, const void* q, const void* k, void* dq, void* dk, void* dv, float* dw_q,
+                                 float* dw_k, void* workspace, cudaStream_t s) {
+  const Geometry& g = p->geo;
+  const int nb = bwd_blocks(p, n.per_head);
+  const dim3 grid(nb, n.per_head ? g.Hh : 1);
+  float* part = static_cast<float*>(workspace);
+#define VSA_RUN(CPR, HV, PK, PH)                                                                                   \
+  norm_rope_bwd_kernel<CPR, HV, PK, PH><<<grid, 256, 0, s>>>(                                                       \
+      n, g, static_cast<const __nv_bfloat16*>(dyq), static_cast<const __nv_bfloat16*>(dyk),                        \
+      static_cast<const __nv_bfloat16*>(dyv), static_cast<const __nv_bfloat16*>(q),                                \
+      static_cast<const __nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk),      \
+      static_cast<__nv_bfloat16*>(dv), part)
+#define VSA_RUN2(CPR, HV)                  \
+  do {                                     \
+    if (packed) {                          \
+      if (n.per_head) VSA_RUN(CPR, HV, true, true);  \
+      else VSA_RUN(CPR, HV, true, false);  \
+    } else {                               \
+      if (n.per_head) VSA_RUN(CPR, HV, false, true); \
+      else VSA_RUN(CPR, HV, false, false); \
+    }                                      \
+  } while (0)
+  if (g.d == 128) {
+    if (n.halves) VSA_RUN2(16, true);
+    else VSA_RUN2(16, false);
+  } else {
+    if (n.halves) VSA_RUN2(8, true);
+    else VSA_RUN2(8, false);
+  }
+#undef VSA_RUN2
+#undef VSA_RUN
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || (!dw_q && !dw_k)) return e;
+  norm_dw_kernel<<<dim3(grid.y, 2), 1024, 0, s>>>(part, nb, g.d, dw_q, dw_k);
+  return cudaGetLastError();
+}
+
+}  // namespace vsa

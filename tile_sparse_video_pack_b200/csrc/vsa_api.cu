@@ -54,6 +54,43 @@ bool on_plan_device(const vsa_plan* p) {
   return cur == p->device;
 }
 
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+// The arguments of one norm + rotation call: parameters and the views' strides
+// (null: contiguous), each view `n_views` long and mapped to NormRopeArgs::st by `at`.
+bool resolve_norm(const vsa_plan* p, const vsa_norm_rope* n, const vsa_strides* strides, int n_views, const int* at,
+                  vsa::NormRopeArgs* out) {
+  if (!n) return false;
+  if (!n->cos_table != !n->sin_table) return false;
+  if (!aligned16(n->w_q) || !aligned16(n->w_k) || !aligned16(n->cos_table) || !aligned16(n->sin_table)) return false;
+  if ((n->per_head != 0 && n->per_head != 1) ||
+      (n->layout != VSA_ROPE_INTERLEAVED && n->layout != VSA_ROPE_HALVES))
+    return false;
+  if (!(n->eps >= 0.0f) || isinf(n->eps)) return false;
+  out->w_q = n->w_q;
+  out->w_k = n->w_k;
+  out->cos = n->cos_table;
+  out->sin = n->sin_table;
+  out->eps = n->eps;
+  out->per_head = n->per_head;
+  out->halves = n->layout == VSA_ROPE_HALVES;
+  const int64_t row = int64_t(p->geo.Hh) * p->geo.d;
+  for (int i = 0; i < n_views; ++i) {
+    vsa_strides v = {row * p->geo.n_tokens, row};
+    if (strides) v = strides[i];
+    if (v.token < row || v.token % 8 || v.batch < 0 || v.batch % 8) return false;
+    out->st[at[i]] = v;
+  }
+  return true;
+}
+
+// rows, widths and leading dimensions of a linear call
+bool linear_sizes(int64_t rows, int32_t n_in, int32_t n_out) {
+  return rows >= 0 && rows < (int64_t(1) << 31) - 256 && n_in >= 8 && n_out >= 8 && n_in % 8 == 0 && n_out % 8 == 0 &&
+         n_in <= (1 << 24) && n_out <= (1 << 24);
+}
+bool linear_view(const void* p, int64_t ld, int32_t cols) { return p && aligned16(p) && ld >= cols && ld % 8 == 0; }
+
 // Host-side validation of a descriptor; no CUDA call is made here.
 vsa_status validate(const vsa_desc& d) {
   if (d.batch < 1 || d.heads < 1 || d.heads > VSA_MAX_HEADS) return VSA_ERR_INVALID_ARG;
@@ -604,6 +641,187 @@ vsa_status vsa_index_overlap(vsa_plan* p, const int32_t* idx_a, const int32_t* i
   if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
   if (vsa::launch_overlap(p, idx_a, idx_b, counts, static_cast<cudaStream_t>(stream), k) != cudaSuccess)
     return fail(p, VSA_ERR_CUDA);
+  return VSA_OK;
+}
+
+vsa_status vsa_qk_norm_rope(vsa_plan* p, const vsa_norm_rope* norm, const void* q, const void* k, void* q_out,
+                            void* k_out, const vsa_strides* strides, void* stream) {
+  Range r("vsa_qk_norm_rope");
+  if (!p || !q || !k || !q_out || !k_out) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return fail(p, VSA_ERR_INVALID_ARG);
+  vsa::NormRopeArgs n = {};
+  const int at[4] = {0, 1, 2, 3};
+  if (!resolve_norm(p, norm, strides, 4, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (vsa::launch_norm_rope(p, n, q, k, q_out, k_out, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return fail(p, VSA_ERR_CUDA);
+  return VSA_OK;
+}
+
+vsa_status vsa_tile_norm_rope_pack_pool(vsa_plan* p, const vsa_norm_rope* norm, const void* q, const void* k,
+                                        const void* v, const vsa_strides* strides, void* qp, void* kp, void* vp,
+                                        void* ws, void* stream) {
+  Range r("vsa_tile_norm_rope_pack_pool");
+  if (!p || !q || !k || !v || !qp || !kp || !vp || !ws) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(qp) || !aligned16(kp) || !aligned16(vp) ||
+      !aligned256(ws))
+    return fail(p, VSA_ERR_INVALID_ARG);
+  vsa::NormRopeArgs n = {};
+  const int at[3] = {0, 1, 2};
+  if (!resolve_norm(p, norm, strides, 3, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
+  p->stats.calls_pack++;
+  float *pq, *pk;
+  vsa::score_pooled_ptrs(p, ws, &pq, &pk);
+  if (vsa::launch_norm_rope_pack(p, n, q, k, v, qp, kp, vp, pq, pk, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return fail(p, VSA_ERR_CUDA);
+  return VSA_OK;
+}
+
+vsa_status vsa_pooled_descriptors(const vsa_plan* p, void* ws, float** pooled_q, float** pooled_k) {
+  if (!p || !ws || !pooled_q || !pooled_k || !aligned256(ws)) return VSA_ERR_INVALID_ARG;
+  vsa::score_pooled_ptrs(p, ws, pooled_q, pooled_k);
+  return VSA_OK;
+}
+
+vsa_status vsa_norm_bwd_workspace(const vsa_plan* p, int64_t* bytes) {
+  if (!p || !bytes) return VSA_ERR_INVALID_ARG;
+  *bytes = vsa::norm_bwd_workspace_bytes(p);
+  return VSA_OK;
+}
+
+vsa_status vsa_qk_norm_rope_bwd(vsa_plan* p, const vsa_norm_rope* norm, const void* dq_out, const void* dk_out,
+                                const void* q, const void* k, void* dq, void* dk, const vsa_strides* strides,
+                                float* dw_q, float* dw_k, void* ws, void* stream) {
+  Range r("vsa_qk_norm_rope_bwd");
+  if (!p || !dq_out || !dk_out || !q || !k || !dq || !dk || !ws) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(q) || !aligned16(k) || !aligned16(dq) ||
+      !aligned16(dk) || !aligned16(dw_q) || !aligned16(dw_k) || !aligned256(ws))
+    return fail(p, VSA_ERR_INVALID_ARG);
+  vsa::NormRopeArgs n = {};
+  const int at[6] = {5, 6, 0, 1, 2, 3};
+  if (!resolve_norm(p, norm, strides, 6, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (vsa::launch_norm_rope_bwd(p, n, false, dq_out, dk_out, nullptr, q, k, dq, dk, nullptr, dw_q, dw_k, ws,
+                                static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return fail(p, VSA_ERR_CUDA);
+  return VSA_OK;
+}
+
+vsa_status vsa_tile_norm_rope_bwd(vsa_plan* p, const vsa_norm_rope* norm, const void* dqp, const void* dkp,
+                                  const void* dvp, const void* q, const void* k, void* dq, void* dk, void* dv,
+                                  const vsa_strides* strides, float* dw_q, float* dw_k, void* ws, void* stream) {
+  Range r("vsa_tile_norm_rope_bwd");
+  if (!p || !dqp || !dkp || !dvp || !q || !k || !dq || !dk || !dv || !ws) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!aligned16(dqp) || !aligned16(dkp) || !aligned16(dvp) || !aligned16(q) || !aligned16(k) || !aligned16(dq) ||
+      !aligned16(dk) || !aligned16(dv) || !aligned16(dw_q) || !aligned16(dw_k) || !aligned256(ws))
+    return fail(p, VSA_ERR_INVALID_ARG);
+  vsa::NormRopeArgs n = {};
+  const int at[5] = {0, 1, 2, 3, 4};
+  if (!resolve_norm(p, norm, strides, 5, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (vsa::launch_norm_rope_bwd(p, n, true, dqp, dkp, dvp, q, k, dq, dk, dv, dw_q, dw_k, ws,
+                                static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return fail(p, VSA_ERR_CUDA);
+  return VSA_OK;
+}
+
+vsa_status vsa_attn_bwd_workspace(const vsa_plan* p, int64_t* bytes) {
+  if (!p || !bytes) return VSA_ERR_INVALID_ARG;
+  *bytes = vsa::attn_bwd_workspace_bytes(p);
+  return VSA_OK;
+}
+
+static vsa_status attn_bwd(vsa_plan* p, const void* qp, const void* kp, const void* vp, const void* op,
+                           const float* lse, const void* dop, const int32_t* idx, const int32_t* idx_ref,
+                           const int32_t* k_per_head, void* dqp, void* dkp, void* dvp, void* ws, void* stream) {
+  if (!p || !qp || !kp || !vp || !op || !lse || !dop || !idx || !dqp || !dkp || !dvp || !ws)
+    return fail(p, VSA_ERR_INVALID_ARG);
+  const void* all[] = {qp, kp, vp, op, lse, dop, idx, idx_ref, dqp, dkp, dvp};
+  for (const void* x : all)
+    if (!aligned16(x)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!aligned256(ws)) return fail(p, VSA_ERR_INVALID_ARG);
+  int32_t k[VSA_MAX_HEADS];
+  if (!resolve_k(p, k_per_head, k)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (int64_t(p->geo.B) * p->geo.Hh > 65535) return fail(p, VSA_ERR_UNSUPPORTED);   // grid of the list kernel
+  if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (vsa::launch_attn_bwd(p, qp, kp, vp, op, lse, dop, idx, idx_ref, k, dqp, dkp, dvp, ws,
+                           static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return fail(p, VSA_ERR_CUDA);
+  return VSA_OK;
+}
+
+vsa_status vsa_sparse_attn_bwd(vsa_plan* p, const void* qp, const void* kp, const void* vp, const void* op,
+                               const float* lse, const void* dop, const int32_t* idx, const int32_t* k_per_head,
+                               void* dqp, void* dkp, void* dvp, void* ws, void* stream) {
+  Range r("vsa_sparse_attn_bwd");
+  return attn_bwd(p, qp, kp, vp, op, lse, dop, idx, nullptr, k_per_head, dqp, dkp, dvp, ws, stream);
+}
+
+vsa_status vsa_sparse_attn_ref_bwd(vsa_plan* p, const void* qp, const void* kp, const void* vp, const void* op,
+                                   const float* lse, const void* dop, const int32_t* idx, const int32_t* idx_ref,
+                                   const int32_t* k_per_head, void* dqp, void* dkp, void* dvp, void* ws,
+                                   void* stream) {
+  Range r("vsa_sparse_attn_ref_bwd");
+  if (!p || !idx_ref || p->geo.n_ref == 0) return fail(p, VSA_ERR_INVALID_ARG);
+  return attn_bwd(p, qp, kp, vp, op, lse, dop, idx, idx_ref, k_per_head, dqp, dkp, dvp, ws, stream);
+}
+
+vsa_status vsa_linear_workspace(const vsa_plan* p, int64_t rows, int32_t n_in, int32_t n_out, int32_t backward,
+                                int64_t rows_per_gate, int64_t* bytes) {
+  if (!p || !bytes || !linear_sizes(rows, n_in, n_out) || (backward != 0 && backward != 1) || rows_per_gate < 0)
+    return VSA_ERR_INVALID_ARG;
+  if (rows_per_gate > 0 && rows % rows_per_gate) return VSA_ERR_INVALID_ARG;
+  *bytes = vsa::linear_workspace_bytes(p, rows, n_in, n_out, backward == 1, rows_per_gate);
+  return VSA_OK;
+}
+
+vsa_status vsa_linear(vsa_plan* p, const vsa_linear_args* args, void* ws, void* stream) {
+  Range r("vsa_linear");
+  if (!p || !args) return fail(p, VSA_ERR_INVALID_ARG);
+  const vsa_linear_args& a = *args;
+  if (!linear_sizes(a.rows, a.n_in, a.n_out) || a.act < VSA_ACT_NONE || a.act > VSA_ACT_SILU)
+    return fail(p, VSA_ERR_INVALID_ARG);
+  if (!a.w || !aligned16(a.w) || !aligned16(a.bias) || !aligned16(a.gate)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (a.gate && (a.rows_per_gate < 1 || a.rows % a.rows_per_gate)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (a.rows == 0) return VSA_OK;
+  if (!linear_view(a.x, a.ld_x, a.n_in) || !linear_view(a.y, a.ld_y, a.n_out) ||
+      (a.residual && !linear_view(a.residual, a.ld_residual, a.n_out)) ||
+      (a.pre && !linear_view(a.pre, a.ld_pre, a.n_out)))
+    return fail(p, VSA_ERR_INVALID_ARG);
+  const int64_t need = vsa::linear_workspace_bytes(p, a.rows, a.n_in, a.n_out, false, 0);
+  if (need > 0 && (!ws || !aligned256(ws))) return fail(p, VSA_ERR_INVALID_ARG);
+  if (vsa::launch_linear(p, a, ws, static_cast<cudaStream_t>(stream)) != cudaSuccess) return fail(p, VSA_ERR_CUDA);
+  return VSA_OK;
+}
+
+vsa_status vsa_linear_bwd(vsa_plan* p, const vsa_linear_grad_args* args, void* ws, void* stream) {
+  Range r("vsa_linear_bwd");
+  if (!p || !args) return fail(p, VSA_ERR_INVALID_ARG);
+  const vsa_linear_grad_args& a = *args;
+  if (!linear_sizes(a.rows, a.n_in, a.n_out) || a.act < VSA_ACT_NONE || a.act > VSA_ACT_SILU)
+    return fail(p, VSA_ERR_INVALID_ARG);
+  if (!aligned16(a.w) || !aligned16(a.gate) || !aligned16(a.dw) || !aligned16(a.dbias) || !aligned16(a.dgate))
+    return fail(p, VSA_ERR_INVALID_ARG);
+  if (a.gate && (a.rows_per_gate < 1 || a.rows % a.rows_per_gate)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (a.dgate && !a.gate) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a.rows == 0) {   // sums over no rows
+    cudaError_t e = cudaSuccess;
+    if (a.dw) e = cudaMemsetAsync(a.dw, 0, size_t(a.n_in) * a.n_out * 2, s);
+    if (e == cudaSuccess && a.dbias) e = cudaMemsetAsync(a.dbias, 0, size_t(a.n_out) * 4, s);
+    return e == cudaSuccess ? VSA_OK : fail(p, VSA_ERR_CUDA);
+  }
+  if (!linear_view(a.dy, a.ld_dy, a.n_out) || (a.dw && !linear_view(a.x, a.ld_x, a.n_in)) ||
+      (a.dx && (!a.w || !linear_view(a.dx, a.ld_dx, a.n_in))))
+    return fail(p, VSA_ERR_INVALID_ARG);
+  if ((a.act != VSA_ACT_NONE || a.dgate) && !linear_view(a.pre, a.ld_pre, a.n_out))
+    return fail(p, VSA_ERR_INVALID_ARG);
+  const int64_t need = vsa::linear_workspace_bytes(p, a.rows, a.n_in, a.n_out, true, a.gate ? a.rows_per_gate : 0);
+  if (need > 0 && (!ws || !aligned256(ws))) return fail(p, VSA_ERR_INVALID_ARG);
+  if (vsa::launch_linear_bwd(p, a, ws, s) != cudaSuccess) return fail(p, VSA_ERR_CUDA);
   return VSA_OK;
 }
 

@@ -44,6 +44,17 @@ struct WorkItem {
   int32_t kind;    // 0: prefix query tiles (dense rows), 1: video query tiles
 };
 
+// The norm and rotation of one call, by value. st: element strides (batch, token)
+// of q, k, then of the outputs -- norm_rope: q_out, k_out at 2, 3; pack: v at 2;
+// gradient: dq, dk, dv at 2 .. 4 and, token-major, the incoming dq, dk at 5, 6.
+struct NormRopeArgs {
+  const float *w_q, *w_k;   // [d] or (per_head) [heads][d]; null: ones
+  const float *cos, *sin;   // [n_tokens][d / 2]; null: no rotation
+  float eps;
+  int32_t per_head, halves;
+  vsa_strides st[7];
+};
+
 }  // namespace vsa
 
 struct vsa_plan {
@@ -111,5 +122,26 @@ cudaError_t launch_teacher(vsa_plan* p, const void* qp, const void* kp, const fl
                            cudaStream_t s);
 cudaError_t launch_overlap(vsa_plan* p, const int32_t* a, const int32_t* b, int32_t* counts, cudaStream_t s,
                            const int32_t* k);
+
+// RMS norm + rotation (norm_rope.cu).
+cudaError_t launch_norm_rope(const vsa_plan* p, const NormRopeArgs& n, const void* q, const void* k, void* qo, void* ko,
+                             cudaStream_t s);
+cudaError_t launch_norm_rope_pack(const vsa_plan* p, const NormRopeArgs& n, const void* q, const void* k, const void* v,
+                                  void* qp, void* kp, void* vp, float* pooled_q, float* pooled_k, cudaStream_t s);
+int64_t norm_bwd_workspace_bytes(const vsa_plan* p);
+cudaError_t launch_norm_rope_bwd(const vsa_plan* p, const NormRopeArgs& n, bool packed, const void* dyq, const void* dyk,
+                                 const void* dyv, const void* q, const void* k, void* dq, void* dk, void* dv, float* dw_q,
+                                 float* dw_k, void* workspace, cudaStream_t s);
+
+// Linear layer with epilogue and its gradient (linear.cu); arguments validated by the entry points.
+int64_t linear_workspace_bytes(const vsa_plan* p, int64_t rows, int64_t n_in, int64_t n_out, bool backward,
+                               int64_t rows_per_gate);
+cudaError_t launch_linear(const vsa_plan* p, const vsa_linear_args& a, void* workspace, cudaStream_t s);
+cudaError_t launch_linear_bwd(const vsa_plan* p, const vsa_linear_grad_args& a, void* workspace, cudaStream_t s);
+// Gradient of the sparse attention (attn_bwd.cu).
+int64_t attn_bwd_workspace_bytes(const vsa_plan* p);
+cudaError_t launch_attn_bwd(const vsa_plan* p, const void* qp, const void* kp, const void* vp, const void* op,
+                            const float* lse, const void* dop, const int32_t* idx, const int32_t* idx_ref,
+                            const int32_t* k, void* dqp, void* dkp, void* dvp, void* workspace, cudaStream_t s);
 
 }  // namespace vsa

@@ -29,7 +29,12 @@ EXPORTS = ("vsa_plan_create", "vsa_plan_destroy", "vsa_plan_query", "vsa_plan_ge
            "vsa_tile_pack_pool", "vsa_tile_score_pooled", "vsa_teacher_tiles", "vsa_index_overlap",
            "vsa_ref_score", "vsa_topk_select_ref", "vsa_sparse_attn_ref", "vsa_tile_pack_pool_fp8",
            "vsa_sparse_attn_fp8", "vsa_plan_set_wait_limit", "vsa_plan_set_test_hold", "vsa_tile_pool",
-           "vsa_sparse_attn_direct")
+           "vsa_sparse_attn_direct", "vsa_qk_norm_rope", "vsa_tile_norm_rope_pack_pool", "vsa_pooled_descriptors",
+           "vsa_norm_bwd_workspace", "vsa_qk_norm_rope_bwd", "vsa_tile_norm_rope_bwd",
+           "vsa_attn_bwd_workspace", "vsa_sparse_attn_bwd", "vsa_sparse_attn_ref_bwd",
+           "vsa_linear_workspace", "vsa_linear", "vsa_linear_bwd")
+ROPE_LAYOUTS = {"interleaved": 0, "halves": 1}
+ACTIVATIONS = {"none": 0, "gelu_tanh": 1, "silu": 2}
 
 
 class VsaDesc(ctypes.Structure):
@@ -61,6 +66,38 @@ class VsaPlanStats(ctypes.Structure):
         ("calls_pack", ctypes.c_int64), ("calls_score", ctypes.c_int64), ("calls_select", ctypes.c_int64),
         ("calls_attn", ctypes.c_int64), ("calls_unpack", ctypes.c_int64), ("errors", ctypes.c_int64),
         ("computed_pairs", ctypes.c_int64), ("dense_pairs", ctypes.c_int64),
+    ]
+
+
+class VsaStrides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class VsaNormRope(ctypes.Structure):
+    _fields_ = [
+        ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p),
+        ("cos_table", ctypes.c_void_p), ("sin_table", ctypes.c_void_p),
+        ("per_head", ctypes.c_int32), ("layout", ctypes.c_int32), ("eps", ctypes.c_float),
+    ]
+
+
+class VsaLinearArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("act", ctypes.c_int32), ("gate", ctypes.c_void_p), ("rows_per_gate", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("y", ctypes.c_void_p),
+        ("ld_y", ctypes.c_int64), ("pre", ctypes.c_void_p), ("ld_pre", ctypes.c_int64),
+    ]
+
+
+class VsaLinearGradArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32),
+        ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+        ("w", ctypes.c_void_p), ("act", ctypes.c_int32), ("pre", ctypes.c_void_p), ("ld_pre", ctypes.c_int64),
+        ("gate", ctypes.c_void_p), ("rows_per_gate", ctypes.c_int64), ("dx", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64), ("dw", ctypes.c_void_p), ("dbias", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
     ]
 
 
@@ -110,6 +147,18 @@ def library() -> ctypes.CDLL:
         "vsa_plan_set_test_hold": (I32, [P, I32]),
         "vsa_tile_pool": (I32, [P] * 5),
         "vsa_sparse_attn_direct": (I32, [P] * 9),
+        "vsa_qk_norm_rope": (I32, [P] * 8),
+        "vsa_tile_norm_rope_pack_pool": (I32, [P] * 11),
+        "vsa_pooled_descriptors": (I32, [P] * 4),
+        "vsa_norm_bwd_workspace": (I32, [P, ctypes.POINTER(I64)]),
+        "vsa_qk_norm_rope_bwd": (I32, [P] * 13),
+        "vsa_tile_norm_rope_bwd": (I32, [P] * 15),
+        "vsa_attn_bwd_workspace": (I32, [P, ctypes.POINTER(I64)]),
+        "vsa_sparse_attn_bwd": (I32, [P] * 14),
+        "vsa_sparse_attn_ref_bwd": (I32, [P] * 15),
+        "vsa_linear_workspace": (I32, [P, I64, I32, I32, I32, I64, ctypes.POINTER(I64)]),
+        "vsa_linear": (I32, [P, ctypes.POINTER(VsaLinearArgs), P, P]),
+        "vsa_linear_bwd": (I32, [P, ctypes.POINTER(VsaLinearGradArgs), P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -169,6 +218,77 @@ def _ptr(t, dtype, name, min_numel=0):
     if t.numel() < min_numel:
         raise ValueError(f"{name} holds {t.numel()} elements, needs {min_numel}")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _device_ptr(t, dtype, name):
+    """Device pointer of a CUDA tensor of any strides on the current device."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but cuda:{torch.cuda.current_device()} is the current device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _matrix(t, cols, name, rows=None):
+    """(pointer, row stride, rows) of a bf16 [..., cols] tensor whose leading dimensions form one row axis."""
+    import torch
+    p = _device_ptr(t, torch.bfloat16, name)
+    if t.dim() < 1 or t.shape[-1] != cols:
+        raise ValueError(f"{name} must be [..., {cols}], got {tuple(t.shape)}")
+    if t.numel() == 0:
+        m = t.reshape(-1, cols)
+    else:
+        try:
+            m = t.view(-1, cols)
+        except RuntimeError:
+            raise ValueError(f"{name}'s leading dimensions {tuple(t.shape)} are not one row axis "
+                             f"(strides {t.stride()})") from None
+    if m.shape[0] > 0 and cols > 1 and m.stride(1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if rows is not None and m.shape[0] != rows:
+        raise ValueError(f"{name} has {m.shape[0]} rows, needs {rows}")
+    return p, (m.stride(0) if m.shape[0] > 1 else cols), m.shape[0]
+
+
+class NormRope:
+    """RMS norm weights and rotation table of :meth:`Plan.qk_norm_rope` and its kin.
+
+    ``w_q``, ``w_k``: fp32 ``[head_dim]`` or, one row per head, ``[heads, head_dim]`` (None: ones; both the
+    same shape). ``cos``, ``sin``: fp32 ``[n_tokens, head_dim / 2]``, one angle per token and channel pair
+    (both None: no rotation). ``layout``: "interleaved" turns channels (2i, 2i + 1) together, "halves"
+    channels (i, i + head_dim / 2). :func:`axial_rope_table` makes a table for a (T, H, W) grid.
+    """
+
+    def __init__(self, w_q=None, w_k=None, cos=None, sin=None, layout="interleaved", eps=1e-6):
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+        if (cos is None) != (sin is None):
+            raise ValueError("cos and sin come together")
+        if w_q is not None and w_k is not None and w_q.shape != w_k.shape:
+            raise ValueError(f"w_q {tuple(w_q.shape)} and w_k {tuple(w_k.shape)} differ in shape")
+        self.w_q, self.w_k, self.cos, self.sin = w_q, w_k, cos, sin
+        self.layout, self.eps = layout, float(eps)
+
+    @property
+    def per_head(self):
+        w = self.w_q if self.w_q is not None else self.w_k
+        return w is not None and w.dim() == 2
+
+    def _struct(self, plan):
+        import torch
+        d, heads, n = plan.desc.head_dim, plan.desc.heads, plan.info.n_tokens
+        for w, name in ((self.w_q, "w_q"), (self.w_k, "w_k")):
+            if w is not None and tuple(w.shape) != ((heads, d) if self.per_head else (d,)):
+                raise ValueError(f"{name} must be [{d}] or [{heads}, {d}], got {tuple(w.shape)}")
+        for t, name in ((self.cos, "cos"), (self.sin, "sin")):
+            if t is not None and tuple(t.shape) != (n, d // 2):
+                raise ValueError(f"{name} must be [{n}, {d // 2}], got {tuple(t.shape)}")
+        f32 = torch.float32
+        return VsaNormRope(_ptr(self.w_q, f32, "w_q"), _ptr(self.w_k, f32, "w_k"), _ptr(self.cos, f32, "cos"),
+                           _ptr(self.sin, f32, "sin"), int(self.per_head), ROPE_LAYOUTS[self.layout], self.eps)
 
 
 def _karray(k_per_head, heads):
@@ -461,6 +581,211 @@ class Plan:
             _ptr(bufs.get("lse"), torch.float32, "lse", self.info.lse_elems),
             _ptr(bufs["workspace"], torch.uint8, "workspace", self.info.workspace_bytes),
             _ptr(o, bf, "o", n_tok), _stream(stream)), "vsa_layer_forward")
+
+    # ---- norm + rotation, and its gradient ------------------------------------------
+    def _token_view(self, t, name):
+        """(pointer, strides) of a bf16 [B, N, heads, head_dim] view with contiguous heads and channels."""
+        import torch
+        p = _device_ptr(t, torch.bfloat16, name)
+        B, n, heads, d = want = self.shapes()["tokens"]
+        if tuple(t.shape) != want:
+            raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+        if t.stride(3) != 1 or (heads > 1 and t.stride(2) != d):
+            raise ValueError(f"{name}'s heads and channels must be contiguous (strides {t.stride()})")
+        token = t.stride(1) if n > 1 else heads * d
+        return p, VsaStrides(t.stride(0) if B > 1 else token * n, token)
+
+    def _token_views(self, **views):
+        ptrs, strides = zip(*(self._token_view(t, name) for name, t in views.items()))
+        return ptrs, (VsaStrides * len(strides))(*strides)
+
+    def qk_norm_rope(self, q, k, norm, q_out, k_out, stream=None):
+        """RMS norm of every head's q and k row and the rotation, token-major views to token-major views
+        (an output may be its own input)."""
+        (pq, pk, pqo, pko), st = self._token_views(q=q, k=k, q_out=q_out, k_out=k_out)
+        n = norm._struct(self)
+        _check(library().vsa_qk_norm_rope(self._h, ctypes.byref(n), pq, pk, pqo, pko, st, _stream(stream)),
+               "vsa_qk_norm_rope")
+
+    def tile_norm_rope_pack_pool(self, q, k, v, norm, qp, kp, vp, workspace, stream=None):
+        """qk_norm_rope and tile_pack_pool in one pass; follow with tile_score_pooled."""
+        import torch
+        (pq, pk, pv), st = self._token_views(q=q, k=k, v=v)
+        n = norm._struct(self)
+        pe, bf = self.info.packed_elems, torch.bfloat16
+        _check(library().vsa_tile_norm_rope_pack_pool(
+            self._h, ctypes.byref(n), pq, pk, pv, st, _ptr(qp, bf, "qp", pe), _ptr(kp, bf, "kp", pe),
+            _ptr(vp, bf, "vp", pe), _ptr(workspace, torch.uint8, "workspace", self.info.workspace_bytes),
+            _stream(stream)), "vsa_tile_norm_rope_pack_pool")
+
+    def pooled(self, workspace):
+        """The descriptors that a pooling call left in the workspace: fp32 views [B, heads, ntv_max, w] of Q and K."""
+        import torch
+        base = _ptr(workspace, torch.uint8, "workspace", self.info.workspace_bytes)
+        pq, pk = ctypes.c_void_p(), ctypes.c_void_p()
+        _check(library().vsa_pooled_descriptors(self._h, base, ctypes.byref(pq), ctypes.byref(pk)),
+               "vsa_pooled_descriptors")
+        d, i = self.desc, self.info
+        w = d.head_dim * (3 if d.score_mode == SCORE_MODES["tripool"] else 1)
+        shape = (d.batch, d.heads, i.ntv_max, w)
+        n = d.batch * d.heads * i.ntv_max * w * 4
+        flat = workspace.view(-1)
+        return tuple(flat[p.value - base.value:p.value - base.value + n].view(torch.float32).view(shape)
+                     for p in (pq, pk))
+
+    def norm_bwd_workspace_bytes(self):
+        n = ctypes.c_int64()
+        _check(library().vsa_norm_bwd_workspace(self._h, ctypes.byref(n)), "vsa_norm_bwd_workspace")
+        return n.value
+
+    def _dw_ptrs(self, norm, dw_q, dw_k):
+        import torch
+        want = (self.desc.heads, self.desc.head_dim) if norm.per_head else (self.desc.head_dim,)
+        for t, name in ((dw_q, "dw_q"), (dw_k, "dw_k")):
+            if t is not None and tuple(t.shape) != want:
+                raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+        return _ptr(dw_q, torch.float32, "dw_q"), _ptr(dw_k, torch.float32, "dw_k")
+
+    def qk_norm_rope_bwd(self, dq_out, dk_out, q, k, norm, dq, dk, dw_q, dw_k, workspace, stream=None):
+        """Gradient of qk_norm_rope: dq, dk and (unless None) the weights' dw_q, dw_k."""
+        import torch
+        ptrs, st = self._token_views(dq_out=dq_out, dk_out=dk_out, q=q, k=k, dq=dq, dk=dk)
+        n = norm._struct(self)
+        _check(library().vsa_qk_norm_rope_bwd(
+            self._h, ctypes.byref(n), *ptrs, st, *self._dw_ptrs(norm, dw_q, dw_k),
+            _ptr(workspace, torch.uint8, "workspace", self.norm_bwd_workspace_bytes()), _stream(stream)),
+            "vsa_qk_norm_rope_bwd")
+
+    def tile_norm_rope_bwd(self, dqp, dkp, dvp, q, k, norm, dq, dk, dv, dw_q, dw_k, workspace, stream=None):
+        """Gradient of tile_norm_rope_pack_pool: packed gradients back to token-major dq, dk, dv and to the weights."""
+        import torch
+        pe, bf = self.info.packed_elems, torch.bfloat16
+        ptrs, st = self._token_views(q=q, k=k, dq=dq, dk=dk, dv=dv)
+        n = norm._struct(self)
+        _check(library().vsa_tile_norm_rope_bwd(
+            self._h, ctypes.byref(n), _ptr(dqp, bf, "dqp", pe), _ptr(dkp, bf, "dkp", pe), _ptr(dvp, bf, "dvp", pe),
+            *ptrs, st, *self._dw_ptrs(norm, dw_q, dw_k),
+            _ptr(workspace, torch.uint8, "workspace", self.norm_bwd_workspace_bytes()), _stream(stream)),
+            "vsa_tile_norm_rope_bwd")
+
+    # ---- gradient of the sparse attention --------------------------------------------
+    def attn_bwd_workspace_bytes(self):
+        n = ctypes.c_int64()
+        _check(library().vsa_attn_bwd_workspace(self._h, ctypes.byref(n)), "vsa_attn_bwd_workspace")
+        return n.value
+
+    def _attn_bwd_args(self, qp, kp, vp, op, lse, dop, idx):
+        import torch
+        pe, bf = self.info.packed_elems, torch.bfloat16
+        return (_ptr(qp, bf, "qp", pe), _ptr(kp, bf, "kp", pe), _ptr(vp, bf, "vp", pe), _ptr(op, bf, "op", pe),
+                _ptr(lse, torch.float32, "lse", self.info.lse_elems), _ptr(dop, bf, "dop", pe),
+                _ptr(idx, torch.int32, "idx", self.info.index_elems))
+
+    def _attn_bwd_outs(self, dqp, dkp, dvp, workspace, stream):
+        import torch
+        pe, bf = self.info.packed_elems, torch.bfloat16
+        return (_ptr(dqp, bf, "dqp", pe), _ptr(dkp, bf, "dkp", pe), _ptr(dvp, bf, "dvp", pe),
+                _ptr(workspace, torch.uint8, "workspace", self.attn_bwd_workspace_bytes()), _stream(stream))
+
+    def sparse_attn_bwd(self, qp, kp, vp, op, lse, dop, idx, dqp, dkp, dvp, workspace, stream=None, k_per_head=None):
+        """Gradient of sparse_attn on packed tiles: dqp, dkp, dvp from dop, the forward's inputs and its op, lse."""
+        _check(library().vsa_sparse_attn_bwd(
+            self._h, *self._attn_bwd_args(qp, kp, vp, op, lse, dop, idx), _karray(k_per_head, self.desc.heads),
+            *self._attn_bwd_outs(dqp, dkp, dvp, workspace, stream)), "vsa_sparse_attn_bwd")
+
+    def sparse_attn_ref_bwd(self, qp, kp, vp, op, lse, dop, idx, idx_ref, dqp, dkp, dvp, workspace, stream=None,
+                            k_per_head=None):
+        """Gradient of sparse_attn_ref (R2VA budgets)."""
+        import torch
+        _check(library().vsa_sparse_attn_ref_bwd(
+            self._h, *self._attn_bwd_args(qp, kp, vp, op, lse, dop, idx),
+            _ptr(idx_ref, torch.int32, "idx_ref", self.info.ref_index_elems),
+            _karray(k_per_head, self.desc.heads), *self._attn_bwd_outs(dqp, dkp, dvp, workspace, stream)),
+            "vsa_sparse_attn_ref_bwd")
+
+    # ---- linear layer with epilogue, and its gradient ---------------------------------
+    def linear_workspace_bytes(self, rows, n_in, n_out, backward=False, samples=0):
+        """Workspace of :meth:`linear` (or :meth:`linear_bwd`); samples: rows of the gate, 0 without one."""
+        per = rows // samples if samples else 0
+        if samples and rows % samples:
+            raise ValueError(f"{rows} rows do not divide into {samples} samples")
+        n = ctypes.c_int64()
+        _check(library().vsa_linear_workspace(self._h, int(rows), int(n_in), int(n_out), int(bool(backward)), int(per),
+                                              ctypes.byref(n)), "vsa_linear_workspace")
+        return n.value
+
+    @staticmethod
+    def _gate(gate, rows, n_out, name="gate"):
+        import torch
+        if gate is None:
+            return None, 0, 0
+        if gate.dim() != 2 or gate.shape[1] != n_out or gate.shape[0] < 1 or rows % gate.shape[0]:
+            raise ValueError(f"{name} must be [samples, {n_out}] with samples dividing {rows} rows, "
+                             f"got {tuple(gate.shape)}")
+        return _ptr(gate, torch.float32, name), rows // gate.shape[0], gate.shape[0]
+
+    @staticmethod
+    def _act(act):
+        if act not in ACTIVATIONS:
+            raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+        return ACTIVATIONS[act]
+
+    def _linear_workspace(self, workspace, need):
+        import torch
+        if need == 0:
+            return None
+        if workspace is None:
+            raise ValueError(f"this size needs a workspace of {need} bytes")
+        return _ptr(workspace, torch.uint8, "workspace", need)
+
+    def linear(self, x, w, y, bias=None, act="none", gate=None, residual=None, pre=None, workspace=None, stream=None):
+        """y = residual + gate * act(x w^T + bias): x [..., n_in], w [n_out, n_in], y [..., n_out] bf16, bias [n_out]
+        and gate [samples, n_out] fp32. pre, if given, receives x w^T + bias for :meth:`linear_bwd`."""
+        import torch
+        if w.dim() != 2:
+            raise ValueError(f"w must be [n_out, n_in], got {tuple(w.shape)}")
+        n_out, n_in = w.shape
+        px, ld_x, rows = _matrix(x, n_in, "x")
+        py, ld_y, _ = _matrix(y, n_out, "y", rows)
+        pr, ld_r = _matrix(residual, n_out, "residual", rows)[:2] if residual is not None else (None, 0)
+        pp, ld_p = _matrix(pre, n_out, "pre", rows)[:2] if pre is not None else (None, 0)
+        if bias is not None and tuple(bias.shape) != (n_out,):
+            raise ValueError(f"bias must be [{n_out}], got {tuple(bias.shape)}")
+        pg, per, _ = self._gate(gate, rows, n_out)
+        a = VsaLinearArgs(rows, n_in, n_out, px, ld_x, _ptr(w, torch.bfloat16, "w"),
+                          _ptr(bias, torch.float32, "bias"), self._act(act), pg, per, pr, ld_r, py, ld_y, pp, ld_p)
+        ws = self._linear_workspace(workspace, self.linear_workspace_bytes(rows, n_in, n_out))
+        _check(library().vsa_linear(self._h, ctypes.byref(a), ws, _stream(stream)), "vsa_linear")
+
+    def linear_bwd(self, dy, x, w, dx=None, dw=None, act="none", pre=None, gate=None, dbias=None, dgate=None,
+                   workspace=None, stream=None):
+        """Gradient of :meth:`linear`: any of dx [..., n_in], dw [n_out, n_in] (bf16), dbias [n_out] and dgate
+        [samples, n_out] (fp32); that of the residual is dy itself."""
+        import torch
+        if w.dim() != 2:
+            raise ValueError(f"w must be [n_out, n_in], got {tuple(w.shape)}")
+        n_out, n_in = w.shape
+        pdy, ld_dy, rows = _matrix(dy, n_out, "dy")
+        px, ld_x = _matrix(x, n_in, "x", rows)[:2] if x is not None else (None, 0)
+        pdx, ld_dx = _matrix(dx, n_in, "dx", rows)[:2] if dx is not None else (None, 0)
+        pp, ld_p = _matrix(pre, n_out, "pre", rows)[:2] if pre is not None else (None, 0)
+        if (act != "none" or dgate is not None) and pre is None:
+            raise ValueError("an activation's or a gate's gradient needs pre")
+        if dw is not None and x is None:
+            raise ValueError("dw needs x")
+        pg, per, samples = self._gate(gate, rows, n_out)
+        if dgate is not None and (gate is None or dgate.shape != gate.shape):
+            raise ValueError("dgate comes with a gate of its shape")
+        if dw is not None and dw.shape != w.shape:
+            raise ValueError(f"dw must be {tuple(w.shape)}, got {tuple(dw.shape)}")
+        if dbias is not None and tuple(dbias.shape) != (n_out,):
+            raise ValueError(f"dbias must be [{n_out}], got {tuple(dbias.shape)}")
+        bf, f32 = torch.bfloat16, torch.float32
+        a = VsaLinearGradArgs(rows, n_in, n_out, pdy, ld_dy, px, ld_x, _ptr(w, bf, "w"), self._act(act), pp, ld_p, pg,
+                              per, pdx, ld_dx, _ptr(dw, bf, "dw"), _ptr(dbias, f32, "dbias"),
+                              _ptr(dgate, f32, "dgate"))
+        ws = self._linear_workspace(workspace, self.linear_workspace_bytes(rows, n_in, n_out, True, samples))
+        _check(library().vsa_linear_bwd(self._h, ctypes.byref(a), ws, _stream(stream)), "vsa_linear_bwd")
 
     def set_wait_limit(self, limit_ns: int = 0):
         """Bound of every device-side wait of the plan's tcgen05 kernels (0: the two-second default)."""
