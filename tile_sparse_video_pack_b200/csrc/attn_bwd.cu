@@ -29,10 +29,14 @@
 // built from the index lists (validated on the way), its transpose by 32 x 32
 // ballots. The producer walks the stationary tile's row of it.
 //
-// Warp roles (320 threads): warp 0 producer (item, bit row, TMA), warp 1 MMA,
-// warps 2-9 two warpgroups that turn S and dP of alternate streamed pairs into
-// P and dS and write the finished gradients. Every wait is bounded as in the
-// forward.
+// Warp roles (416 threads): warp 0 producer (item, bit row, TMA); warps 1-3 and
+// 12 one MMA issuer for each of S, dP, acc1 and acc0, because an issuing thread
+// spends about 88 cycles on each instruction and its barriers where these N = 64
+// products take 32 to 48 (one thread for all four: 4,030 cycles per streamed pair
+// in the key pass); warps 4-11 two warpgroups that turn S and dP of alternate
+// streamed pairs into P and dS and write the finished gradients. X and Y have
+// their own rings of stages, since in the query pass Y is done after dP. Every
+// wait is bounded as in the forward.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -47,8 +51,15 @@ namespace {
 
 using namespace tc;
 
-constexpr int kBThreads = 320;
+constexpr int kBThreads = 416;
+constexpr int kWarpS = 1, kWarpDp = 2, kWarpAcc1 = 3, kWarpAcc0 = 12;   // MMA issuers
 constexpr uint32_t kBox = 64 * 64 * 2;           // one 64 x 64 bf16 TMA box
+
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 // ------------------------------------------------------------ preparation ----
 
@@ -166,27 +177,35 @@ struct BwdPair {
 template <int D, bool KEY>
 struct BSmem {
   static constexpr uint32_t kHalf = 128 * 128;                 // 128 rows x 64 channels
-  static constexpr uint32_t kTensor = (D / 64) * kHalf;        // one streamed tensor's pair
-  static constexpr uint32_t kStage = 2 * kTensor;              // Y, then X
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr uint32_t kTensor = (D / 64) * kHalf;        // one streamed tensor's pair of tiles
+  // stages of X and Y: what fits beside the stationary tiles and the P, dS buffers; the
+  // query pass holds X longer than Y
+  static constexpr int kXStages = D == 128 ? (KEY ? 2 : 3) : 4;
+  static constexpr int kYStages = D == 128 ? 2 : 4;
   static constexpr uint32_t kStat = (D / 64) * kBox;           // one stationary tile
   static constexpr uint32_t kPd = 128 * 128;                   // P or dS of a pair: 128 rows x 64 bf16
-  static constexpr uint32_t oStage = 0;
-  static constexpr uint32_t oStat = oStage + kStages * kStage;               // Xs, Ys
+  // D = 64: stage i of Y is followed by stage i of X (one operand of 128 channels)
+  static constexpr uint32_t kYStride = D == 128 ? kTensor : 2 * kTensor;
+  static constexpr uint32_t oY = 0;
+  static constexpr uint32_t oX = D == 128 ? kYStages * kTensor : kTensor;
+  static constexpr uint32_t kXStride = kYStride;
+  static constexpr uint32_t oStat = (kXStages + kYStages) * kTensor;         // Xs, Ys
   static constexpr uint32_t oDs = oStat + 2 * kStat;                         // two buffers
   static constexpr uint32_t oP = oDs + 2 * kPd;                              // two buffers (key pass)
   static constexpr uint32_t oBar = oP + (KEY ? 2 : 0) * kPd;
-  static constexpr uint32_t oMisc = oBar + 32 * 8;
+  static constexpr uint32_t oMisc = oBar + 40 * 8;
   static constexpr uint32_t oItem = oMisc + 16;
   static constexpr uint32_t oPair = oItem + 2 * sizeof(BwdItem);
   static constexpr uint32_t oCol = oPair + 4 * sizeof(BwdPair);              // query pass: lse2, delta of the tile
   static constexpr uint32_t oEnd = oCol + (KEY ? 0 : 2 * 2 * 64 * 4);        // per warpgroup
+  static_assert(D == 128 || kXStages == kYStages, "[Y; X] stages are shared");
 };
 
 enum {
-  Q_FULL = 0, Q_EMPTY = 4, Q_SFULL = 8, Q_PREADY = 10, Q_PFREE = 12, Q_IFULL = 14, Q_IEMPTY = 16, Q_STATFULL = 18,
-  Q_STATEMPTY, Q_ACCFULL, Q_ACCFREE, Q_DRAIN
+  Q_XFULL = 0, Q_XEMPTY = 4, Q_YFULL = 8, Q_YEMPTY = 12, Q_SFULL = 16, Q_PREADY = 18, Q_DSFREE = 20, Q_PFREE = 22,
+  Q_IFULL = 24, Q_IEMPTY = 26, Q_STATFULL = 28, Q_STATEMPTY, Q_ACCFULL, Q_ACCFREE, Q_DRAIN, Q_COUNT
 };
+static_assert(Q_COUNT <= 40, "barrier slots");
 
 struct BwdParams {
   const uint32_t* bits;             // this pass's bit matrix (rows = stationary tiles)
@@ -218,24 +237,28 @@ __global__ void __launch_bounds__(kBThreads, 1)
   uint32_t* gerr = prm.state;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kH = D / 64;                     // 64-channel halves
+  constexpr int kIssuers = KEY ? 4 : 3;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(bar(Q_FULL + i), 1);
-      mbar_init(bar(Q_EMPTY + i), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(Q_XFULL + i), 1);
+      mbar_init(bar(Q_XEMPTY + i), D == 128 || !KEY ? 1 : 2);   // acc1's product (d = 64: acc0's reads X too)
+      mbar_init(bar(Q_YFULL + i), 1);
+      mbar_init(bar(Q_YEMPTY + i), D == 128 || !KEY ? 1 : 2);   // acc0's (query pass: dP's, d = 64: acc1's); key pass, d = 64: acc1's too
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(Q_SFULL + i), 1);
+      mbar_init(bar(Q_SFULL + i), 2);            // S and dP
       mbar_init(bar(Q_PREADY + i), 4);           // one arrival per warp of the warpgroup
+      mbar_init(bar(Q_DSFREE + i), 1);
       mbar_init(bar(Q_PFREE + i), 1);
       mbar_init(bar(Q_IFULL + i), 1);
-      mbar_init(bar(Q_IEMPTY + i), 9);           // MMA thread, eight warps
+      mbar_init(bar(Q_IEMPTY + i), kIssuers + 8);
     }
     mbar_init(bar(Q_STATFULL), 1);
-    mbar_init(bar(Q_STATEMPTY), 1);
-    mbar_init(bar(Q_ACCFULL), 1);
+    mbar_init(bar(Q_STATEMPTY), 2);              // S and dP
+    mbar_init(bar(Q_ACCFULL), kIssuers - 2);
     mbar_init(bar(Q_ACCFREE), 8);
-    mbar_init(bar(Q_DRAIN), 1);
+    mbar_init(bar(Q_DRAIN), kIssuers);
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -251,7 +274,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer ---
-    uint32_t g = 0;                              // streamed pairs issued
+    uint32_t g = 0;                              // streamed pairs issued by this lane (0: X, 1: Y)
     int stat_it = -1;                            // item of the last stationary load
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
@@ -286,103 +309,82 @@ __global__ void __launch_bounds__(kBThreads, 1)
         b.count = prm.counts[int64_t(h) * prm.nt_max + tile];
         b.end = 0;
         mbar_arrive(bar(Q_IFULL + slot));
-        if (npairs > 0) {
-          ok = wait_bar(bar(Q_STATEMPTY), (it & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
-          if (ok) {
-            mbar_expect_tx(bar(Q_STATFULL), 2 * L::kStat);
-            const int y = (bh * prm.nt_max + tile) * 64;
-            for (int c = 0; c < kH; ++c) {
-              tma_load_2d(sbase + L::oStat + c * kBox, &txs, 64 * c, y, bar(Q_STATFULL));
-              tma_load_2d(sbase + L::oStat + L::kStat + c * kBox, &tys, 64 * c, y, bar(Q_STATFULL));
-            }
-            stat_it = int(it);
+        ok = wait_bar(bar(Q_STATEMPTY), (it & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
+        if (ok && npairs > 0) {
+          mbar_expect_tx(bar(Q_STATFULL), 2 * L::kStat);
+          const int y = (bh * prm.nt_max + tile) * 64;
+          for (int c = 0; c < kH; ++c) {
+            tma_load_2d(sbase + L::oStat + c * kBox, &txs, 64 * c, y, bar(Q_STATFULL));
+            tma_load_2d(sbase + L::oStat + L::kStat + c * kBox, &tys, 64 * c, y, bar(Q_STATFULL));
           }
-        } else {                                 // nothing to load: keep the barrier's phases in step with the items
-          ok = wait_bar(bar(Q_STATEMPTY), (it & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
-          if (ok) mbar_arrive(bar(Q_STATFULL));
+          stat_it = int(it);
+        } else if (ok) {
+          mbar_arrive(bar(Q_STATFULL));          // nothing to load: keep the phases in step with the items
         }
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      // the streamed tiles, two at a time, in ascending order
-      int first = -1;
-      for (int w0 = 0; w0 < prm.words && ok; w0 += 32) {
-        const uint32_t mine = w0 + lane < prm.words ? row[w0 + lane] : 0u;
-        const int wn = min(32, prm.words - w0);
-        for (int w = 0; w <= wn && ok; ++w) {
-          uint32_t bitsw = w < wn ? __shfl_sync(0xffffffffu, mine, w) : 0u;
-          const bool last = w == wn && w0 + 32 >= prm.words;   // after the last word: a tile left over
-          if (w == wn && !last) break;
-          while ((bitsw || (last && first >= 0)) && ok) {
-            int t = -1;
+      // the streamed tiles, two at a time, in ascending order: lane 0 loads X, lane 1 Y, each
+      // at its own pace (diverged lanes make independent progress)
+      if (lane < 2) {
+        const bool is_x = lane == 0;
+        const uint32_t ns = is_x ? L::kXStages : L::kYStages;
+        const CUtensorMap* map = is_x ? &tx : &ty;
+        int first = -1;
+        uint32_t next = row[0];
+        for (int w = 0; w < prm.words && ok; ++w) {
+          uint32_t bitsw = next;
+          const bool last = w + 1 == prm.words;
+          if (!last) next = row[w + 1];
+          while (ok && (bitsw || (last && first >= 0))) {
+            int t = -1;                          // a tile left over at the end streams alone
             if (bitsw) {
-              t = (w0 + w) * 32 + __ffs(bitsw) - 1;
+              t = w * 32 + __ffs(bitsw) - 1;
               bitsw &= bitsw - 1;
               if (first < 0) {
                 first = t;
                 continue;
               }
             }
-            if (lane == 0) {
-              const int st = int(g % L::kStages);
-              ok = wait_bar(bar(Q_EMPTY + st), ((g / L::kStages) & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
-              if (ok) {
-                pairs[st].ta = first;
-                pairs[st].tb = t;
-                const uint32_t fb = bar(Q_FULL + st);
-                mbar_expect_tx(fb, L::kStage);
-                const int ya = (bh * prm.nt_max + first) * 64, yb = t >= 0 ? (bh * prm.nt_max + t) * 64 : ya;
-                const uint32_t sy = sbase + L::oStage + st * L::kStage, sx = sy + L::kTensor;
-                for (int c = 0; c < kH; ++c) {
-                  tma_load_2d(sx + c * L::kHalf, &tx, 64 * c, ya, fb);
-                  tma_load_2d(sx + c * L::kHalf + kBox, &tx, 64 * c, yb, fb);
-                }
-                for (int c = 0; c < kH; ++c) {
-                  tma_load_2d(sy + c * L::kHalf, &ty, 64 * c, ya, fb);
-                  tma_load_2d(sy + c * L::kHalf + kBox, &ty, 64 * c, yb, fb);
-                }
-              }
+            const uint32_t st = g % ns;
+            ok = wait_bar(bar((is_x ? Q_XEMPTY : Q_YEMPTY) + int(st)), ((g / ns) & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
+            if (!ok) break;
+            if (is_x) pairs[g & 3] = BwdPair{first, t};   // read before this pair's stage is free again
+            const uint32_t fb = bar((is_x ? Q_XFULL : Q_YFULL) + int(st));
+            mbar_expect_tx(fb, L::kTensor);
+            const int ya = (bh * prm.nt_max + first) * 64, yb = t >= 0 ? (bh * prm.nt_max + t) * 64 : ya;
+            const uint32_t dst = sbase + (is_x ? L::oX + st * L::kXStride : L::oY + st * L::kYStride);
+            for (int c = 0; c < kH; ++c) {
+              tma_load_2d(dst + c * L::kHalf, map, 64 * c, ya, fb);
+              tma_load_2d(dst + c * L::kHalf + kBox, map, 64 * c, yb, fb);
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (ok) ++g;
+            ++g;
             first = -1;
           }
         }
       }
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok);
     }
-    if (lane == 0 && *abort_flag) {              // let the copies land before shared memory is released
-      if (stat_it >= 0) drain_wait(bar(Q_STATFULL), uint32_t(stat_it) & 1);
-      for (uint32_t j = g >= uint32_t(L::kStages) ? g - L::kStages : 0; j < g; ++j)
-        drain_wait(bar(Q_FULL + int(j % L::kStages)), (j / L::kStages) & 1);
+    if (lane < 2 && *abort_flag) {               // let the copies land before shared memory is released
+      if (lane == 0 && stat_it >= 0) drain_wait(bar(Q_STATFULL), uint32_t(stat_it) & 1);
+      const uint32_t ns = lane == 0 ? L::kXStages : L::kYStages;
+      for (uint32_t j = g >= ns ? g - ns : 0; j < g; ++j)
+        drain_wait(bar((lane == 0 ? Q_XFULL : Q_YFULL) + int(j % ns)), (j / ns) & 1);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // --------------------------------------------------------------- MMA ---
+  } else if (warp == kWarpS || warp == kWarpDp) {
+    // -------------------------------------------- S = X Xs^T, dP = Y Ys^T ---
     if (lane == 0) {
+      const bool is_s = warp == kWarpS;
       constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0);
-      constexpr uint32_t idA = idesc_bf16(128, 64, 1, 1);
-      const uint64_t dxs = sw128_desc(sbase + L::oStat, 16, 1024);
-      const uint64_t dys = sw128_desc(sbase + L::oStat + L::kStat, 16, 1024);
-      uint32_t g = 0;                            // streamed pairs of earlier items
+      const uint64_t db = sw128_desc(sbase + L::oStat + (is_s ? 0 : L::kStat), 16, 1024);
+      const uint64_t da0 = sw128_desc(sbase + (is_s ? L::oX : L::oY), 16, 1024);
+      const uint32_t stride = (is_s ? L::kXStride : L::kYStride) >> 4;
+      const uint32_t ns = is_s ? L::kXStages : L::kYStages;
+      const int full = is_s ? Q_XFULL : Q_YFULL;
+      const uint32_t td = tmem + (is_s ? 0 : 64);
+      uint32_t g = 0;
       bool ok = true;
-      // S and dP of pair p into buffer p & 1
-      auto scores = [&](uint32_t p) {
-        const int st = int(p % L::kStages);
-        if (!wait_bar(bar(Q_FULL + st), (p / L::kStages) & 1, abort_flag, gerr, prm.wait_ns)) return false;
-        tc_fence_after();
-        const uint32_t sy = sbase + L::oStage + st * L::kStage, sx = sy + L::kTensor;
-        const uint64_t dx = sw128_desc(sx, 16, 1024), dy = sw128_desc(sy, 16, 1024);
-        const uint32_t tS = tmem + (p & 1) * 128;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma(tS, dx + (((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4), dxs + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
-                 idS, kk > 0 ? 1u : 0u);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma(tS + 64, dy + (((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4),
-                 dys + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
-        tc_commit(bar(Q_SFULL + int(p & 1)));
-        return true;
-      };
       for (uint32_t it = 0; ok; ++it) {
         const int slot = it & 1;
         if (!(ok = wait_bar(bar(Q_IFULL + slot), (it >> 1) & 1, abort_flag, gerr, prm.wait_ns))) break;
@@ -391,42 +393,68 @@ __global__ void __launch_bounds__(kBThreads, 1)
         mbar_arrive(bar(Q_IEMPTY + slot));
         if (end) break;
         if (!(ok = wait_bar(bar(Q_STATFULL), it & 1, abort_flag, gerr, prm.wait_ns))) break;
+        for (int j = 0; j < npairs; ++j, ++g) {
+          const uint32_t st = g % ns, b = g & 1;
+          if (!(ok = wait_bar(bar(full + int(st)), (g / ns) & 1, abort_flag, gerr, prm.wait_ns))) break;
+          // the buffer's previous pair has been read
+          if (g >= 2 && !(ok = wait_bar(bar(Q_PREADY + int(b)), ((g >> 1) - 1) & 1, abort_flag, gerr, prm.wait_ns))) break;
+          tc_fence_after();
+          const uint64_t da = da0 + st * stride;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma(td + b * 128, da + (((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4),
+                   db + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+          tc_commit(bar(Q_SFULL + int(b)));
+          if constexpr (!KEY && D == 128) {
+            if (!is_s) tc_commit(bar(Q_YEMPTY + int(st)));   // dP is the query pass's only use of Y
+          }
+        }
+        if (ok) tc_commit(bar(Q_STATEMPTY));
+      }
+      tc_commit(bar(Q_DRAIN));
+      drain_wait(bar(Q_DRAIN), 0);
+    }
+    __syncwarp();
+  } else if (warp == kWarpAcc1 || warp == kWarpAcc0) {
+    // ---------------------------------- acc1^T += X^T dS, acc0^T += Y^T P ---
+    if (lane == 0 && (KEY || warp == kWarpAcc1)) {
+      const bool is1 = warp == kWarpAcc1;
+      constexpr uint32_t idA = idesc_bf16(128, 64, 1, 1);
+      // A = X^T or Y^T, MN-major: 64-channel chunks kHalf apart. For d = 64 both are one
+      // operand of 128 channels, [Y; X]: dV^T is in lanes 0-63 of acc0, dK^T / dQ^T in
+      // lanes 64-127 of acc1, and the other halves are not used (Y's stage is then read
+      // here too, so its release counts this product).
+      const uint64_t da0 = sw128_desc(sbase + (is1 && D == 128 ? L::oX : L::oY), L::kHalf, 1024);
+      const uint32_t stride = (is1 ? L::kXStride : L::kYStride) >> 4;
+      const uint32_t ns = is1 ? L::kXStages : L::kYStages;
+      const uint64_t db0 = sw128_desc(sbase + (is1 ? L::oDs : L::oP), 8192, 1024);
+      const uint32_t td = tmem + (is1 ? 320 : 256);
+      const int full = is1 ? Q_XFULL : Q_YFULL;
+      uint32_t g = 0;
+      bool ok = true;
+      for (uint32_t it = 0; ok; ++it) {
+        const int slot = it & 1;
+        if (!(ok = wait_bar(bar(Q_IFULL + slot), (it >> 1) & 1, abort_flag, gerr, prm.wait_ns))) break;
+        const int npairs = items[slot].pairs;
+        const bool end = items[slot].end != 0;
+        mbar_arrive(bar(Q_IEMPTY + slot));
+        if (end) break;
         // the accumulators are free once the previous item's gradients are read
         if (!(ok = wait_bar(bar(Q_ACCFREE), (it & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
-        tc_fence_after();
-        if (npairs > 0 && !(ok = scores(g))) break;
-        if (npairs <= 1) tc_commit(bar(Q_STATEMPTY));
         for (int j = 0; j < npairs; ++j, ++g) {
-          if (j + 1 < npairs) {
-            // buffer (g + 1) & 1 was read before PREADY of pair g - 1, which was waited for
-            if (!(ok = scores(g + 1))) break;
-            if (j + 2 == npairs) tc_commit(bar(Q_STATEMPTY));
-          }
-          const int b = g & 1;
-          if (!(ok = wait_bar(bar(Q_PREADY + b), (g >> 1) & 1, abort_flag, gerr, prm.wait_ns))) break;
+          const uint32_t st = g % ns, b = g & 1;
+          if (!(ok = wait_bar(bar(full + int(st)), (g / ns) & 1, abort_flag, gerr, prm.wait_ns))) break;
+          if (!(ok = wait_bar(bar(Q_PREADY + int(b)), (g >> 1) & 1, abort_flag, gerr, prm.wait_ns))) break;
           tc_fence_after();
-          const int st = int(g % L::kStages);
-          const uint32_t sy = sbase + L::oStage + st * L::kStage;
-          // A = Y^T and X^T, MN-major: 64-channel chunks kHalf apart. For d = 64 both
-          // are one operand of 128 channels, [Y; X]: dV^T is in lanes 0-63 of acc0,
-          // dK^T / dQ^T in lanes 64-127 of acc1, and the other halves are not used.
-          const uint64_t day = sw128_desc(sy, L::kHalf, 1024);
-          const uint64_t dax = D == 128 ? sw128_desc(sy + L::kTensor, L::kHalf, 1024) : day;
-          const uint64_t dds = sw128_desc(sbase + L::oDs + b * L::kPd, 8192, 1024);
-          const uint64_t dp = sw128_desc(sbase + L::oP + b * L::kPd, 8192, 1024);
-          if constexpr (KEY) {
+          const uint64_t da = da0 + st * stride, db = db0 + b * (L::kPd >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)       // 16 streamed rows per step
-              tc_mma(tmem + 256, day + ((kk * 2048) >> 4), dp + ((kk * 2048) >> 4), idA, (j > 0 || kk > 0) ? 1u : 0u);
-          }
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma(tmem + 320, dax + ((kk * 2048) >> 4), dds + ((kk * 2048) >> 4), idA, (j > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(bar(Q_EMPTY + st));
-          tc_commit(bar(Q_PFREE + b));
+          for (int kk = 0; kk < 8; ++kk)         // 16 streamed rows per step
+            tc_mma(td, da + ((kk * 2048) >> 4), db + ((kk * 2048) >> 4), idA, (j > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(bar((is1 ? Q_DSFREE : Q_PFREE) + int(b)));
+          if (is1 || D == 64) tc_commit(bar(Q_XEMPTY + int(st)));
+          if ((!is1 && KEY) || (is1 && D == 64)) tc_commit(bar(Q_YEMPTY + int(st)));
         }
-        if (!ok) break;
-        tc_commit(bar(Q_ACCFULL));
+        if (ok) tc_commit(bar(Q_ACCFULL));
       }
       tc_commit(bar(Q_DRAIN));
       drain_wait(bar(Q_DRAIN), 0);
@@ -434,11 +462,12 @@ __global__ void __launch_bounds__(kBThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------- P, dS, output ---
-    const int wg = (warp - 2) >> 2;
+    const int wg = (warp - 4) >> 2;
     const int q4 = warp & 3;                     // TMEM lane quarter this warp may read
     const int r = q4 * 32 + lane;                // streamed row, TMEM lane
     const uint32_t lane_off = uint32_t(q4 * 32) << 16;
-    float* col = reinterpret_cast<float*>(smem + L::oCol) + wg * 128;   // query pass: lse2 [64], delta [64]
+    float* col = reinterpret_cast<float*>(smem + L::oCol) + wg * 128;   // query pass: -lse2 [64], -delta [64]
+    const uint64_t c2 = f2pack(prm.scale_log2, prm.scale_log2);
     uint32_t g = 0;
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
@@ -454,32 +483,43 @@ __global__ void __launch_bounds__(kBThreads, 1)
         // this warpgroup's copy of the stationary queries' lse2 and delta; its warps meet
         // before the write (the previous item's reads) and after it
         asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
-        const int x = (warp - 2 - 4 * wg) * 32 + lane;
-        col[x] = x < 64 ? prm.lse2[(base + inf.tile) * 64 + x] : prm.delta[(base + inf.tile) * 64 + x - 64];
+        const int x = (warp - 4 - 4 * wg) * 32 + lane;
+        col[x] = -(x < 64 ? prm.lse2[(base + inf.tile) * 64 + x] : prm.delta[(base + inf.tile) * 64 + x - 64]);
         asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
       }
       for (int j = 0; j < inf.pairs; ++j, ++g) {
         if (int(g & 1) != wg) continue;
-        const int st = int(g % L::kStages);
-        ok = wait_bar(bar(Q_FULL + st), (g / L::kStages) & 1, abort_flag, gerr, prm.wait_ns);
+        const uint32_t st = g % L::kXStages;
+        ok = wait_bar(bar(Q_XFULL + int(st)), (g / L::kXStages) & 1, abort_flag, gerr, prm.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        const int tile = r < 64 ? pairs[st].ta : pairs[st].tb;
-        float rl = 0.f, rd = 0.f;                // key pass: lse2, delta of my query row
-        bool live = tile >= 0;
-        if (live) {
-          if constexpr (KEY) {
-            rl = prm.lse2[(base + tile) * 64 + (r & 63)];
-            rd = prm.delta[(base + tile) * 64 + (r & 63)];
-            live = rl < INFINITY;
-          } else {
-            live = (r & 63) < prm.counts[int64_t(h) * prm.nt_max + tile];
+        const BwdPair pr = pairs[g & 3];
+        const int tile = r < 64 ? pr.ta : pr.tb;
+        // key pass: minus lse2 and minus delta of my query row (an unused slot's lse2 is +inf,
+        // which makes its P and dS 0); query pass: whether my key row is one
+        float rl = -INFINITY, rd = 0.f;
+        bool live = true;
+        if constexpr (KEY) {
+          if (tile >= 0) {
+            rl = -prm.lse2[(base + tile) * 64 + (r & 63)];
+            rd = -prm.delta[(base + tile) * 64 + (r & 63)];
           }
+        } else {
+          live = tile >= 0 && (r & 63) < prm.counts[int64_t(h) * prm.nt_max + tile];
+        }
+        // the buffers' previous pair has been consumed by its products
+        if (g >= 2) {
+          ok = wait_bar(bar(Q_DSFREE + wg), ((g >> 1) - 1) & 1, abort_flag, gerr, prm.wait_ns);
+          if (KEY && ok) ok = wait_bar(bar(Q_PFREE + wg), ((g >> 1) - 1) & 1, abort_flag, gerr, prm.wait_ns);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         }
         ok = wait_bar(bar(Q_SFULL + wg), (g >> 1) & 1, abort_flag, gerr, prm.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
-        uint32_t pk[KEY ? 32 : 1], dk[32];
         const uint32_t tS = tmem + wg * 128 + lane_off;
+        // row r, 64 columns: 128 bytes, 16-byte chunks swizzled by the row
+        uint8_t* drow = smem + L::oDs + wg * L::kPd + r * 128;
+        uint8_t* prow = smem + L::oP + wg * L::kPd + r * 128;
+        const uint64_t rl2 = f2pack(rl, rl), rd2 = f2pack(rd, rd);
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           uint32_t s[32], dp[32];
@@ -488,35 +528,36 @@ __global__ void __launch_bounds__(kBThreads, 1)
           tmem_wait_ld(s);
           reg_fence(dp);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float p[2], ds[2];
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t pk[4], dk[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float l2 = KEY ? rl : col[c + i + e], dl = KEY ? rd : col[64 + c + i + e];
-              const float x = ex2(fmaf(__uint_as_float(s[i + e]), prm.scale_log2, -l2));
-              p[e] = live ? x : 0.f;
-              ds[e] = live ? x * (__uint_as_float(dp[i + e]) - dl) : 0.f;
+            for (int e = 0; e < 4; ++e) {
+              const int n = i + 2 * e;
+              uint64_t l2 = rl2, dl = rd2;
+              if constexpr (!KEY) {
+                l2 = *reinterpret_cast<const uint64_t*>(col + c + n);
+                dl = *reinterpret_cast<const uint64_t*>(col + 64 + c + n);
+              }
+              float x0, x1, d0, d1;
+              f2unpack(ffma2(f2pack(__uint_as_float(s[n]), __uint_as_float(s[n + 1])), c2, l2), x0, x1);
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              if constexpr (!KEY) {
+                x0 = live ? x0 : 0.f;
+                x1 = live ? x1 : 0.f;
+              }
+              f2unpack(fmul2(f2pack(x0, x1),
+                             fadd2(f2pack(__uint_as_float(dp[n]), __uint_as_float(dp[n + 1])), dl)),
+                       d0, d1);
+              pk[e] = bf16x2(x0, x1);
+              dk[e] = bf16x2(d0, d1);
             }
-            if constexpr (KEY) pk[(c + i) / 2] = bf16x2(p[0], p[1]);
-            dk[(c + i) / 2] = bf16x2(ds[0], ds[1]);
+            const int at = (((c + i) >> 3) ^ (r & 7)) * 16;
+            *reinterpret_cast<uint4*>(drow + at) = make_uint4(dk[0], dk[1], dk[2], dk[3]);
+            if constexpr (KEY) *reinterpret_cast<uint4*>(prow + at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
         }
         tc_fence_before();
-        // the buffer's previous pair has been consumed by its products
-        if (g >= 2) {
-          ok = wait_bar(bar(Q_PFREE + wg), ((g >> 1) - 1) & 1, abort_flag, gerr, prm.wait_ns);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        }
-        // row r, 64 columns: 128 bytes, 16-byte chunks swizzled by the row
-        uint8_t* drow = smem + L::oDs + wg * L::kPd + r * 128;
-        uint8_t* prow = smem + L::oP + wg * L::kPd + r * 128;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = (i ^ (r & 7)) * 16;
-          *reinterpret_cast<uint4*>(drow + at) = make_uint4(dk[4 * i], dk[4 * i + 1], dk[4 * i + 2], dk[4 * i + 3]);
-          if constexpr (KEY)
-            *reinterpret_cast<uint4*>(prow + at) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         warp_arrive(bar(Q_PREADY + wg));
       }
@@ -533,7 +574,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const float f = is_v ? 1.f : prm.scale;
       constexpr int kCols = KEY ? 64 : 32;
       const int c0 = KEY ? 0 : 32 * wg;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < kCols; c += 32) {
         uint32_t v[32];
         tmem_ld32(tmem + (is_v ? 256 : 320) + lane_off + c0 + c, v);

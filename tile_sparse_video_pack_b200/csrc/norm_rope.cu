@@ -125,20 +125,44 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// The normed and turned row as stored (bf16 words).
+// Sum of squares of a row: a pairwise tree over its d / 4 channel quads, the same
+// in either layout -- a chain inside a quad, then quads d / 8, d / 16, .., 1 apart --
+// so that every term passes through at most eight roundings. Halves: a lane
+// holds quads c and c + d / 8, so the first step needs no exchange. Interleaved: a
+// lane holds quads 2c and 2c + 1; the first step trades one of its two sums for
+// the other lane's, so that the tree costs one shuffle more, not twice as many.
+template <int CPR, bool HALVES>
+__device__ __forceinline__ float square_sum(const float (&a)[4], const float (&b)[4]) {
+  // squares of bf16 values are exact in fp32, so the fused chains round like plain ones
+  if (HALVES) {
+    float s = fmaf(a[3], a[3], fmaf(a[2], a[2], fmaf(a[1], a[1], a[0] * a[0]))) +
+              fmaf(b[3], b[3], fmaf(b[2], b[2], fmaf(b[1], b[1], b[0] * b[0])));
+#pragma unroll
+    for (int o = CPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  }
+  const float even = fmaf(b[1], b[1], fmaf(a[1], a[1], fmaf(b[0], b[0], a[0] * a[0])));
+  const float odd = fmaf(b[3], b[3], fmaf(a[3], a[3], fmaf(b[2], b[2], a[2] * a[2])));
+  const bool upper = threadIdx.x & (CPR / 2);
+  float s = (upper ? odd : even) + __shfl_xor_sync(0xffffffffu, upper ? even : odd, CPR / 2);
+#pragma unroll
+  for (int o = CPR / 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s + __shfl_xor_sync(0xffffffffu, s, CPR / 2);
+}
+
+// The normed and turned row as stored (bf16 words). Each product of the rotation
+// is rounded by itself, as the formula is written: with a fused multiply-add one
+// of a pair's two products would be exact and the other not.
 template <int CPR, bool HALVES>
 __device__ __forceinline__ uint4 norm_rope_row(uint4 v, const Weights& w, const Turn& t, float eps) {
   float a[4], b[4];
   to_pairs<HALVES>(v, a, b);
-  float ss = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
-  const float r = rsqrtf(row_sum<CPR>(ss) * (1.f / (CPR * 8)) + eps);
+  const float r = rsqrtf(square_sum<CPR, HALVES>(a, b) * (1.f / (CPR * 8)) + eps);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float na = a[j] * r * w.a[j], nb = b[j] * r * w.b[j];
-    a[j] = fmaf(na, t.c[j], -nb * t.s[j]);
-    b[j] = fmaf(na, t.s[j], nb * t.c[j]);
+    const float na = __fmul_rn(__fmul_rn(a[j], r), w.a[j]), nb = __fmul_rn(__fmul_rn(b[j], r), w.b[j]);
+    a[j] = __fsub_rn(__fmul_rn(na, t.c[j]), __fmul_rn(nb, t.s[j]));
+    b[j] = __fadd_rn(__fmul_rn(na, t.s[j]), __fmul_rn(nb, t.c[j]));
   }
   return from_pairs<HALVES>(a, b);
 }
@@ -324,10 +348,7 @@ __device__ __forceinline__ uint4 norm_rope_grad_row(uint4 vy, uint4 vx, const We
   float xa[4], xb[4], ya[4], yb[4];
   to_pairs<HALVES>(vx, xa, xb);
   to_pairs<HALVES>(vy, ya, yb);
-  float ss = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) ss = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], ss));
-  const float r = rsqrtf(row_sum<CPR>(ss) * (1.f / (CPR * 8)) + eps);
+  const float r = rsqrtf(square_sum<CPR, HALVES>(xa, xb) * (1.f / (CPR * 8)) + eps);
   float dot = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
