@@ -33,10 +33,12 @@
 // 12 one MMA issuer for each of S, dP, acc1 and acc0, because an issuing thread
 // spends about 88 cycles on each instruction and its barriers where these N = 64
 // products take 32 to 48 (one thread for all four: 4,030 cycles per streamed pair
-// in the key pass); warps 4-11 two warpgroups that turn S and dP of alternate
-// streamed pairs into P and dS and write the finished gradients. X and Y have
-// their own rings of stages, since in the query pass Y is done after dP. Every
-// wait is bounded as in the forward.
+// in the key pass); warps 4-11 two warpgroups that turn S and dP into P and dS,
+// half of the columns each, and write the finished gradients. Both work on the
+// same pair: with alternate pairs the step from S to P took twice as long, and it
+// is on the path of a stage's release. P and dS stay in registers until the
+// previous pair's products have read theirs, so they need one buffer. Every wait
+// is bounded as in the forward.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -177,33 +179,41 @@ struct BwdPair {
 template <int D, bool KEY>
 struct BSmem {
   static constexpr uint32_t kHalf = 128 * 128;                 // 128 rows x 64 channels
-  static constexpr uint32_t kTensor = (D / 64) * kHalf;        // one streamed tensor's pair of tiles
-  // stages of X and Y: what fits beside the stationary tiles and the P, dS buffers; the
-  // query pass holds X longer than Y
-  static constexpr int kXStages = D == 128 ? (KEY ? 2 : 3) : 4;
-  static constexpr int kYStages = D == 128 ? 2 : 4;
+  static constexpr uint32_t kTensor = (D / 64) * kHalf;        // one slot: one streamed tensor's pair of tiles
+  static constexpr int kSlots = D == 128 ? 5 : 8;              // what fits beside the rest (D = 64: ample)
   static constexpr uint32_t kStat = (D / 64) * kBox;           // one stationary tile
   static constexpr uint32_t kPd = 128 * 128;                   // P or dS of a pair: 128 rows x 64 bf16
-  // D = 64: stage i of Y is followed by stage i of X (one operand of 128 channels)
-  static constexpr uint32_t kYStride = D == 128 ? kTensor : 2 * kTensor;
-  static constexpr uint32_t oY = 0;
-  static constexpr uint32_t oX = D == 128 ? kYStages * kTensor : kTensor;
-  static constexpr uint32_t kXStride = kYStride;
-  static constexpr uint32_t oStat = (kXStages + kYStages) * kTensor;         // Xs, Ys
-  static constexpr uint32_t oDs = oStat + 2 * kStat;                         // two buffers
-  static constexpr uint32_t oP = oDs + 2 * kPd;                              // two buffers (key pass)
-  static constexpr uint32_t oBar = oP + (KEY ? 2 : 0) * kPd;
+  static constexpr uint32_t oStat = kSlots * kTensor;          // Xs, Ys
+  static constexpr uint32_t oDs = oStat + 2 * kStat;
+  static constexpr uint32_t oP = oDs + kPd;                    // key pass
+  static constexpr uint32_t oBar = oP + (KEY ? 1 : 0) * kPd;
   static constexpr uint32_t oMisc = oBar + 40 * 8;
   static constexpr uint32_t oItem = oMisc + 16;
   static constexpr uint32_t oPair = oItem + 2 * sizeof(BwdItem);
   static constexpr uint32_t oCol = oPair + 4 * sizeof(BwdPair);              // query pass: lse2, delta of the tile
-  static constexpr uint32_t oEnd = oCol + (KEY ? 0 : 2 * 2 * 64 * 4);        // per warpgroup
-  static_assert(D == 128 || kXStages == kYStages, "[Y; X] stages are shared");
+  static constexpr uint32_t oEnd = oCol + (KEY ? 0 : 2 * 2 * 64 * 4);        // two items' worth
 };
 
+// Slot and use count of streamed pair g's X or Y. d = 128, key pass: both live
+// from their load to the end of acc0 / acc1, so one ring of five alternates them
+// (2.5 pairs). Query pass: Y is done after dP, X after acc1: rings of two and
+// three. d = 64: slots in pairs, [Y; X] one operand of 128 channels, four pairs.
+struct SlotUse {
+  uint32_t slot, use;
+};
+template <int D, bool KEY>
+__device__ __forceinline__ SlotUse slot_of(uint32_t g, bool is_x) {
+  if (D == 64) return {2 * (g % 4) + (is_x ? 1u : 0u), g / 4};
+  if (KEY) {
+    const uint32_t n = 2 * g + (is_x ? 0 : 1);
+    return {n % 5, n / 5};
+  }
+  return is_x ? SlotUse{g % 3, g / 3} : SlotUse{3 + g % 2, g / 2};
+}
+
 enum {
-  Q_XFULL = 0, Q_XEMPTY = 4, Q_YFULL = 8, Q_YEMPTY = 12, Q_SFULL = 16, Q_PREADY = 18, Q_DSFREE = 20, Q_PFREE = 22,
-  Q_IFULL = 24, Q_IEMPTY = 26, Q_STATFULL = 28, Q_STATEMPTY, Q_ACCFULL, Q_ACCFREE, Q_DRAIN, Q_COUNT
+  Q_FULL = 0, Q_EMPTY = 8, Q_SFULL = 16, Q_SFREE = 18, Q_IFULL = 20, Q_IEMPTY = 22, Q_PREADY = 24, Q_PFREE,
+  Q_STATFULL, Q_STATEMPTY, Q_ACCFULL, Q_ACCFREE, Q_COLS, Q_DRAIN, Q_COUNT
 };
 static_assert(Q_COUNT <= 40, "barrier slots");
 
@@ -240,24 +250,23 @@ __global__ void __launch_bounds__(kBThreads, 1)
   constexpr int kIssuers = KEY ? 4 : 3;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(Q_XFULL + i), 1);
-      mbar_init(bar(Q_XEMPTY + i), D == 128 || !KEY ? 1 : 2);   // acc1's product (d = 64: acc0's reads X too)
-      mbar_init(bar(Q_YFULL + i), 1);
-      mbar_init(bar(Q_YEMPTY + i), D == 128 || !KEY ? 1 : 2);   // acc0's (query pass: dP's, d = 64: acc1's); key pass, d = 64: acc1's too
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(bar(Q_FULL + i), 1);
+      mbar_init(bar(Q_EMPTY + i), D == 64 && KEY ? 2 : 1);   // d = 64: acc0 and acc1 read both of [Y; X]
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Q_SFULL + i), 2);            // S and dP
-      mbar_init(bar(Q_PREADY + i), 4);           // one arrival per warp of the warpgroup
-      mbar_init(bar(Q_DSFREE + i), 1);
-      mbar_init(bar(Q_PFREE + i), 1);
+      mbar_init(bar(Q_SFREE + i), 8);            // one arrival per warp of the warpgroups
       mbar_init(bar(Q_IFULL + i), 1);
       mbar_init(bar(Q_IEMPTY + i), kIssuers + 8);
     }
+    mbar_init(bar(Q_PREADY), 8);
+    mbar_init(bar(Q_PFREE), kIssuers - 2);
     mbar_init(bar(Q_STATFULL), 1);
     mbar_init(bar(Q_STATEMPTY), 2);              // S and dP
     mbar_init(bar(Q_ACCFULL), kIssuers - 2);
     mbar_init(bar(Q_ACCFREE), 8);
+    mbar_init(bar(Q_COLS), 8);
     mbar_init(bar(Q_DRAIN), kIssuers);
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -327,7 +336,6 @@ __global__ void __launch_bounds__(kBThreads, 1)
       // at its own pace (diverged lanes make independent progress)
       if (lane < 2) {
         const bool is_x = lane == 0;
-        const uint32_t ns = is_x ? L::kXStages : L::kYStages;
         const CUtensorMap* map = is_x ? &tx : &ty;
         int first = -1;
         uint32_t next = row[0];
@@ -345,14 +353,14 @@ __global__ void __launch_bounds__(kBThreads, 1)
                 continue;
               }
             }
-            const uint32_t st = g % ns;
-            ok = wait_bar(bar((is_x ? Q_XEMPTY : Q_YEMPTY) + int(st)), ((g / ns) & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
+            const SlotUse u = slot_of<D, KEY>(g, is_x);
+            ok = wait_bar(bar(Q_EMPTY + int(u.slot)), (u.use & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
             if (!ok) break;
             if (is_x) pairs[g & 3] = BwdPair{first, t};   // read before this pair's stage is free again
-            const uint32_t fb = bar((is_x ? Q_XFULL : Q_YFULL) + int(st));
+            const uint32_t fb = bar(Q_FULL + int(u.slot));
             mbar_expect_tx(fb, L::kTensor);
             const int ya = (bh * prm.nt_max + first) * 64, yb = t >= 0 ? (bh * prm.nt_max + t) * 64 : ya;
-            const uint32_t dst = sbase + (is_x ? L::oX + st * L::kXStride : L::oY + st * L::kYStride);
+            const uint32_t dst = sbase + u.slot * L::kTensor;
             for (int c = 0; c < kH; ++c) {
               tma_load_2d(dst + c * L::kHalf, map, 64 * c, ya, fb);
               tma_load_2d(dst + c * L::kHalf + kBox, map, 64 * c, yb, fb);
@@ -367,9 +375,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
     }
     if (lane < 2 && *abort_flag) {               // let the copies land before shared memory is released
       if (lane == 0 && stat_it >= 0) drain_wait(bar(Q_STATFULL), uint32_t(stat_it) & 1);
-      const uint32_t ns = lane == 0 ? L::kXStages : L::kYStages;
-      for (uint32_t j = g >= ns ? g - ns : 0; j < g; ++j)
-        drain_wait(bar((lane == 0 ? Q_XFULL : Q_YFULL) + int(j % ns)), (j / ns) & 1);
+      for (uint32_t j = g >= 4 ? g - 4 : 0; j < g; ++j) {   // at most four loads of a lane are in flight
+        const SlotUse u = slot_of<D, KEY>(j, lane == 0);
+        drain_wait(bar(Q_FULL + int(u.slot)), u.use & 1);
+      }
     }
     __syncwarp();
   } else if (warp == kWarpS || warp == kWarpDp) {
@@ -378,10 +387,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const bool is_s = warp == kWarpS;
       constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0);
       const uint64_t db = sw128_desc(sbase + L::oStat + (is_s ? 0 : L::kStat), 16, 1024);
-      const uint64_t da0 = sw128_desc(sbase + (is_s ? L::oX : L::oY), 16, 1024);
-      const uint32_t stride = (is_s ? L::kXStride : L::kYStride) >> 4;
-      const uint32_t ns = is_s ? L::kXStages : L::kYStages;
-      const int full = is_s ? Q_XFULL : Q_YFULL;
+      const uint64_t da0 = sw128_desc(sbase, 16, 1024);
       const uint32_t td = tmem + (is_s ? 0 : 64);
       uint32_t g = 0;
       bool ok = true;
@@ -394,19 +400,20 @@ __global__ void __launch_bounds__(kBThreads, 1)
         if (end) break;
         if (!(ok = wait_bar(bar(Q_STATFULL), it & 1, abort_flag, gerr, prm.wait_ns))) break;
         for (int j = 0; j < npairs; ++j, ++g) {
-          const uint32_t st = g % ns, b = g & 1;
-          if (!(ok = wait_bar(bar(full + int(st)), (g / ns) & 1, abort_flag, gerr, prm.wait_ns))) break;
+          const uint32_t b = g & 1;
+          const SlotUse u = slot_of<D, KEY>(g, is_s);
+          if (!(ok = wait_bar(bar(Q_FULL + int(u.slot)), u.use & 1, abort_flag, gerr, prm.wait_ns))) break;
           // the buffer's previous pair has been read
-          if (g >= 2 && !(ok = wait_bar(bar(Q_PREADY + int(b)), ((g >> 1) - 1) & 1, abort_flag, gerr, prm.wait_ns))) break;
+          if (!(ok = wait_bar(bar(Q_SFREE + int(b)), ((g >> 1) & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
           tc_fence_after();
-          const uint64_t da = da0 + st * stride;
+          const uint64_t da = da0 + u.slot * (L::kTensor >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             tc_mma(td + b * 128, da + (((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4),
                    db + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
           tc_commit(bar(Q_SFULL + int(b)));
           if constexpr (!KEY && D == 128) {
-            if (!is_s) tc_commit(bar(Q_YEMPTY + int(st)));   // dP is the query pass's only use of Y
+            if (!is_s) tc_commit(bar(Q_EMPTY + int(u.slot)));   // dP is the query pass's only use of Y
           }
         }
         if (ok) tc_commit(bar(Q_STATEMPTY));
@@ -424,12 +431,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
       // operand of 128 channels, [Y; X]: dV^T is in lanes 0-63 of acc0, dK^T / dQ^T in
       // lanes 64-127 of acc1, and the other halves are not used (Y's stage is then read
       // here too, so its release counts this product).
-      const uint64_t da0 = sw128_desc(sbase + (is1 && D == 128 ? L::oX : L::oY), L::kHalf, 1024);
-      const uint32_t stride = (is1 ? L::kXStride : L::kYStride) >> 4;
-      const uint32_t ns = is1 ? L::kXStages : L::kYStages;
-      const uint64_t db0 = sw128_desc(sbase + (is1 ? L::oDs : L::oP), 8192, 1024);
+      const bool a_is_x = is1 && D == 128;
+      const uint64_t da0 = sw128_desc(sbase, L::kHalf, 1024);
+      const uint64_t db = sw128_desc(sbase + (is1 ? L::oDs : L::oP), 8192, 1024);
       const uint32_t td = tmem + (is1 ? 320 : 256);
-      const int full = is1 ? Q_XFULL : Q_YFULL;
       uint32_t g = 0;
       bool ok = true;
       for (uint32_t it = 0; ok; ++it) {
@@ -442,17 +447,17 @@ __global__ void __launch_bounds__(kBThreads, 1)
         // the accumulators are free once the previous item's gradients are read
         if (!(ok = wait_bar(bar(Q_ACCFREE), (it & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
         for (int j = 0; j < npairs; ++j, ++g) {
-          const uint32_t st = g % ns, b = g & 1;
-          if (!(ok = wait_bar(bar(full + int(st)), (g / ns) & 1, abort_flag, gerr, prm.wait_ns))) break;
-          if (!(ok = wait_bar(bar(Q_PREADY + int(b)), (g >> 1) & 1, abort_flag, gerr, prm.wait_ns))) break;
+          const SlotUse u = slot_of<D, KEY>(g, a_is_x);
+          if (!(ok = wait_bar(bar(Q_FULL + int(u.slot)), u.use & 1, abort_flag, gerr, prm.wait_ns))) break;
+          if (!(ok = wait_bar(bar(Q_PREADY), g & 1, abort_flag, gerr, prm.wait_ns))) break;
           tc_fence_after();
-          const uint64_t da = da0 + st * stride, db = db0 + b * (L::kPd >> 4);
+          const uint64_t da = da0 + u.slot * (L::kTensor >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)         // 16 streamed rows per step
             tc_mma(td, da + ((kk * 2048) >> 4), db + ((kk * 2048) >> 4), idA, (j > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(bar((is1 ? Q_DSFREE : Q_PFREE) + int(b)));
-          if (is1 || D == 64) tc_commit(bar(Q_XEMPTY + int(st)));
-          if ((!is1 && KEY) || (is1 && D == 64)) tc_commit(bar(Q_YEMPTY + int(st)));
+          tc_commit(bar(Q_PFREE));
+          tc_commit(bar(Q_EMPTY + int(u.slot)));
+          if (D == 64) tc_commit(bar(Q_EMPTY + int(u.slot) + 1));   // X of [Y; X]
         }
         if (ok) tc_commit(bar(Q_ACCFULL));
       }
@@ -466,7 +471,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const int q4 = warp & 3;                     // TMEM lane quarter this warp may read
     const int r = q4 * 32 + lane;                // streamed row, TMEM lane
     const uint32_t lane_off = uint32_t(q4 * 32) << 16;
-    float* col = reinterpret_cast<float*>(smem + L::oCol) + wg * 128;   // query pass: -lse2 [64], -delta [64]
+    const int c0 = 32 * wg;                      // my warpgroup's 32 of the stationary tile's 64 rows
+    float* cols = reinterpret_cast<float*>(smem + L::oCol);   // query pass: -lse2 [64], -delta [64] of two items
     const uint64_t c2 = f2pack(prm.scale_log2, prm.scale_log2);
     uint32_t g = 0;
     bool ok = true;
@@ -480,17 +486,20 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const int h = inf.bh % prm.heads;
       const int64_t base = int64_t(inf.bh) * prm.nt_max;
       if constexpr (!KEY) {
-        // this warpgroup's copy of the stationary queries' lse2 and delta; its warps meet
-        // before the write (the previous item's reads) and after it
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
-        const int x = (warp - 4 - 4 * wg) * 32 + lane;
-        col[x] = -(x < 64 ? prm.lse2[(base + inf.tile) * 64 + x] : prm.delta[(base + inf.tile) * 64 + x - 64]);
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+        // the stationary queries' lse2 and delta, negated, in this item's buffer: every warp has
+        // read what it held two items ago before it arrived for the last item
+        float* col = cols + slot * 128;
+        if (warp < 8) {
+          const int x = (warp - 4) * 32 + lane;
+          col[x] = -(x < 64 ? prm.lse2[(base + inf.tile) * 64 + x] : prm.delta[(base + inf.tile) * 64 + x - 64]);
+        }
+        warp_arrive(bar(Q_COLS));
+        ok = wait_bar(bar(Q_COLS), it & 1, abort_flag, gerr, prm.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) break;
       }
       for (int j = 0; j < inf.pairs; ++j, ++g) {
-        if (int(g & 1) != wg) continue;
-        const uint32_t st = g % L::kXStages;
-        ok = wait_bar(bar(Q_XFULL + int(st)), (g / L::kXStages) & 1, abort_flag, gerr, prm.wait_ns);
+        const SlotUse u = slot_of<D, KEY>(g, true);
+        ok = wait_bar(bar(Q_FULL + int(u.slot)), u.use & 1, abort_flag, gerr, prm.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         const BwdPair pr = pairs[g & 3];
         const int tile = r < 64 ? pr.ta : pr.tb;
@@ -506,60 +515,55 @@ __global__ void __launch_bounds__(kBThreads, 1)
         } else {
           live = tile >= 0 && (r & 63) < prm.counts[int64_t(h) * prm.nt_max + tile];
         }
-        // the buffers' previous pair has been consumed by its products
-        if (g >= 2) {
-          ok = wait_bar(bar(Q_DSFREE + wg), ((g >> 1) - 1) & 1, abort_flag, gerr, prm.wait_ns);
-          if (KEY && ok) ok = wait_bar(bar(Q_PFREE + wg), ((g >> 1) - 1) & 1, abort_flag, gerr, prm.wait_ns);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        }
-        ok = wait_bar(bar(Q_SFULL + wg), (g >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+        const int b = int(g & 1);
+        ok = wait_bar(bar(Q_SFULL + b), (g >> 1) & 1, abort_flag, gerr, prm.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t tS = tmem + wg * 128 + lane_off;
-        // row r, 64 columns: 128 bytes, 16-byte chunks swizzled by the row
-        uint8_t* drow = smem + L::oDs + wg * L::kPd + r * 128;
-        uint8_t* prow = smem + L::oP + wg * L::kPd + r * 128;
-        const uint64_t rl2 = f2pack(rl, rl), rd2 = f2pack(rd, rd);
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t s[32], dp[32];
-          tmem_ld32(tS + c, s);
-          tmem_ld32(tS + 64 + c, dp);
-          tmem_wait_ld(s);
-          reg_fence(dp);
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint32_t pk[4], dk[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int n = i + 2 * e;
-              uint64_t l2 = rl2, dl = rd2;
-              if constexpr (!KEY) {
-                l2 = *reinterpret_cast<const uint64_t*>(col + c + n);
-                dl = *reinterpret_cast<const uint64_t*>(col + 64 + c + n);
-              }
-              float x0, x1, d0, d1;
-              f2unpack(ffma2(f2pack(__uint_as_float(s[n]), __uint_as_float(s[n + 1])), c2, l2), x0, x1);
-              x0 = ex2(x0);
-              x1 = ex2(x1);
-              if constexpr (!KEY) {
-                x0 = live ? x0 : 0.f;
-                x1 = live ? x1 : 0.f;
-              }
-              f2unpack(fmul2(f2pack(x0, x1),
-                             fadd2(f2pack(__uint_as_float(dp[n]), __uint_as_float(dp[n + 1])), dl)),
-                       d0, d1);
-              pk[e] = bf16x2(x0, x1);
-              dk[e] = bf16x2(d0, d1);
-            }
-            const int at = (((c + i) >> 3) ^ (r & 7)) * 16;
-            *reinterpret_cast<uint4*>(drow + at) = make_uint4(dk[0], dk[1], dk[2], dk[3]);
-            if constexpr (KEY) *reinterpret_cast<uint4*>(prow + at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          }
-        }
+        uint32_t s[32], dp[32];
+        tmem_ld32(tmem + b * 128 + lane_off + c0, s);
+        tmem_ld32(tmem + b * 128 + 64 + lane_off + c0, dp);
+        tmem_wait_ld(s);
+        reg_fence(dp);
         tc_fence_before();
+        warp_arrive(bar(Q_SFREE + b));
+        const uint64_t rl2 = f2pack(rl, rl), rd2 = f2pack(rd, rd);
+        uint32_t pk[KEY ? 16 : 1], dk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          uint64_t l2 = rl2, dl = rd2;
+          if constexpr (!KEY) {
+            l2 = *reinterpret_cast<const uint64_t*>(cols + slot * 128 + c0 + 2 * e);
+            dl = *reinterpret_cast<const uint64_t*>(cols + slot * 128 + 64 + c0 + 2 * e);
+          }
+          float x0, x1, d0, d1;
+          f2unpack(ffma2(f2pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, l2), x0, x1);
+          x0 = ex2(x0);
+          x1 = ex2(x1);
+          if constexpr (!KEY) {
+            x0 = live ? x0 : 0.f;
+            x1 = live ? x1 : 0.f;
+          }
+          f2unpack(fmul2(f2pack(x0, x1),
+                         fadd2(f2pack(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), dl)),
+                   d0, d1);
+          if constexpr (KEY) pk[e] = bf16x2(x0, x1);
+          dk[e] = bf16x2(d0, d1);
+        }
+        // the previous pair's P and dS have been consumed by its products
+        ok = wait_bar(bar(Q_PFREE), (g & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        // row r: 128 bytes, 16-byte chunks swizzled by the row; my warpgroup's four
+        uint8_t* drow = smem + L::oDs + r * 128;
+        uint8_t* prow = smem + L::oP + r * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = ((4 * wg + i) ^ (r & 7)) * 16;
+          *reinterpret_cast<uint4*>(drow + at) = make_uint4(dk[4 * i], dk[4 * i + 1], dk[4 * i + 2], dk[4 * i + 3]);
+          if constexpr (KEY)
+            *reinterpret_cast<uint4*>(prow + at) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        warp_arrive(bar(Q_PREADY + wg));
+        warp_arrive(bar(Q_PREADY));
       }
       if (!ok) break;
       // the finished gradients: lanes = channels, columns = the tile's rows. Key pass:
@@ -572,17 +576,15 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const bool mine = ch >= 0 && ch < D;
       __nv_bfloat16* out = (is_v ? prm.out0 : prm.out1) + (base + inf.tile) * 64 * D + (mine ? ch : 0);
       const float f = is_v ? 1.f : prm.scale;
-      constexpr int kCols = KEY ? 64 : 32;
-      const int c0 = KEY ? 0 : 32 * wg;
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 32) {
+      for (int c = KEY ? 0 : c0; c < (KEY ? 64 : c0 + 32); c += 32) {
         uint32_t v[32];
-        tmem_ld32(tmem + (is_v ? 256 : 320) + lane_off + c0 + c, v);
+        tmem_ld32(tmem + (is_v ? 256 : 320) + lane_off + c, v);
         tmem_wait_ld(v);
         if (mine) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int row = c0 + c + i;
+            const int row = c + i;
             const float x = (row < inf.count && inf.pairs > 0) ? __uint_as_float(v[i]) * f : 0.f;
             out[int64_t(row) * D] = __float2bfloat16_rn(x);
           }
