@@ -79,32 +79,76 @@ __device__ __forceinline__ uint4 to_bf16x8(const float (&v)[8]) {
   return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
 }
 
-// Eight columns of one row: v holds the accumulator.
-__device__ __forceinline__ void store8(const Epilogue& e, int64_t row, int col, float (&v)[8]) {
-  if (e.bias) {
-    float b[8];
-    load8(e.bias + col, b);
+// Eight columns of one row: v holds the accumulator, b the columns' bias.
+__device__ __forceinline__ void store8(const Epilogue& e, int64_t row, int col, float (&v)[8], const float (&b)[8]) {
+  // the loads first: they do not wait for the arithmetic
+  uint4 res = make_uint4(0, 0, 0, 0);
+  float g[8];
+  if (e.residual) res = __ldcs(reinterpret_cast<const uint4*>(e.residual + row * e.ld_res + col));
+  if (e.gate) load8(e.gate + (row / e.rows_per_gate) * e.ld_gate + col, g);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
+  for (int i = 0; i < 8; ++i) v[i] += b[i];
   if (e.pre) *reinterpret_cast<uint4*>(e.pre + row * e.ld_pre + col) = to_bf16x8(v);
   if (e.act != VSA_ACT_NONE) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = act_fwd(v[i], e.act);
   }
   if (e.gate) {
-    float g[8];
-    load8(e.gate + (row / e.rows_per_gate) * e.ld_gate + col, g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= g[i];
   }
   if (e.residual) {
     float r[8];
-    bf16x8_to_f32(*reinterpret_cast<const uint4*>(e.residual + row * e.ld_res + col), r);
+    bf16x8_to_f32(res, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += r[i];
   }
   *reinterpret_cast<uint4*>(e.out + row * e.ld_out + col) = to_bf16x8(v);
+}
+__device__ __forceinline__ void load_bias(const Epilogue& e, int col, float (&b)[8]) {
+  if (e.bias) {
+    load8(e.bias + col, b);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = 0.f;
+  }
+}
+
+// 32 rows by 32 columns of an accumulator, from one warp's TMEM lanes (lane =
+// row; r: this lane's 32 columns) to the output: through 4 KB of shared memory,
+// so that four lanes share a row and every global access moves 64 bytes of a row
+// instead of 16. The 16-byte chunks of a staged row are swizzled by the row, which
+// keeps both sides free of bank conflicts. partial: fp32 results instead.
+__device__ __forceinline__ void store_chunk(const Epilogue& e, float* partial, int64_t M, int N, int64_t row0, int col0,
+                                            const uint32_t (&r)[32], uint8_t* stage, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) * 16)) =
+        make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+  __syncwarp();
+  const int c8 = lane & 3;                       // my eight columns
+  const int col = col0 + 8 * c8;
+  if (col < N) {                                 // N is a multiple of eight
+    float b[8];
+    if (!partial) load_bias(e, col, b);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int rr = it * 8 + (lane >> 2);
+      const int64_t row = row0 + rr;
+      if (row >= M) continue;
+      const float4 lo = *reinterpret_cast<const float4*>(stage + rr * 128 + (((2 * c8) ^ (rr & 7)) * 16));
+      const float4 hi = *reinterpret_cast<const float4*>(stage + rr * 128 + (((2 * c8 + 1) ^ (rr & 7)) * 16));
+      if (partial) {
+        float4* dst = reinterpret_cast<float4*>(partial + row * N + col);
+        dst[0] = lo;
+        dst[1] = hi;
+      } else {
+        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        store8(e, row, col, v, b);
+      }
+    }
+  }
+  __syncwarp();                                  // the stage is rewritten for the next chunk
 }
 
 // --------------------------------------------------------------- product ----
@@ -126,7 +170,8 @@ struct GSmem {
   static constexpr uint32_t kB = BN * 128;
   static constexpr uint32_t kStage = kA + kB;
   static constexpr int kStages = BN == 256 ? 4 : 6;
-  static constexpr uint32_t oBar = kStages * kStage;
+  static constexpr uint32_t oOut = kStages * kStage;           // the epilogue warps' 4 KB each
+  static constexpr uint32_t oBar = oOut + 4 * 4096;
   static constexpr uint32_t oMisc = oBar + 24 * 8;
   static constexpr uint32_t oEnd = oMisc + 16;
 };
@@ -259,8 +304,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
       const bool ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const int64_t row = int64_t(t.m) * 128 + q4 * 32 + lane;
-      const bool in = row < prm.M;
+      const int64_t row0 = int64_t(t.m) * 128 + q4 * 32;
+      float* partial = prm.splits > 1 ? prm.partial + int64_t(t.split) * prm.M * prm.N : nullptr;
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
         uint32_t r[32];
@@ -270,22 +315,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
           tc_fence_before();
           warp_arrive(bar(G_AEMPTY + ab));
         }
-        if (!in) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = t.n * BN + c + 8 * j;  // N is a multiple of eight
-          if (col >= prm.N) continue;
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
-          if (prm.splits > 1) {
-            float4* dst = reinterpret_cast<float4*>(prm.partial + (int64_t(t.split) * prm.M + row) * prm.N + col);
-            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-          } else {
-            store8(prm.ep, row, col, v);
-          }
-        }
+        store_chunk(prm.ep, partial, prm.M, prm.N, row0, t.n * BN + c, r, smem + L::oOut + q4 * 4096, lane);
       }
     }
   }
@@ -293,6 +323,163 @@ __global__ void __launch_bounds__(kGThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+}
+
+// The same product on CTA pairs: a cluster of two CTAs computes a 256 x 256 tile
+// with cta_group::2 products, each CTA holding its 128 rows of A and its half of
+// the 256 columns of B, so that a k block moves 32 KB into each SM where two
+// single CTAs would move 48 KB for the same work, and one 256 x 256 instruction
+// (128 cycles) is long enough for one issuing thread. The leader (rank 0) issues;
+// loads of both CTAs count on the leader's full barrier, the products' completion
+// arrives in both CTAs. Two 256-column accumulators fill TMEM: a tile's epilogue
+// runs under the next tile's products.
+constexpr int kPThreads = 192;
+constexpr int kPStages = 6;
+struct PSmem {
+  static constexpr uint32_t kA = 128 * 128, kB = 128 * 128, kStage = kA + kB;
+  static constexpr uint32_t oOut = kPStages * kStage;
+  static constexpr uint32_t oBar = oOut + 4 * 4096;
+  static constexpr uint32_t oMisc = oBar + 24 * 8;
+  static constexpr uint32_t oEnd = oMisc + 16;
+};
+
+template <bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
+    gemm_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                     const __grid_constant__ GemmParams prm) {
+  using L = PSmem;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + L::oBar + 8u * uint32_t(i); };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::oMisc);
+  volatile uint32_t* abort_flag = misc + 1;
+  uint32_t* gerr = prm.state;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = int(blockIdx.x >> 1), pairs = int(gridDim.x >> 1);
+  const int units = prm.tiles_m * prm.tiles_n;   // 256 x 256 tiles
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPStages; ++i) {
+      mbar_init(bar(G_FULL + i), 1);
+      mbar_init(bar(G_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(G_AFULL + i), 1);
+      mbar_init(bar(G_AEMPTY + i), 8);           // the epilogue warps of both CTAs
+    }
+    mbar_init(bar(G_DRAIN), 1);
+    misc[1] = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sbase + L::oMisc));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                // the pair's barriers and TMEM are ready
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = pair; u < units && ok; u += pairs) {
+        const Unit t = unit_of(prm, u);
+        const int m0 = t.m * 256 + int(rank) * 128, n0 = t.n * 256 + int(rank) * 128;
+        for (int kb = 0; kb < prm.kblocks; ++kb, ++it) {
+          const int st = int(it % kPStages);
+          if (!(ok = wait_bar(bar(G_EMPTY + st), ((it / kPStages) & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
+          const uint32_t fb = map_to_rank(bar(G_FULL + st), 0);
+          const uint32_t sa = sbase + st * L::kStage, sb = sa + L::kA;
+          if (rank == 0) mbar_expect_tx(bar(G_FULL + st), 2 * L::kStage);
+          if constexpr (A_MN) {
+            tma_load_2d_pair(sa, &ta, m0, kb * 64, fb);
+            tma_load_2d_pair(sa + 8192, &ta, m0 + 64, kb * 64, fb);
+          } else {
+            tma_load_2d_pair(sa, &ta, kb * 64, m0, fb);
+          }
+          if constexpr (B_MN) {
+            tma_load_2d_pair(sb, &tb, n0, kb * 64, fb);
+            tma_load_2d_pair(sb + 8192, &tb, n0 + 64, kb * 64, fb);
+          } else {
+            tma_load_2d_pair(sb, &tb, kb * 64, n0, fb);
+          }
+        }
+      }
+      // every stage is consumed (in both CTAs) before the CTA may end; after an abort the
+      // copies in flight are given time to land
+      if (ok) {
+        for (uint32_t j = it >= uint32_t(kPStages) ? it - kPStages : 0; j < it && ok; ++j)
+          ok = wait_bar(bar(G_EMPTY + int(j % kPStages)), (j / kPStages) & 1, abort_flag, gerr, prm.wait_ns);
+      }
+      if (!ok) {
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16(256, 256, A_MN, B_MN);
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (int u = pair; u < units && ok; u += pairs, ++n) {
+        const int ab = n & 1;
+        if (!(ok = wait_bar(bar(G_AEMPTY + ab), ((n >> 1) & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
+        for (int kb = 0; kb < prm.kblocks; ++kb, ++it) {
+          const int st = int(it % kPStages);
+          if (!(ok = wait_bar(bar(G_FULL + st), (it / kPStages) & 1, abort_flag, gerr, prm.wait_ns))) break;
+          tc_fence_after();
+          const uint32_t sa = sbase + st * L::kStage;
+          const uint64_t da = A_MN ? sw128_desc(sa, 8192, 1024) : sw128_desc(sa, 16, 1024);
+          const uint64_t db = B_MN ? sw128_desc(sa + L::kA, 8192, 1024) : sw128_desc(sa + L::kA, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_pair(tmem + ab * 256, da + ((kk * (A_MN ? 2048 : 32)) >> 4), db + ((kk * (B_MN ? 2048 : 32)) >> 4),
+                        idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          tc_commit_pair(bar(G_EMPTY + st));
+        }
+        if (ok) tc_commit_pair(bar(G_AFULL + ab));
+      }
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar(G_DRAIN))
+                   : "memory");
+      drain_wait(bar(G_DRAIN), 0);
+    }
+    __syncwarp();
+  } else {
+    const int q4 = warp & 3;
+    uint32_t n = 0;
+    for (int u = pair; u < units; u += pairs, ++n) {
+      const Unit t = unit_of(prm, u);
+      const int ab = n & 1;
+      const bool ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const int64_t row0 = int64_t(t.m) * 256 + rank * 128 + q4 * 32;
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tmem + ab * 256 + (uint32_t(q4 * 32) << 16) + c, r);
+        tmem_wait_ld(r);
+        if (c == 224) {                          // the accumulator is read: the leader may use it again
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(bar(G_AEMPTY + ab), 0));
+        }
+        store_chunk(prm.ep, nullptr, prm.M, prm.N, row0, t.n * 256 + c, r, smem + L::oOut + q4 * 4096, lane);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                // neither CTA's shared memory or TMEM is in use any more
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // The splits of K joined in order, then the epilogue: eight columns per thread.
@@ -308,7 +495,9 @@ __global__ void __launch_bounds__(256) split_join_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += t[j];
     }
-    store8(prm.ep, row, col, v);
+    float b[8];
+    load_bias(prm.ep, col, b);
+    store8(prm.ep, row, col, v, b);
   }
 }
 
@@ -414,9 +603,16 @@ inline int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
 constexpr int kBN = 128;
 
+// Pairs of CTAs on 256 x 256 tiles, or single CTAs on 128 x 128 tiles and splits of
+// K: pairs from the point where their tiles fill most of the SMs.
+bool use_pairs(const vsa_plan* p, int64_t M, int64_t N) {
+  return cdiv64(M, 256) * cdiv64(N, 256) * 2 >= p->num_sms * 3 / 4;
+}
+
 // Splits of K: one tile per CTA leaves SMs idle when there are fewer tiles than
 // half the SMs; each split keeps at least four k blocks of work.
 int choose_splits(const vsa_plan* p, int64_t M, int64_t N, int64_t K) {
+  if (use_pairs(p, M, N)) return 1;
   const int64_t tiles = cdiv64(M, 128) * cdiv64(N, kBN), kb = cdiv64(K, 64);
   if (tiles * 2 > p->num_sms) return 1;
   int64_t s = p->num_sms / tiles;
@@ -442,9 +638,11 @@ template <bool A_MN, bool B_MN>
 cudaError_t run_gemm(const vsa_plan* p, const void* a, int64_t ld_a, const void* b, int64_t ld_b, int64_t M, int64_t N,
                      int64_t K, const Epilogue& ep, void* partial, cudaStream_t s) {
   using L = GSmem<kBN>;
+  const bool pairs = use_pairs(p, M, N);
+  const int bn = pairs ? 128 : kBN;              // rows of B one CTA loads
   CUtensorMap ta, tb;
   const bool ma = A_MN ? make_map2(&ta, a, K, M, ld_a, 64, 64) : make_map2(&ta, a, M, K, ld_a, 64, 128);
-  const bool mb = B_MN ? make_map2(&tb, b, K, N, ld_b, 64, 64) : make_map2(&tb, b, N, K, ld_b, 64, kBN);
+  const bool mb = B_MN ? make_map2(&tb, b, K, N, ld_b, 64, 64) : make_map2(&tb, b, N, K, ld_b, 64, bn);
   if (!ma || !mb) return cudaErrorInvalidValue;
   GemmParams prm;
   prm.ep = ep;
@@ -454,10 +652,19 @@ cudaError_t run_gemm(const vsa_plan* p, const void* a, int64_t ld_a, const void*
   prm.M = int32_t(M);
   prm.N = int32_t(N);
   prm.kblocks = int32_t(cdiv64(K, 64));
-  prm.tiles_m = int32_t(cdiv64(M, 128));
-  prm.tiles_n = int32_t(cdiv64(N, kBN));
+  prm.tiles_m = int32_t(cdiv64(M, pairs ? 256 : 128));
+  prm.tiles_n = int32_t(cdiv64(N, pairs ? 256 : kBN));
   prm.splits = choose_splits(p, M, N, K);
   const int64_t units = int64_t(prm.tiles_m) * prm.tiles_n * prm.splits;
+  if (pairs) {
+    const int smem = 1024 + int(PSmem::oEnd);
+    const cudaError_t e =
+        cudaFuncSetAttribute(gemm_pair_kernel<A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t most = p->num_sms / 2;
+    gemm_pair_kernel<A_MN, B_MN><<<2 * unsigned(units < most ? units : most), kPThreads, smem, s>>>(ta, tb, prm);
+    return cudaGetLastError();
+  }
   const int grid = int(units < p->num_sms ? units : p->num_sms);
   const int smem = 1024 + int(L::oEnd);
   cudaError_t e = cudaFuncSetAttribute(gemm_kernel<kBN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
