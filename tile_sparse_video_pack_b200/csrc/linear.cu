@@ -153,7 +153,9 @@ __device__ __forceinline__ void store_chunk(const Epilogue& e, float* partial, i
 
 // --------------------------------------------------------------- product ----
 
-constexpr int kGThreads = 192;   // warp 0 producer, warp 1 MMA, warps 2-5 epilogue
+constexpr int kGThreads = 320;   // warp 0 producer, warp 1 MMA, warps 2-9 epilogue
+constexpr int kEWarps = 8;       // two per TMEM lane quarter, half of the columns each: a GELU's chain of
+                                 // dependent steps leaves one warp per scheduler idle most of the time
 
 struct GemmParams {
   Epilogue ep;
@@ -171,7 +173,7 @@ struct GSmem {
   static constexpr uint32_t kStage = kA + kB;
   static constexpr int kStages = BN == 256 ? 4 : 6;
   static constexpr uint32_t oOut = kStages * kStage;           // the epilogue warps' 4 KB each
-  static constexpr uint32_t oBar = oOut + 4 * 4096;
+  static constexpr uint32_t oBar = oOut + kEWarps * 4096;
   static constexpr uint32_t oMisc = oBar + 24 * 8;
   static constexpr uint32_t oEnd = oMisc + 16;
 };
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(G_AFULL + i), 1);
-      mbar_init(bar(G_AEMPTY + i), 4);           // one arrival per epilogue warp
+      mbar_init(bar(G_AEMPTY + i), kEWarps);     // one arrival per epilogue warp
     }
     mbar_init(bar(G_DRAIN), 1);
     misc[1] = 0u;
@@ -296,7 +298,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
     }
     __syncwarp();
   } else {
-    const int q4 = warp & 3;
+    const int q4 = warp & 3, c0 = ((warp - 2) >> 2) * (BN / 2);   // my lanes and columns
+    uint8_t* stage = smem + L::oOut + (warp - 2) * 4096;
     uint32_t n = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++n) {
       const Unit t = unit_of(prm, u);
@@ -307,15 +310,15 @@ __global__ void __launch_bounds__(kGThreads, 1)
       const int64_t row0 = int64_t(t.m) * 128 + q4 * 32;
       float* partial = prm.splits > 1 ? prm.partial + int64_t(t.split) * prm.M * prm.N : nullptr;
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
+      for (int c = c0; c < c0 + BN / 2; c += 32) {
         uint32_t r[32];
         tmem_ld32(tmem + ab * BN + (uint32_t(q4 * 32) << 16) + c, r);
         tmem_wait_ld(r);
-        if (c + 32 >= BN) {                      // the accumulator is read: the next tile may use it
+        if (c + 32 >= c0 + BN / 2) {             // the accumulator is read: the next tile may use it
           tc_fence_before();
           warp_arrive(bar(G_AEMPTY + ab));
         }
-        store_chunk(prm.ep, partial, prm.M, prm.N, row0, t.n * BN + c, r, smem + L::oOut + q4 * 4096, lane);
+        store_chunk(prm.ep, partial, prm.M, prm.N, row0, t.n * BN + c, r, stage, lane);
       }
     }
   }
@@ -333,18 +336,17 @@ __global__ void __launch_bounds__(kGThreads, 1)
 // loads of both CTAs count on the leader's full barrier, the products' completion
 // arrives in both CTAs. Two 256-column accumulators fill TMEM: a tile's epilogue
 // runs under the next tile's products.
-constexpr int kPThreads = 192;
 constexpr int kPStages = 6;
 struct PSmem {
   static constexpr uint32_t kA = 128 * 128, kB = 128 * 128, kStage = kA + kB;
   static constexpr uint32_t oOut = kPStages * kStage;
-  static constexpr uint32_t oBar = oOut + 4 * 4096;
+  static constexpr uint32_t oBar = oOut + kEWarps * 4096;
   static constexpr uint32_t oMisc = oBar + 24 * 8;
   static constexpr uint32_t oEnd = oMisc + 16;
 };
 
 template <bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                      const __grid_constant__ GemmParams prm) {
   using L = PSmem;
@@ -367,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(G_AFULL + i), 1);
-      mbar_init(bar(G_AEMPTY + i), 8);           // the epilogue warps of both CTAs
+      mbar_init(bar(G_AEMPTY + i), 2 * kEWarps); // the epilogue warps of both CTAs
     }
     mbar_init(bar(G_DRAIN), 1);
     misc[1] = 0u;
@@ -452,7 +454,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     }
     __syncwarp();
   } else {
-    const int q4 = warp & 3;
+    const int q4 = warp & 3, c0 = ((warp - 2) >> 2) * 128;
+    uint8_t* stage = smem + L::oOut + (warp - 2) * 4096;
     uint32_t n = 0;
     for (int u = pair; u < units; u += pairs, ++n) {
       const Unit t = unit_of(prm, u);
@@ -462,16 +465,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       tc_fence_after();
       const int64_t row0 = int64_t(t.m) * 256 + rank * 128 + q4 * 32;
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
+      for (int c = c0; c < c0 + 128; c += 32) {
         uint32_t r[32];
         tmem_ld32(tmem + ab * 256 + (uint32_t(q4 * 32) << 16) + c, r);
         tmem_wait_ld(r);
-        if (c == 224) {                          // the accumulator is read: the leader may use it again
+        if (c == c0 + 96) {                      // the accumulator is read: the leader may use it again
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to_rank(bar(G_AEMPTY + ab), 0));
         }
-        store_chunk(prm.ep, nullptr, prm.M, prm.N, row0, t.n * 256 + c, r, smem + L::oOut + q4 * 4096, lane);
+        store_chunk(prm.ep, nullptr, prm.M, prm.N, row0, t.n * 256 + c, r, stage, lane);
       }
     }
   }
@@ -662,7 +665,7 @@ cudaError_t run_gemm(const vsa_plan* p, const void* a, int64_t ld_a, const void*
         cudaFuncSetAttribute(gemm_pair_kernel<A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t most = p->num_sms / 2;
-    gemm_pair_kernel<A_MN, B_MN><<<2 * unsigned(units < most ? units : most), kPThreads, smem, s>>>(ta, tb, prm);
+    gemm_pair_kernel<A_MN, B_MN><<<2 * unsigned(units < most ? units : most), kGThreads, smem, s>>>(ta, tb, prm);
     return cudaGetLastError();
   }
   const int grid = int(units < p->num_sms ? units : p->num_sms);
