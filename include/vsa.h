@@ -525,12 +525,7 @@ typedef struct {
   int64_t ld_pre;
 } vsa_linear_args;
 
-/* Workspace of vsa_linear (backward 0) or vsa_linear_bwd (1) in bytes (0: none
- * is needed); with a gate, rows_per_gate as in the call, else 0. Sizes that the
- * calls refuse are refused. */
-VSA_API vsa_status vsa_linear_workspace(const vsa_plan* plan, int64_t rows, int32_t n_in, int32_t n_out,
-                                        int32_t backward, int64_t rows_per_gate, int64_t* bytes);
-VSA_API vsa_status vsa_linear(vsa_plan* plan, const vsa_linear_args* args, void* workspace, void* stream);
+VSA_API vsa_status vsa_linear(vsa_plan* plan, const vsa_linear_args* args, void* stream);
 
 /* Gradient of vsa_linear (that of the residual is dy itself): with dz = gate *
  * dy * act'(pre), dx = dz w (bf16), dw = dz^T x (bf16), dbias = sum of dz,
@@ -556,6 +551,10 @@ typedef struct {
   float* dbias;
   float* dgate;
 } vsa_linear_grad_args;
+/* Workspace of vsa_linear_bwd in bytes; with a gate, rows_per_gate as in the
+ * call, else 0. Sizes that the call refuses are refused. */
+VSA_API vsa_status vsa_linear_bwd_workspace(const vsa_plan* plan, int64_t rows, int32_t n_in, int32_t n_out,
+                                            int64_t rows_per_gate, int64_t* bytes);
 VSA_API vsa_status vsa_linear_bwd(vsa_plan* plan, const vsa_linear_grad_args* args, void* workspace, void* stream);
 
 /* Bound of every device-side wait of the plan's tcgen05 kernels (attention,

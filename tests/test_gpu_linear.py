@@ -44,7 +44,7 @@ def f64(t):
 
 def workspace(plan, *a, **kw):
     import torch
-    return torch.empty(plan.linear_workspace_bytes(*a, **kw), dtype=torch.uint8, device="cuda")
+    return torch.empty(plan.linear_bwd_workspace_bytes(*a, **kw), dtype=torch.uint8, device="cuda")
 
 
 def check_forward(t, got, pre, act, use):
@@ -71,9 +71,8 @@ def test_forward(plan, M, K, N, act):
     import torch
     t = tensors(M, K, N, M if M < 4 else 1)
     y, pre = torch.full_like(t["residual"], 7), torch.full_like(t["residual"], 7)
-    ws = workspace(plan, M, K, N)
     for use in (dict(bias=False, gate=False, residual=False), dict(bias=True, gate=True, residual=True)):
-        plan.linear(t["x"], t["w"], y, act=act, pre=pre if use["bias"] else None, workspace=ws,
+        plan.linear(t["x"], t["w"], y, act=act, pre=pre if use["bias"] else None,
                     **{k: t[k] if v else None for k, v in use.items()})
         plan.check()
         check_forward(t, y, pre if use["bias"] else None, act, use)
@@ -90,15 +89,14 @@ def test_gate_per_sample_and_views(plan):
     for k, v in wide.items():
         v[:, 8:-16] = t[k]
     x, r = wide["x"][:, 8:-16], wide["residual"][:, 8:-16]
-    ws = workspace(plan, M, K, N)
     use = dict(bias=True, gate=True, residual=True)
-    plan.linear(x, t["w"], r, bias=t["bias"], act="silu", gate=t["gate"], residual=r, workspace=ws)
+    plan.linear(x, t["w"], r, bias=t["bias"], act="silu", gate=t["gate"], residual=r)
     plan.check()
     check_forward(t, r, None, "silu", use)
     assert torch.all(wide["residual"][:, :8] == 5) and torch.all(wide["residual"][:, -16:] == 5)
     y3 = torch.empty(3, 43, N, dtype=torch.bfloat16, device="cuda")      # three-dimensional x and y
     plan.linear(t["x"].view(3, 43, K), t["w"], y3, bias=t["bias"], act="silu", gate=t["gate"],
-                residual=t["residual"].view(3, 43, N), workspace=ws)
+                residual=t["residual"].view(3, 43, N))
     plan.check()
     assert torch.equal(y3.view(M, N), r)
 
@@ -134,7 +132,7 @@ def test_backward(plan, M, K, N, gated, act):
     pre = tensors(M, K, N, S, seed=2)["residual"]
     out = dict(dx=torch.full_like(t["x"], 7), dw=torch.full_like(t["w"], 7), dbias=torch.full_like(t["bias"], 7),
                dgate=torch.full_like(t["gate"], 7) if gated else None)
-    ws = workspace(plan, M, K, N, backward=True, samples=S if gated else 0)
+    ws = workspace(plan, M, K, N, samples=S if gated else 0)
     plan.linear_bwd(t["dy"], t["x"], t["w"], act=act, pre=pre, gate=t["gate"] if gated else None, workspace=ws, **out)
     plan.check()
     check_backward(t, out, act, pre, gated)
@@ -143,20 +141,20 @@ def test_backward(plan, M, K, N, gated, act):
     plan.check()
     for k, v in out.items():
         assert v is None or torch.equal(v, again[k]), k       # the same on every call
-    # each output alone
+    # each output alone (K may be split otherwise, so to the same tolerances and not to the bit)
     for k in ("dx", "dw", "dbias"):
         one = torch.empty_like(out[k])
         plan.linear_bwd(t["dy"], t["x"], t["w"], act=act, pre=pre, gate=t["gate"] if gated else None, workspace=ws,
                         **{k: one})
         plan.check()
-        assert torch.equal(one, out[k]), k
+        check_backward(t, {**out, k: one}, act, pre, gated)
 
 
 def test_no_rows(plan):
     import torch
     t = tensors(1, 64, 128, 1)
     e = lambda n: torch.empty(0, n, dtype=torch.bfloat16, device="cuda")
-    assert plan.linear_workspace_bytes(0, 64, 128) == 0
+    assert plan.linear_bwd_workspace_bytes(0, 64, 128) == 0
     plan.linear(e(64), t["w"], e(128), bias=t["bias"], act="silu")
     dw, db = torch.full_like(t["w"], 7), torch.full_like(t["bias"], 7)
     plan.linear_bwd(e(128), e(64), t["w"], dx=e(64), dw=dw, dbias=db)
@@ -168,20 +166,19 @@ def test_special_values_stay_in_their_rows(plan):
     """A row with an infinity or a NaN spoils its own output row only; large |z| saturates the activation."""
     import torch
     t = tensors(130, 128, 256, 1)
-    ws = workspace(plan, 130, 128, 256)
     y = torch.empty_like(t["residual"])
-    plan.linear(t["x"], t["w"], y, act="gelu_tanh", workspace=ws)
+    plan.linear(t["x"], t["w"], y, act="gelu_tanh")
     base = y.clone()
     t["x"][5, 3] = float("nan")
     t["x"][129, 0] = float("inf")
-    plan.linear(t["x"], t["w"], y, act="gelu_tanh", workspace=ws)
+    plan.linear(t["x"], t["w"], y, act="gelu_tanh")
     plan.check()
     rows = [i for i in range(130) if i not in (5, 129)]
     assert torch.equal(y[rows], base[rows]) and torch.isnan(y[5]).all()
     t = tensors(4, 128, 256, 1)
     t["x"] *= 200
     for act in ("silu", "gelu_tanh"):
-        plan.linear(t["x"], t["w"], y[:4], act=act, workspace=ws)
+        plan.linear(t["x"], t["w"], y[:4], act=act)
         plan.check()
         check_forward(t, y[:4], None, act, dict(bias=False, gate=False, residual=False))
 
@@ -210,7 +207,7 @@ def test_refusals(plan):
     with pytest.raises(T.VsaError):
         plan.linear(t["x"][:, :60].contiguous(), t["w"][:, :60].contiguous(), y)   # n_in not a multiple of 8
     with pytest.raises(T.VsaError):
-        plan.linear_workspace_bytes(-1, 64, 64)
+        plan.linear_bwd_workspace_bytes(-1, 64, 64)
     with pytest.raises(ValueError):
         plan.linear_bwd(t["dy"], t["x"], t["w"], dx=torch.empty_like(t["x"]), act="silu")   # no pre
     with pytest.raises(ValueError):

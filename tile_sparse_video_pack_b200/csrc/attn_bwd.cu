@@ -57,12 +57,6 @@ constexpr int kBThreads = 416;
 constexpr int kWarpS = 1, kWarpDp = 2, kWarpAcc1 = 3, kWarpAcc0 = 12;   // MMA issuers
 constexpr uint32_t kBox = 64 * 64 * 2;           // one 64 x 64 bf16 TMA box
 
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // ------------------------------------------------------------ preparation ----
 
 // Per packed row: log-sum-exp in log2 units, and delta = sum of do * o. Rows of

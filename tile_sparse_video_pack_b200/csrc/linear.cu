@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "tc_sm100.h"
 #include "tile_map.h"
@@ -33,15 +34,30 @@ using namespace tc;
 
 // ------------------------------------------------------------ activation ----
 
-// sigmoid(x) = 1 / (1 + e^-x); e^-x overflows to infinity for x << 0, which gives 0.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
-// gelu_tanh(z) = z (1 + tanh(u)) / 2 = z sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3)
+// gelu_tanh(z) = z (1 + tanh(u)) / 2 = z sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3);
+// sigmoid(x) = 1 / (1 + 2^(-x log2 e)): 2^x overflows to infinity for x << 0, which gives 0.
+// The approximate exponential and reciprocal are within 2^-21 for the arguments that
+// matter, far below the output's rounding to bf16. Two elements at a time in packed fp32.
 constexpr float kGeluB = 1.5957691216057308f;   // 2 sqrt(2/pi)
-__device__ __forceinline__ float act_fwd(float z, int act) {
-  if (act == VSA_ACT_GELU_TANH) return z * sigmoid(kGeluB * z * fmaf(0.044715f * z, z, 1.f));
-  if (act == VSA_ACT_SILU) return z * sigmoid(z);
-  return z;
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void act_fwd(float (&v)[8], int act) {
+  if (act == VSA_ACT_NONE) return;
+  const bool gelu = act == VSA_ACT_GELU_TANH;
+  const float c1 = gelu ? -kGeluB * kLog2e : -kLog2e, c3 = gelu ? -0.044715f * kGeluB * kLog2e : 0.f;
+  const uint64_t c1p = f2pack(c1, c1), c3p = f2pack(c3, c3), one = f2pack(1.f, 1.f);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t z = f2pack(v[i], v[i + 1]);
+    float x0, x1;
+    f2unpack(fmul2(z, ffma2(fmul2(z, z), c3p, c1p)), x0, x1);   // -2u log2 e (SiLU: -z log2 e)
+    f2unpack(fadd2(f2pack(ex2(x0), ex2(x1)), one), x0, x1);
+    f2unpack(fmul2(z, f2pack(rcp(x0), rcp(x1))), v[i], v[i + 1]);
+  }
 }
 // act(z) and act'(z), with the accurate exponential: they go into fp32 sums.
 __device__ __forceinline__ void act_both(float z, int act, float& f, float& df) {
@@ -88,11 +104,8 @@ __device__ __forceinline__ void store8(const Epilogue& e, int64_t row, int col, 
   if (e.gate) load8(e.gate + (row / e.rows_per_gate) * e.ld_gate + col, g);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] += b[i];
-  if (e.pre) *reinterpret_cast<uint4*>(e.pre + row * e.ld_pre + col) = to_bf16x8(v);
-  if (e.act != VSA_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_fwd(v[i], e.act);
-  }
+  if (e.pre) __stcs(reinterpret_cast<uint4*>(e.pre + row * e.ld_pre + col), to_bf16x8(v));
+  act_fwd(v, e.act);
   if (e.gate) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= g[i];
@@ -103,7 +116,7 @@ __device__ __forceinline__ void store8(const Epilogue& e, int64_t row, int col, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += r[i];
   }
-  *reinterpret_cast<uint4*>(e.out + row * e.ld_out + col) = to_bf16x8(v);
+  __stcs(reinterpret_cast<uint4*>(e.out + row * e.ld_out + col), to_bf16x8(v));
 }
 __device__ __forceinline__ void load_bias(const Epilogue& e, int col, float (&b)[8]) {
   if (e.bias) {
@@ -118,8 +131,8 @@ __device__ __forceinline__ void load_bias(const Epilogue& e, int col, float (&b)
 // row; r: this lane's 32 columns) to the output: through 4 KB of shared memory,
 // so that four lanes share a row and every global access moves 64 bytes of a row
 // instead of 16. The 16-byte chunks of a staged row are swizzled by the row, which
-// keeps both sides free of bank conflicts. partial: fp32 results instead.
-__device__ __forceinline__ void store_chunk(const Epilogue& e, float* partial, int64_t M, int N, int64_t row0, int col0,
+// keeps both sides free of bank conflicts.
+__device__ __forceinline__ void store_chunk(const Epilogue& e, int64_t M, int N, int64_t row0, int col0,
                                             const uint32_t (&r)[32], uint8_t* stage, int lane) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -130,7 +143,7 @@ __device__ __forceinline__ void store_chunk(const Epilogue& e, float* partial, i
   const int col = col0 + 8 * c8;
   if (col < N) {                                 // N is a multiple of eight
     float b[8];
-    if (!partial) load_bias(e, col, b);
+    load_bias(e, col, b);
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int rr = it * 8 + (lane >> 2);
@@ -138,14 +151,8 @@ __device__ __forceinline__ void store_chunk(const Epilogue& e, float* partial, i
       if (row >= M) continue;
       const float4 lo = *reinterpret_cast<const float4*>(stage + rr * 128 + (((2 * c8) ^ (rr & 7)) * 16));
       const float4 hi = *reinterpret_cast<const float4*>(stage + rr * 128 + (((2 * c8 + 1) ^ (rr & 7)) * 16));
-      if (partial) {
-        float4* dst = reinterpret_cast<float4*>(partial + row * N + col);
-        dst[0] = lo;
-        dst[1] = hi;
-      } else {
-        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        store8(e, row, col, v, b);
-      }
+      float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      store8(e, row, col, v, b);
     }
   }
   __syncwarp();                                  // the stage is rewritten for the next chunk
@@ -157,21 +164,29 @@ constexpr int kGThreads = 320;   // warp 0 producer, warp 1 MMA, warps 2-9 epilo
 constexpr int kEWarps = 8;       // two per TMEM lane quarter, half of the columns each: a GELU's chain of
                                  // dependent steps leaves one warp per scheduler idle most of the time
 
-struct GemmParams {
+// One product. a_mn / b_mn: that operand is stored [K][M] / [K][N].
+struct Product {
   Epilogue ep;
-  float* partial;          // splits > 1: fp32 [splits][M][N]
+  int32_t M, N, kblocks;   // K in blocks of 64
+  int32_t tiles_m, tiles_n;
+  int32_t a_mn, b_mn;
+};
+struct GemmParams {
+  Product prod[2];
   uint32_t* state;         // [0] error word
   uint64_t wait_ns;
-  int32_t M, N, kblocks;   // K in blocks of 64
-  int32_t tiles_m, tiles_n, splits;
+  int32_t n_prod, units;   // products and the tiles of all of them
+  int32_t splits;          // CTAs of a cluster that share a tile's K
+  int32_t group;           // row tiles per group of the tile order
+};
+struct GemmMaps {
+  CUtensorMap a[2], b[2];
 };
 
-template <int BN>
+constexpr int kBM = 128, kBN = 128;
 struct GSmem {
-  static constexpr uint32_t kA = 128 * 128;        // 128 x 64 bf16
-  static constexpr uint32_t kB = BN * 128;
-  static constexpr uint32_t kStage = kA + kB;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr uint32_t kA = kBM * 128, kB = kBN * 128, kStage = kA + kB;   // 64 of K
+  static constexpr int kStages = 6;
   static constexpr uint32_t oOut = kStages * kStage;           // the epilogue warps' 4 KB each
   static constexpr uint32_t oBar = oOut + kEWarps * 4096;
   static constexpr uint32_t oMisc = oBar + 24 * 8;
@@ -179,31 +194,65 @@ struct GSmem {
 };
 enum { G_FULL = 0, G_EMPTY = 8, G_AFULL = 16, G_AEMPTY = 18, G_DRAIN = 20 };
 
-// The tile and k range of work unit u: the splits of a tile are neighbours, and
-// tiles run down groups of eight row tiles before the next column tile, so that
-// the CTAs at work share operand tiles in L2.
-struct Unit {
-  int m, n, k0, k1, split;
+// Tile u: tiles run down groups of `group` row tiles before the next column tile,
+// so that the CTAs at work share operand tiles in L2.
+struct Tile {
+  int prod, m, n;
 };
-__device__ __forceinline__ Unit unit_of(const GemmParams& p, int u) {
-  Unit r;
-  r.split = u % p.splits;
-  const int t = u / p.splits;
-  const int per_group = 8 * p.tiles_n;
-  const int grp = t / per_group, in = t - grp * per_group;
-  const int rows = min(8, p.tiles_m - grp * 8);
-  r.m = grp * 8 + in % rows;
+__device__ __forceinline__ Tile tile_of(const GemmParams& p, int u) {
+  Tile r;
+  const int first = p.prod[0].tiles_m * p.prod[0].tiles_n;
+  r.prod = u >= first ? 1 : 0;
+  if (r.prod) u -= first;
+  const Product& q = p.prod[r.prod];
+  const int per_group = p.group * q.tiles_n;
+  const int grp = u / per_group, in = u - grp * per_group;
+  const int rows = min(p.group, q.tiles_m - grp * p.group);
+  r.m = grp * p.group + in % rows;
   r.n = in / rows;
-  r.k0 = int(int64_t(p.kblocks) * r.split / p.splits);
-  r.k1 = int(int64_t(p.kblocks) * (r.split + 1) / p.splits);
   return r;
 }
 
-template <int BN, bool A_MN, bool B_MN>
+// Loads of one k block: 128 rows of a K-major operand are one box of 64 of K by
+// 128 rows, of an MN-major one two boxes of 64 columns by 64 of K.
+template <bool PAIR>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, bool mn, int row0, int kb, uint32_t fb) {
+  auto load = [&](uint32_t d, int x, int y) {
+    if (PAIR) tma_load_2d_pair(d, map, x, y, fb);
+    else tma_load_2d(d, map, x, y, fb);
+  };
+  if (mn) {
+    load(dst, row0, kb * 64);
+    load(dst + 8192, row0 + 64, kb * 64);
+  } else {
+    load(dst, kb * 64, row0);
+  }
+}
+// Shared-memory descriptor of an operand's stage and the advance per 16 of K.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
+  return mn ? sw128_desc(addr, 8192, 1024) : sw128_desc(addr, 16, 1024);
+}
+__device__ __forceinline__ uint32_t operand_step(bool mn) { return (mn ? 2048u : 32u) >> 4; }
+
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {   // addr: an address mapped into a CTA of the cluster
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// SPLIT = false: every CTA works through tiles on its own, the epilogue of one tile
+// under the products of the next. SPLIT = true, for problems with few tiles: the
+// `splits` CTAs of a cluster take a share of a tile's K each, leave their fp32
+// accumulators in their own shared memory (the stages, all consumed by then), and
+// each joins 1 / splits of the rows from all of them, in rank order -- one launch,
+// no partial sums in global memory, the same result every time.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kGThreads, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                const __grid_constant__ GemmParams prm) {
-  using L = GSmem<BN>;
+    gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams prm) {
+  using L = GSmem;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -212,8 +261,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
   volatile uint32_t* abort_flag = misc + 1;
   uint32_t* gerr = prm.state;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int units = prm.tiles_m * prm.tiles_n * prm.splits;
-  constexpr uint32_t kCols = 2 * BN;             // two accumulators
+  const int splits = SPLIT ? prm.splits : 1;
+  const int rank = SPLIT ? int(cluster_rank()) : 0;
+  const int u0 = int(blockIdx.x) / splits, du = int(gridDim.x) / splits;
+  constexpr uint32_t kCols = 2 * kBN;            // two accumulators
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
@@ -238,92 +289,114 @@ __global__ void __launch_bounds__(kGThreads, 1)
   tc_fence_after();
   const uint32_t tmem = misc[0];
 
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;                           // k blocks issued
-      bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const Unit t = unit_of(prm, u);
-        for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+  uint32_t it = 0, n = 0;                        // k blocks and tiles so far, counted alike by every role
+  bool ok = true;
+  for (int u = u0; u < prm.units; u += du, ++n) {
+    const Tile t = tile_of(prm, u);
+    const Product& pr = prm.prod[t.prod];
+    const int k0 = int(int64_t(pr.kblocks) * rank / splits), k1 = int(int64_t(pr.kblocks) * (rank + 1) / splits);
+    const int ab = n & 1;
+    if (warp == 0) {
+      if (lane == 0) {
+        const CUtensorMap* ta = &maps.a[t.prod];
+        const CUtensorMap* tb = &maps.b[t.prod];
+        for (int kb = k0; kb < k1 && ok; ++kb, ++it) {
           const int st = int(it % L::kStages);
-          const uint32_t ph = (it / L::kStages) & 1;
-          if (!(ok = wait_bar(bar(G_EMPTY + st), ph ^ 1, abort_flag, gerr, prm.wait_ns))) break;
-          const uint32_t fb = bar(G_FULL + st);
-          const uint32_t sa = sbase + st * L::kStage, sb = sa + L::kA;
-          mbar_expect_tx(fb, L::kStage);
-          if constexpr (A_MN) {                  // 64 columns of M by 64 rows of K per box
-            tma_load_2d(sa, &ta, t.m * 128, kb * 64, fb);
-            tma_load_2d(sa + 8192, &ta, t.m * 128 + 64, kb * 64, fb);
-          } else {                               // 64 columns of K by 128 rows of M
-            tma_load_2d(sa, &ta, kb * 64, t.m * 128, fb);
-          }
-          if constexpr (B_MN) {
-            for (int i = 0; i < BN / 64; ++i) tma_load_2d(sb + 8192 * i, &tb, t.n * BN + 64 * i, kb * 64, fb);
-          } else {
-            tma_load_2d(sb, &tb, kb * 64, t.n * BN, fb);
-          }
+          if (!(ok = wait_bar(bar(G_EMPTY + st), ((it / L::kStages) & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
+          const uint32_t sa = sbase + st * L::kStage;
+          mbar_expect_tx(bar(G_FULL + st), L::kStage);
+          load_operand<false>(sa, ta, pr.a_mn, t.m * kBM, kb, bar(G_FULL + st));
+          load_operand<false>(sa + L::kA, tb, pr.b_mn, t.n * kBN, kb, bar(G_FULL + st));
         }
       }
-      if (*abort_flag)                           // let the copies land before shared memory is released
-        for (uint32_t j = it >= uint32_t(L::kStages) ? it - L::kStages : 0; j < it; ++j)
-          drain_wait(bar(G_FULL + int(j % L::kStages)), (j / L::kStages) & 1);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(128, BN, A_MN, B_MN);
-      uint32_t it = 0, n = 0;                    // k blocks, tiles
-      bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++n) {
-        const Unit t = unit_of(prm, u);
-        const int ab = n & 1;
-        if (!(ok = wait_bar(bar(G_AEMPTY + ab), ((n >> 1) & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
-        for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+      __syncwarp();
+    } else if (warp == 1) {
+      if (lane == 0 && ok) {
+        const uint32_t idesc = idesc_bf16(kBM, kBN, pr.a_mn, pr.b_mn);
+        const uint32_t as = operand_step(pr.a_mn), bs = operand_step(pr.b_mn);
+        ok = wait_bar(bar(G_AEMPTY + ab), ((n >> 1) & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
+        for (int kb = k0; kb < k1 && ok; ++kb, ++it) {
           const int st = int(it % L::kStages);
           if (!(ok = wait_bar(bar(G_FULL + st), (it / L::kStages) & 1, abort_flag, gerr, prm.wait_ns))) break;
           tc_fence_after();
           const uint32_t sa = sbase + st * L::kStage;
-          const uint64_t da = A_MN ? sw128_desc(sa, 8192, 1024) : sw128_desc(sa, 16, 1024);
-          const uint64_t db = B_MN ? sw128_desc(sa + L::kA, 8192, 1024) : sw128_desc(sa + L::kA, 16, 1024);
+          const uint64_t da = operand_desc(sa, pr.a_mn), db = operand_desc(sa + L::kA, pr.b_mn);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)         // 16 of K per instruction
-            tc_mma(tmem + ab * BN, da + ((kk * (A_MN ? 2048 : 32)) >> 4), db + ((kk * (B_MN ? 2048 : 32)) >> 4), idesc,
-                   (kb > t.k0 || kk > 0) ? 1u : 0u);
+            tc_mma(tmem + ab * kBN, da + kk * as, db + kk * bs, idesc, (kb > k0 || kk > 0) ? 1u : 0u);
           tc_commit(bar(G_EMPTY + st));
         }
         if (ok) tc_commit(bar(G_AFULL + ab));
       }
-      tc_commit(bar(G_DRAIN));                   // nothing of ours may run when TMEM is freed
-      drain_wait(bar(G_DRAIN), 0);
-    }
-    __syncwarp();
-  } else {
-    const int q4 = warp & 3, c0 = ((warp - 2) >> 2) * (BN / 2);   // my lanes and columns
-    uint8_t* stage = smem + L::oOut + (warp - 2) * 4096;
-    uint32_t n = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++n) {
-      const Unit t = unit_of(prm, u);
-      const int ab = n & 1;
-      const bool ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      const int64_t row0 = int64_t(t.m) * 128 + q4 * 32;
-      float* partial = prm.splits > 1 ? prm.partial + int64_t(t.split) * prm.M * prm.N : nullptr;
+      __syncwarp();
+    } else if (ok) {
+      const int ew = warp - 2, q4 = warp & 3, c0 = (ew >> 2) * (kBN / 2);   // my lanes and columns
+      ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
 #pragma unroll 1
-      for (int c = c0; c < c0 + BN / 2; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(tmem + ab * BN + (uint32_t(q4 * 32) << 16) + c, r);
-        tmem_wait_ld(r);
-        if (c + 32 >= c0 + BN / 2) {             // the accumulator is read: the next tile may use it
-          tc_fence_before();
-          warp_arrive(bar(G_AEMPTY + ab));
+        for (int c = c0; c < c0 + kBN / 2; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(tmem + ab * kBN + (uint32_t(q4 * 32) << 16) + c, r);
+          tmem_wait_ld(r);
+          if (c + 32 >= c0 + kBN / 2) {          // the accumulator is read: the next tile may use it
+            tc_fence_before();
+            warp_arrive(bar(G_AEMPTY + ab));
+          }
+          if constexpr (SPLIT) {                 // row q4 * 32 + lane of 512 bytes, 16-byte chunks swizzled by the row
+            uint8_t* row = smem + (q4 * 32 + lane) * (kBN * 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(row + (((c >> 2) + i) ^ (lane & 7)) * 16) =
+                  make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          } else {
+            store_chunk(pr.ep, pr.M, pr.N, int64_t(t.m) * kBM + q4 * 32, t.n * kBN + c, r,
+                        smem + L::oOut + ew * 4096, lane);
+          }
         }
-        store_chunk(prm.ep, partial, prm.M, prm.N, row0, t.n * BN + c, r, stage, lane);
       }
     }
+    if constexpr (SPLIT) {
+      cluster_sync();                            // every CTA's accumulator is in its shared memory
+      if (warp >= 2 && ok) {
+        const int r0 = kBM * rank / splits, r1 = kBM * (rank + 1) / splits;
+        const int cg = lane & 15;                // eight columns, sixteen lanes to a row
+        const int col = t.n * kBN + 8 * cg;
+        float b[8];
+        if (col < pr.N) load_bias(pr.ep, col, b);
+        for (int rr = r0 + (warp - 2) * 2 + (lane >> 4); rr < r1; rr += 2 * kEWarps) {
+          const int64_t row = int64_t(t.m) * kBM + rr;
+          if (row >= pr.M || col >= pr.N) continue;
+          const uint32_t lo = sbase + rr * (kBN * 4) + ((2 * cg) ^ (rr & 7)) * 16;
+          const uint32_t hi = sbase + rr * (kBN * 4) + ((2 * cg + 1) ^ (rr & 7)) * 16;
+          float v[8] = {};
+#pragma unroll 4
+          for (int s = 0; s < splits; ++s) {
+            // a CTA whose share of K is empty has no accumulator
+            if (int64_t(pr.kblocks) * s / splits == int64_t(pr.kblocks) * (s + 1) / splits) continue;
+            const float4 x = ld_cluster(map_to_rank(lo, s)), y = ld_cluster(map_to_rank(hi, s));
+            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+          }
+          store8(pr.ep, row, col, v, b);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the stages are loaded again after these accesses
+      cluster_sync();                            // every CTA has read: the shared memory may be reused or released
+    }
   }
+  if (warp == 0 && lane == 0 && *abort_flag)     // let the copies land before shared memory is released
+    for (uint32_t j = it >= uint32_t(L::kStages) ? it - L::kStages : 0; j < it; ++j)
+      drain_wait(bar(G_FULL + int(j % L::kStages)), (j / L::kStages) & 1);
+  if (warp == 1 && lane == 0) {                  // nothing of ours may run when TMEM is freed
+    tc_commit(bar(G_DRAIN));
+    drain_wait(bar(G_DRAIN), 0);
+  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if constexpr (SPLIT) cluster_sync();
   tc_fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
 }
@@ -345,10 +418,8 @@ struct PSmem {
   static constexpr uint32_t oEnd = oMisc + 16;
 };
 
-template <bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
-    gemm_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                     const __grid_constant__ GemmParams prm) {
+    gemm_pair_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams prm) {
   using L = PSmem;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -360,7 +431,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = int(blockIdx.x >> 1), pairs = int(gridDim.x >> 1);
-  const int units = prm.tiles_m * prm.tiles_n;   // 256 x 256 tiles
+  const int units = prm.units;                   // 256 x 256 tiles of one product
+  const Product& pr = prm.prod[0];
+  const bool a_mn = pr.a_mn, b_mn = pr.b_mn;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPStages; ++i) {
@@ -390,26 +463,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int u = pair; u < units && ok; u += pairs) {
-        const Unit t = unit_of(prm, u);
+        const Tile t = tile_of(prm, u);
         const int m0 = t.m * 256 + int(rank) * 128, n0 = t.n * 256 + int(rank) * 128;
-        for (int kb = 0; kb < prm.kblocks; ++kb, ++it) {
+        for (int kb = 0; kb < pr.kblocks; ++kb, ++it) {
           const int st = int(it % kPStages);
           if (!(ok = wait_bar(bar(G_EMPTY + st), ((it / kPStages) & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
           const uint32_t fb = map_to_rank(bar(G_FULL + st), 0);
           const uint32_t sa = sbase + st * L::kStage, sb = sa + L::kA;
           if (rank == 0) mbar_expect_tx(bar(G_FULL + st), 2 * L::kStage);
-          if constexpr (A_MN) {
-            tma_load_2d_pair(sa, &ta, m0, kb * 64, fb);
-            tma_load_2d_pair(sa + 8192, &ta, m0 + 64, kb * 64, fb);
-          } else {
-            tma_load_2d_pair(sa, &ta, kb * 64, m0, fb);
-          }
-          if constexpr (B_MN) {
-            tma_load_2d_pair(sb, &tb, n0, kb * 64, fb);
-            tma_load_2d_pair(sb + 8192, &tb, n0 + 64, kb * 64, fb);
-          } else {
-            tma_load_2d_pair(sb, &tb, kb * 64, n0, fb);
-          }
+          load_operand<true>(sa, &maps.a[0], a_mn, m0, kb, fb);
+          load_operand<true>(sb, &maps.b[0], b_mn, n0, kb, fb);
         }
       }
       // every stage is consumed (in both CTAs) before the CTA may end; after an abort the
@@ -427,23 +490,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16(256, 256, A_MN, B_MN);
+      const uint32_t idesc = idesc_bf16(256, 256, a_mn, b_mn);
+      const uint32_t as = operand_step(a_mn), bs = operand_step(b_mn);
       uint32_t it = 0, n = 0;
       bool ok = true;
       for (int u = pair; u < units && ok; u += pairs, ++n) {
         const int ab = n & 1;
         if (!(ok = wait_bar(bar(G_AEMPTY + ab), ((n >> 1) & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
-        for (int kb = 0; kb < prm.kblocks; ++kb, ++it) {
+        for (int kb = 0; kb < pr.kblocks; ++kb, ++it) {
           const int st = int(it % kPStages);
           if (!(ok = wait_bar(bar(G_FULL + st), (it / kPStages) & 1, abort_flag, gerr, prm.wait_ns))) break;
           tc_fence_after();
           const uint32_t sa = sbase + st * L::kStage;
-          const uint64_t da = A_MN ? sw128_desc(sa, 8192, 1024) : sw128_desc(sa, 16, 1024);
-          const uint64_t db = B_MN ? sw128_desc(sa + L::kA, 8192, 1024) : sw128_desc(sa + L::kA, 16, 1024);
+          const uint64_t da = operand_desc(sa, a_mn), db = operand_desc(sa + L::kA, b_mn);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_pair(tmem + ab * 256, da + ((kk * (A_MN ? 2048 : 32)) >> 4), db + ((kk * (B_MN ? 2048 : 32)) >> 4),
-                        idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+            tc_mma_pair(tmem + ab * 256, da + kk * as, db + kk * bs, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
           tc_commit_pair(bar(G_EMPTY + st));
         }
         if (ok) tc_commit_pair(bar(G_AFULL + ab));
@@ -458,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     uint8_t* stage = smem + L::oOut + (warp - 2) * 4096;
     uint32_t n = 0;
     for (int u = pair; u < units; u += pairs, ++n) {
-      const Unit t = unit_of(prm, u);
+      const Tile t = tile_of(prm, u);
       const int ab = n & 1;
       const bool ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -474,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to_rank(bar(G_AEMPTY + ab), 0));
         }
-        store_chunk(prm.ep, nullptr, prm.M, prm.N, row0, t.n * 256 + c, r, stage, lane);
+        store_chunk(pr.ep, pr.M, pr.N, row0, t.n * 256 + c, r, stage, lane);
       }
     }
   }
@@ -483,25 +545,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   cluster_sync();                                // neither CTA's shared memory or TMEM is in use any more
   tc_fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-}
-
-// The splits of K joined in order, then the epilogue: eight columns per thread.
-__global__ void __launch_bounds__(256) split_join_kernel(const __grid_constant__ GemmParams prm) {
-  const int64_t per_row = prm.N / 8, total = int64_t(prm.M) * per_row;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-    const int64_t row = i / per_row;
-    const int col = int(i - row * per_row) * 8;
-    float v[8] = {};
-    for (int s = 0; s < prm.splits; ++s) {
-      float t[8];
-      load8(prm.partial + (int64_t(s) * prm.M + row) * prm.N + col, t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += t[j];
-    }
-    float b[8];
-    load_bias(prm.ep, col, b);
-    store8(prm.ep, row, col, v, b);
-  }
 }
 
 // ----------------------------------------------------- gradient of the rest ----
@@ -604,29 +647,9 @@ __global__ void __launch_bounds__(256) linear_colsum_kernel(const float* __restr
 inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
-constexpr int kBN = 128;
-
-// Pairs of CTAs on 256 x 256 tiles, or single CTAs on 128 x 128 tiles and splits of
-// K: pairs from the point where their tiles fill most of the SMs.
-bool use_pairs(const vsa_plan* p, int64_t M, int64_t N) {
-  return cdiv64(M, 256) * cdiv64(N, 256) * 2 >= p->num_sms * 3 / 4;
-}
-
-// Splits of K: one tile per CTA leaves SMs idle when there are fewer tiles than
-// half the SMs; each split keeps at least four k blocks of work.
-int choose_splits(const vsa_plan* p, int64_t M, int64_t N, int64_t K) {
-  if (use_pairs(p, M, N)) return 1;
-  const int64_t tiles = cdiv64(M, 128) * cdiv64(N, kBN), kb = cdiv64(K, 64);
-  if (tiles * 2 > p->num_sms) return 1;
-  int64_t s = p->num_sms / tiles;
-  if (s > kb / 4) s = kb / 4;
-  if (s > 32) s = 32;
-  return int(s < 1 ? 1 : s);
-}
-int64_t split_bytes(const vsa_plan* p, int64_t M, int64_t N, int64_t K) {
-  const int s = choose_splits(p, M, N, K);
-  return s > 1 ? round256(int64_t(s) * M * N * 4) : 0;
-}
+// Row tiles per group of the tile order. At 18,944 x 2048 -> 8192 groups of 8 read
+// 392 MB from DRAM and groups of 16 234 MB (operands: 111 MB), in the same time.
+constexpr int kGroup = 16;
 
 // A 2-D bf16 tensor map, columns innermost, `ld` elements per row.
 bool make_map2(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols, int box_rows) {
@@ -636,48 +659,98 @@ bool make_map2(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int
   return make_map_nd(m, base, 2, dims, strides, box);
 }
 
-// D[M, N] = A B^T over K. A: [M, K] (K-major) or [K, M] (a_mn), B likewise.
-template <bool A_MN, bool B_MN>
-cudaError_t run_gemm(const vsa_plan* p, const void* a, int64_t ld_a, const void* b, int64_t ld_b, int64_t M, int64_t N,
-                     int64_t K, const Epilogue& ep, void* partial, cudaStream_t s) {
-  using L = GSmem<kBN>;
-  const bool pairs = use_pairs(p, M, N);
-  const int bn = pairs ? 128 : kBN;              // rows of B one CTA loads
-  CUtensorMap ta, tb;
-  const bool ma = A_MN ? make_map2(&ta, a, K, M, ld_a, 64, 64) : make_map2(&ta, a, M, K, ld_a, 64, 128);
-  const bool mb = B_MN ? make_map2(&tb, b, K, N, ld_b, 64, 64) : make_map2(&tb, b, N, K, ld_b, 64, bn);
-  if (!ma || !mb) return cudaErrorInvalidValue;
+// D[M, N] = A B^T over K. a: [M, K], or [K, M] with a_mn; b: [N, K], or [K, N] with b_mn.
+struct Problem {
+  const void *a, *b;
+  int64_t ld_a, ld_b, M, N, K;
+  bool a_mn, b_mn;
+  Epilogue ep;
+};
+
+// Pairs of CTAs on 256 x 256 tiles from the point where those fill most of the SMs,
+// else single CTAs on 128 x 128 tiles.
+bool use_pairs(const vsa_plan* p, int64_t M, int64_t N) {
+  return cdiv64(M, 256) * cdiv64(N, 256) * 2 >= p->num_sms * 3 / 4;
+}
+
+bool add_product(GemmMaps& maps, GemmParams& prm, const Problem& q, int tile) {
+  const int i = prm.n_prod++;
+  // either kernel's CTA loads 128 rows of each operand
+  const bool ma = q.a_mn ? make_map2(&maps.a[i], q.a, q.K, q.M, q.ld_a, 64, 64)
+                         : make_map2(&maps.a[i], q.a, q.M, q.K, q.ld_a, 64, 128);
+  const bool mb = q.b_mn ? make_map2(&maps.b[i], q.b, q.K, q.N, q.ld_b, 64, 64)
+                         : make_map2(&maps.b[i], q.b, q.N, q.K, q.ld_b, 64, 128);
+  Product& r = prm.prod[i];
+  r.ep = q.ep;
+  r.M = int32_t(q.M);
+  r.N = int32_t(q.N);
+  r.kblocks = int32_t(cdiv64(q.K, 64));
+  r.tiles_m = int32_t(cdiv64(q.M, tile));
+  r.tiles_n = int32_t(cdiv64(q.N, tile));
+  r.a_mn = q.a_mn;
+  r.b_mn = q.b_mn;
+  prm.units += r.tiles_m * r.tiles_n;
+  return ma && mb;
+}
+
+// One or two products: in one launch where both go to single CTAs.
+cudaError_t run_products(const vsa_plan* p, const Problem* q, int n, cudaStream_t s) {
+  GemmMaps maps;
   GemmParams prm;
-  prm.ep = ep;
-  prm.partial = static_cast<float*>(partial);
-  prm.state = p->d_state;
-  prm.wait_ns = p->wait_ns;
-  prm.M = int32_t(M);
-  prm.N = int32_t(N);
-  prm.kblocks = int32_t(cdiv64(K, 64));
-  prm.tiles_m = int32_t(cdiv64(M, pairs ? 256 : 128));
-  prm.tiles_n = int32_t(cdiv64(N, pairs ? 256 : kBN));
-  prm.splits = choose_splits(p, M, N, K);
-  const int64_t units = int64_t(prm.tiles_m) * prm.tiles_n * prm.splits;
-  if (pairs) {
+  auto start = [&] {
+    memset(&prm, 0, sizeof(prm));
+    prm.state = p->d_state;
+    prm.wait_ns = p->wait_ns;
+    prm.group = kGroup;
+    prm.splits = 1;
+  };
+  bool single[2] = {};
+  for (int i = 0; i < n; ++i) {
+    single[i] = !use_pairs(p, q[i].M, q[i].N);
+    if (single[i]) continue;
+    start();
+    if (!add_product(maps, prm, q[i], 256)) return cudaErrorInvalidValue;
     const int smem = 1024 + int(PSmem::oEnd);
-    const cudaError_t e =
-        cudaFuncSetAttribute(gemm_pair_kernel<A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t most = p->num_sms / 2;
-    gemm_pair_kernel<A_MN, B_MN><<<2 * unsigned(units < most ? units : most), kGThreads, smem, s>>>(ta, tb, prm);
+    const int most = p->num_sms / 2;
+    gemm_pair_kernel<<<2 * (prm.units < most ? prm.units : most), kGThreads, smem, s>>>(maps, prm);
+  }
+  start();
+  int kb = 1 << 30;                              // k blocks of the shortest product
+  for (int i = 0; i < n; ++i) {
+    if (!single[i]) continue;
+    if (!add_product(maps, prm, q[i], 128)) return cudaErrorInvalidValue;
+    const int k = prm.prod[prm.n_prod - 1].kblocks;
+    kb = k < kb ? k : kb;
+  }
+  if (prm.n_prod == 0) return cudaGetLastError();
+  // Few tiles: clusters of 2, 4 or 8 share a tile's K, while the clusters fill no more
+  // than three quarters of the SMs (clusters of 8 do not pack the rest) and each CTA
+  // has two k blocks at least.
+  while (prm.splits < 8 && int64_t(prm.units) * prm.splits * 2 <= p->num_sms * 3 / 4 && kb >= prm.splits * 4)
+    prm.splits *= 2;
+  const int smem = 1024 + int(GSmem::oEnd);
+  if (prm.splits == 1) {
+    const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    gemm_kernel<false><<<prm.units < p->num_sms ? prm.units : p->num_sms, kGThreads, smem, s>>>(maps, prm);
     return cudaGetLastError();
   }
-  const int grid = int(units < p->num_sms ? units : p->num_sms);
-  const int smem = 1024 + int(L::oEnd);
-  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<kBN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  gemm_kernel<kBN, A_MN, B_MN><<<grid, kGThreads, smem, s>>>(ta, tb, prm);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || prm.splits == 1) return e;
-  const int64_t want = cdiv64(M * (N / 8), 256), cap = int64_t(p->num_sms) * 8;
-  split_join_kernel<<<unsigned(want < cap ? want : cap), 256, 0, s>>>(prm);
-  return cudaGetLastError();
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = unsigned(prm.splits);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(prm.units * prm.splits));
+  cfg.blockDim = dim3(kGThreads);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<true>, maps, prm);
 }
 
 struct GradPlan {
@@ -706,30 +779,34 @@ GradPlan grad_plan(const vsa_plan* p, int64_t rows, int64_t N, int act, bool gat
 
 }  // namespace
 
-int64_t linear_workspace_bytes(const vsa_plan* p, int64_t rows, int64_t n_in, int64_t n_out, bool backward,
-                               int64_t rows_per_gate) {
+int64_t linear_bwd_workspace_bytes(const vsa_plan* p, int64_t rows, int64_t n_out, int64_t rows_per_gate) {
   if (rows == 0) return 0;
-  if (!backward) return split_bytes(p, rows, n_out, n_in);
   // whatever the activation: the largest need
   const GradPlan g = grad_plan(p, rows, n_out, VSA_ACT_SILU, rows_per_gate > 0, rows_per_gate);
-  const int64_t a = split_bytes(p, rows, n_in, n_out), b = split_bytes(p, n_out, n_in, rows);
-  return g.dz_bytes + 2 * g.part_bytes + (a > b ? a : b);
+  return g.dz_bytes + 2 * g.part_bytes;
 }
 
-cudaError_t launch_linear(const vsa_plan* p, const vsa_linear_args& a, void* workspace, cudaStream_t s) {
-  Epilogue ep = {};
-  ep.out = static_cast<__nv_bfloat16*>(a.y);
-  ep.ld_out = a.ld_y;
-  ep.bias = a.bias;
-  ep.gate = a.gate;
-  ep.ld_gate = a.n_out;
-  ep.rows_per_gate = a.gate ? int32_t(a.rows_per_gate) : 1;
-  ep.residual = static_cast<const __nv_bfloat16*>(a.residual);
-  ep.ld_res = a.ld_residual;
-  ep.pre = static_cast<__nv_bfloat16*>(a.pre);
-  ep.ld_pre = a.ld_pre;
-  ep.act = a.act;
-  return run_gemm<false, false>(p, a.x, a.ld_x, a.w, a.n_in, a.rows, a.n_out, a.n_in, ep, workspace, s);
+cudaError_t launch_linear(const vsa_plan* p, const vsa_linear_args& a, cudaStream_t s) {
+  Problem q = {};
+  q.a = a.x;
+  q.ld_a = a.ld_x;
+  q.b = a.w;
+  q.ld_b = a.n_in;
+  q.M = a.rows;
+  q.N = a.n_out;
+  q.K = a.n_in;
+  q.ep.out = static_cast<__nv_bfloat16*>(a.y);
+  q.ep.ld_out = a.ld_y;
+  q.ep.bias = a.bias;
+  q.ep.gate = a.gate;
+  q.ep.ld_gate = a.n_out;
+  q.ep.rows_per_gate = a.gate ? int32_t(a.rows_per_gate) : 1;
+  q.ep.residual = static_cast<const __nv_bfloat16*>(a.residual);
+  q.ep.ld_res = a.ld_residual;
+  q.ep.pre = static_cast<__nv_bfloat16*>(a.pre);
+  q.ep.ld_pre = a.ld_pre;
+  q.ep.act = a.act;
+  return run_products(p, &q, 1, s);
 }
 
 cudaError_t launch_linear_bwd(const vsa_plan* p, const vsa_linear_grad_args& a, void* workspace, cudaStream_t s) {
@@ -738,7 +815,6 @@ cudaError_t launch_linear_bwd(const vsa_plan* p, const vsa_linear_grad_args& a, 
   auto* dz = reinterpret_cast<__nv_bfloat16*>(ws);
   float* part_z = reinterpret_cast<float*>(ws + g.dz_bytes);
   float* part_g = reinterpret_cast<float*>(ws + g.dz_bytes + g.part_bytes);
-  void* split = ws + g.dz_bytes + 2 * g.part_bytes;
   const bool products = a.dx || a.dw;
   if ((g.needs_dz && products) || a.dbias || a.dgate) {
     GradParams gp;
@@ -766,21 +842,38 @@ cudaError_t launch_linear_bwd(const vsa_plan* p, const vsa_linear_grad_args& a, 
   }
   const void* zsrc = g.needs_dz ? static_cast<const void*>(dz) : a.dy;
   const int64_t ld_z = g.needs_dz ? a.n_out : a.ld_dy;
-  Epilogue ep = {};
-  ep.rows_per_gate = 1;
-  if (a.dx) {
-    ep.out = static_cast<__nv_bfloat16*>(a.dx);
-    ep.ld_out = a.ld_dx;
-    const cudaError_t e =
-        run_gemm<false, true>(p, zsrc, ld_z, a.w, a.n_in, a.rows, a.n_in, a.n_out, ep, split, s);
-    if (e != cudaSuccess) return e;
+  Problem q[2] = {};
+  int n = 0;
+  if (a.dx) {                                    // dx = dz W: W is stored with n_out, the K of this product, as its rows
+    Problem& d = q[n++];
+    d.a = zsrc;
+    d.ld_a = ld_z;
+    d.b = a.w;
+    d.ld_b = a.n_in;
+    d.b_mn = true;
+    d.M = a.rows;
+    d.N = a.n_in;
+    d.K = a.n_out;
+    d.ep.out = static_cast<__nv_bfloat16*>(a.dx);
+    d.ep.ld_out = a.ld_dx;
+    d.ep.rows_per_gate = 1;
   }
-  if (a.dw) {
-    ep.out = static_cast<__nv_bfloat16*>(a.dw);
-    ep.ld_out = a.n_in;
-    return run_gemm<true, true>(p, zsrc, ld_z, a.x, a.ld_x, a.n_out, a.n_in, a.rows, ep, split, s);
+  if (a.dw) {                                    // dW = dz^T x: K = rows, both stored with K as their rows
+    Problem& d = q[n++];
+    d.a = zsrc;
+    d.ld_a = ld_z;
+    d.a_mn = true;
+    d.b = a.x;
+    d.ld_b = a.ld_x;
+    d.b_mn = true;
+    d.M = a.n_out;
+    d.N = a.n_in;
+    d.K = a.rows;
+    d.ep.out = static_cast<__nv_bfloat16*>(a.dw);
+    d.ep.ld_out = a.n_in;
+    d.ep.rows_per_gate = 1;
   }
-  return cudaSuccess;
+  return n ? run_products(p, q, n, s) : cudaSuccess;
 }
 
 }  // namespace vsa

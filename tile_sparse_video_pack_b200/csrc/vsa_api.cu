@@ -767,16 +767,15 @@ vsa_status vsa_sparse_attn_ref_bwd(vsa_plan* p, const void* qp, const void* kp, 
   return attn_bwd(p, qp, kp, vp, op, lse, dop, idx, idx_ref, k_per_head, dqp, dkp, dvp, ws, stream);
 }
 
-vsa_status vsa_linear_workspace(const vsa_plan* p, int64_t rows, int32_t n_in, int32_t n_out, int32_t backward,
-                                int64_t rows_per_gate, int64_t* bytes) {
-  if (!p || !bytes || !linear_sizes(rows, n_in, n_out) || (backward != 0 && backward != 1) || rows_per_gate < 0)
-    return VSA_ERR_INVALID_ARG;
+vsa_status vsa_linear_bwd_workspace(const vsa_plan* p, int64_t rows, int32_t n_in, int32_t n_out,
+                                    int64_t rows_per_gate, int64_t* bytes) {
+  if (!p || !bytes || !linear_sizes(rows, n_in, n_out) || rows_per_gate < 0) return VSA_ERR_INVALID_ARG;
   if (rows_per_gate > 0 && rows % rows_per_gate) return VSA_ERR_INVALID_ARG;
-  *bytes = vsa::linear_workspace_bytes(p, rows, n_in, n_out, backward == 1, rows_per_gate);
+  *bytes = vsa::linear_bwd_workspace_bytes(p, rows, n_out, rows_per_gate);
   return VSA_OK;
 }
 
-vsa_status vsa_linear(vsa_plan* p, const vsa_linear_args* args, void* ws, void* stream) {
+vsa_status vsa_linear(vsa_plan* p, const vsa_linear_args* args, void* stream) {
   Range r("vsa_linear");
   if (!p || !args) return fail(p, VSA_ERR_INVALID_ARG);
   const vsa_linear_args& a = *args;
@@ -790,9 +789,7 @@ vsa_status vsa_linear(vsa_plan* p, const vsa_linear_args* args, void* ws, void* 
       (a.residual && !linear_view(a.residual, a.ld_residual, a.n_out)) ||
       (a.pre && !linear_view(a.pre, a.ld_pre, a.n_out)))
     return fail(p, VSA_ERR_INVALID_ARG);
-  const int64_t need = vsa::linear_workspace_bytes(p, a.rows, a.n_in, a.n_out, false, 0);
-  if (need > 0 && (!ws || !aligned256(ws))) return fail(p, VSA_ERR_INVALID_ARG);
-  if (vsa::launch_linear(p, a, ws, static_cast<cudaStream_t>(stream)) != cudaSuccess) return fail(p, VSA_ERR_CUDA);
+  if (vsa::launch_linear(p, a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return fail(p, VSA_ERR_CUDA);
   return VSA_OK;
 }
 
@@ -819,7 +816,7 @@ vsa_status vsa_linear_bwd(vsa_plan* p, const vsa_linear_grad_args* args, void* w
     return fail(p, VSA_ERR_INVALID_ARG);
   if ((a.act != VSA_ACT_NONE || a.dgate) && !linear_view(a.pre, a.ld_pre, a.n_out))
     return fail(p, VSA_ERR_INVALID_ARG);
-  const int64_t need = vsa::linear_workspace_bytes(p, a.rows, a.n_in, a.n_out, true, a.gate ? a.rows_per_gate : 0);
+  const int64_t need = vsa::linear_bwd_workspace_bytes(p, a.rows, a.n_out, a.gate ? a.rows_per_gate : 0);
   if (need > 0 && (!ws || !aligned256(ws))) return fail(p, VSA_ERR_INVALID_ARG);
   if (vsa::launch_linear_bwd(p, a, ws, s) != cudaSuccess) return fail(p, VSA_ERR_CUDA);
   return VSA_OK;

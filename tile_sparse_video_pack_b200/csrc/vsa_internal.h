@@ -134,9 +134,8 @@ cudaError_t launch_norm_rope_bwd(const vsa_plan* p, const NormRopeArgs& n, bool 
                                  float* dw_k, void* workspace, cudaStream_t s);
 
 // Linear layer with epilogue and its gradient (linear.cu); arguments validated by the entry points.
-int64_t linear_workspace_bytes(const vsa_plan* p, int64_t rows, int64_t n_in, int64_t n_out, bool backward,
-                               int64_t rows_per_gate);
-cudaError_t launch_linear(const vsa_plan* p, const vsa_linear_args& a, void* workspace, cudaStream_t s);
+int64_t linear_bwd_workspace_bytes(const vsa_plan* p, int64_t rows, int64_t n_out, int64_t rows_per_gate);
+cudaError_t launch_linear(const vsa_plan* p, const vsa_linear_args& a, cudaStream_t s);
 cudaError_t launch_linear_bwd(const vsa_plan* p, const vsa_linear_grad_args& a, void* workspace, cudaStream_t s);
 // Gradient of the sparse attention (attn_bwd.cu).
 int64_t attn_bwd_workspace_bytes(const vsa_plan* p);

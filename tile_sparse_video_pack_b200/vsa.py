@@ -32,7 +32,7 @@ EXPORTS = ("vsa_plan_create", "vsa_plan_destroy", "vsa_plan_query", "vsa_plan_ge
            "vsa_sparse_attn_direct", "vsa_qk_norm_rope", "vsa_tile_norm_rope_pack_pool", "vsa_pooled_descriptors",
            "vsa_norm_bwd_workspace", "vsa_qk_norm_rope_bwd", "vsa_tile_norm_rope_bwd",
            "vsa_attn_bwd_workspace", "vsa_sparse_attn_bwd", "vsa_sparse_attn_ref_bwd",
-           "vsa_linear_workspace", "vsa_linear", "vsa_linear_bwd")
+           "vsa_linear_bwd_workspace", "vsa_linear", "vsa_linear_bwd")
 ROPE_LAYOUTS = {"interleaved": 0, "halves": 1}
 ACTIVATIONS = {"none": 0, "gelu_tanh": 1, "silu": 2}
 
@@ -156,8 +156,8 @@ def library() -> ctypes.CDLL:
         "vsa_attn_bwd_workspace": (I32, [P, ctypes.POINTER(I64)]),
         "vsa_sparse_attn_bwd": (I32, [P] * 14),
         "vsa_sparse_attn_ref_bwd": (I32, [P] * 15),
-        "vsa_linear_workspace": (I32, [P, I64, I32, I32, I32, I64, ctypes.POINTER(I64)]),
-        "vsa_linear": (I32, [P, ctypes.POINTER(VsaLinearArgs), P, P]),
+        "vsa_linear_bwd_workspace": (I32, [P, I64, I32, I32, I64, ctypes.POINTER(I64)]),
+        "vsa_linear": (I32, [P, ctypes.POINTER(VsaLinearArgs), P]),
         "vsa_linear_bwd": (I32, [P, ctypes.POINTER(VsaLinearGradArgs), P, P]),
     }
     for name, (res, args) in sig.items():
@@ -220,37 +220,57 @@ def _ptr(t, dtype, name, min_numel=0):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _device_ptr(t, dtype, name):
-    """Device pointer of a CUDA tensor of any strides on the current device."""
+# The helpers below serve the calls around the layer, whose smallest sizes run in a few
+# microseconds on the GPU: they check in one pass, pass addresses as plain integers and
+# build the error message only once something is wrong.
+
+def _addr(t, dtype, name, dev, min_numel=0):
+    """Address of a contiguous tensor on device `dev`, the current one (None -> NULL)."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= min_numel:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, dtype, name, min_numel).value     # raises what is wrong
+
+
+def _strided_addr(t, dtype, name, dev):
+    """Address of a tensor of any strides on device `dev`, the current one."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, but cuda:{torch.cuda.current_device()} is the current device")
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but cuda:{dev} is the current device")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _matrix(t, cols, name, rows=None):
-    """(pointer, row stride, rows) of a bf16 [..., cols] tensor whose leading dimensions form one row axis."""
+def _matrix(t, cols, name, dev, rows=None):
+    """(address, row stride, rows) of a bf16 [..., cols] tensor whose leading dimensions form one row axis."""
     import torch
-    p = _device_ptr(t, torch.bfloat16, name)
-    if t.dim() < 1 or t.shape[-1] != cols:
-        raise ValueError(f"{name} must be [..., {cols}], got {tuple(t.shape)}")
-    if t.numel() == 0:
-        m = t.reshape(-1, cols)
+    p = _strided_addr(t, torch.bfloat16, name, dev)
+    shape = t.shape
+    if not shape or shape[-1] != cols:
+        raise ValueError(f"{name} must be [..., {cols}], got {tuple(shape)}")
+    if len(shape) == 2:
+        n, (ld, unit) = shape[0], t.stride()
+    elif t.is_contiguous():
+        n, ld, unit = t.numel() // cols, cols, 1
     else:
         try:
             m = t.view(-1, cols)
         except RuntimeError:
-            raise ValueError(f"{name}'s leading dimensions {tuple(t.shape)} are not one row axis "
+            raise ValueError(f"{name}'s leading dimensions {tuple(shape)} are not one row axis "
                              f"(strides {t.stride()})") from None
-    if m.shape[0] > 0 and cols > 1 and m.stride(1) != 1:
+        n, (ld, unit) = m.shape[0], m.stride()
+    if unit != 1 and n > 0 and cols > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    if rows is not None and m.shape[0] != rows:
-        raise ValueError(f"{name} has {m.shape[0]} rows, needs {rows}")
-    return p, (m.stride(0) if m.shape[0] > 1 else cols), m.shape[0]
+    if rows is not None and n != rows:
+        raise ValueError(f"{name} has {n} rows, needs {rows}")
+    return p, (ld if n > 1 else cols), n
 
 
 class NormRope:
@@ -272,23 +292,31 @@ class NormRope:
         self.w_q, self.w_k, self.cos, self.sin = w_q, w_k, cos, sin
         self.layout, self.eps = layout, float(eps)
 
+        self._made = (None, None)      # the last struct, and the values it was made of
+
     @property
     def per_head(self):
         w = self.w_q if self.w_q is not None else self.w_k
         return w is not None and w.dim() == 2
 
-    def _struct(self, plan):
+    def _struct(self, plan, dev):
         import torch
-        d, heads, n = plan.desc.head_dim, plan.desc.heads, plan.info.n_tokens
-        for w, name in ((self.w_q, "w_q"), (self.w_k, "w_k")):
-            if w is not None and tuple(w.shape) != ((heads, d) if self.per_head else (d,)):
-                raise ValueError(f"{name} must be [{d}] or [{heads}, {d}], got {tuple(w.shape)}")
-        for t, name in ((self.cos, "cos"), (self.sin, "sin")):
-            if t is not None and tuple(t.shape) != (n, d // 2):
-                raise ValueError(f"{name} must be [{n}, {d // 2}], got {tuple(t.shape)}")
         f32 = torch.float32
-        return VsaNormRope(_ptr(self.w_q, f32, "w_q"), _ptr(self.w_k, f32, "w_k"), _ptr(self.cos, f32, "cos"),
-                           _ptr(self.sin, f32, "sin"), int(self.per_head), ROPE_LAYOUTS[self.layout], self.eps)
+        per_head = self.per_head
+        _, n, heads, d = plan._tokens
+        want_w, want_t = ((heads, d) if per_head else (d,)), (n, d // 2)
+        at = []
+        for t, name, want in ((self.w_q, "w_q", want_w), (self.w_k, "w_k", want_w), (self.cos, "cos", want_t),
+                              (self.sin, "sin", want_t)):
+            if t is not None and t.shape != want:
+                raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+            at.append(_addr(t, f32, name, dev))
+        key = (*at, per_head, self.layout, self.eps)
+        made = self._made
+        if made[0] != key:
+            made = (key, VsaNormRope(*at, int(per_head), ROPE_LAYOUTS[self.layout], self.eps))
+            self._made = made
+        return ctypes.byref(made[1])
 
 
 def _karray(k_per_head, heads):
@@ -307,6 +335,13 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _here(stream):
+    """(current device, raw stream) of a call."""
+    import torch
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 class Plan:
     """A vsa_plan: one layer's tiling tables and attention work list on the current device."""
 
@@ -319,6 +354,8 @@ class Plan:
         inf = VsaPlanInfo()
         _check(lib.vsa_plan_query(h, ctypes.byref(inf)), "vsa_plan_query")
         self.info = inf
+        self._tokens = (desc.batch, inf.n_tokens, desc.heads, desc.head_dim)
+        self._bytes = {}               # workspace sizes of this plan, by call
 
     @classmethod
     def from_config(cls, cfg, sparsity: float, k_per_head=None):
@@ -583,40 +620,56 @@ class Plan:
             _ptr(o, bf, "o", n_tok), _stream(stream)), "vsa_layer_forward")
 
     # ---- norm + rotation, and its gradient ------------------------------------------
-    def _token_view(self, t, name):
-        """(pointer, strides) of a bf16 [B, N, heads, head_dim] view with contiguous heads and channels."""
+    def _token_views(self, dev, *views):
+        """(addresses, strides) of bf16 [B, N, heads, head_dim] views with contiguous heads and channels; strides
+        None when all are contiguous."""
         import torch
-        p = _device_ptr(t, torch.bfloat16, name)
-        B, n, heads, d = want = self.shapes()["tokens"]
-        if tuple(t.shape) != want:
-            raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
-        if t.stride(3) != 1 or (heads > 1 and t.stride(2) != d):
-            raise ValueError(f"{name}'s heads and channels must be contiguous (strides {t.stride()})")
-        token = t.stride(1) if n > 1 else heads * d
-        return p, VsaStrides(t.stride(0) if B > 1 else token * n, token)
+        bf, want = torch.bfloat16, self._tokens
+        B, n, heads, d = want
+        ptrs, strides, plain = [], [], True
+        for name, t in views:
+            ptrs.append(_strided_addr(t, bf, name, dev))
+            if t.shape != want:
+                raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+            if t.is_contiguous():
+                strides += (n * heads * d, heads * d)
+                continue
+            plain = False
+            sb, st, sh, sd = t.stride()
+            if sd != 1 or (heads > 1 and sh != d):
+                raise ValueError(f"{name}'s heads and channels must be contiguous (strides {t.stride()})")
+            token = st if n > 1 else heads * d
+            strides += (sb if B > 1 else token * n, token)
+        return ptrs, (None if plain else (ctypes.c_int64 * len(strides))(*strides))
 
-    def _token_views(self, **views):
-        ptrs, strides = zip(*(self._token_view(t, name) for name, t in views.items()))
-        return ptrs, (VsaStrides * len(strides))(*strides)
+    def _workspace(self, call):
+        """Bytes of a call's workspace, which the plan fixes."""
+        n = self._bytes.get(call)
+        if n is None:
+            out = ctypes.c_int64()
+            _check(getattr(library(), call)(self._h, ctypes.byref(out)), call)
+            n = self._bytes[call] = out.value
+        return n
 
     def qk_norm_rope(self, q, k, norm, q_out, k_out, stream=None):
         """RMS norm of every head's q and k row and the rotation, token-major views to token-major views
         (an output may be its own input)."""
-        (pq, pk, pqo, pko), st = self._token_views(q=q, k=k, q_out=q_out, k_out=k_out)
-        n = norm._struct(self)
-        _check(library().vsa_qk_norm_rope(self._h, ctypes.byref(n), pq, pk, pqo, pko, st, _stream(stream)),
-               "vsa_qk_norm_rope")
+        dev, s = _here(stream)
+        ptrs, st = self._token_views(dev, ("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))
+        status = library().vsa_qk_norm_rope(self._h, norm._struct(self, dev), *ptrs, st, s)
+        if status:
+            _check(status, "vsa_qk_norm_rope")
 
     def tile_norm_rope_pack_pool(self, q, k, v, norm, qp, kp, vp, workspace, stream=None):
         """qk_norm_rope and tile_pack_pool in one pass; follow with tile_score_pooled."""
         import torch
-        (pq, pk, pv), st = self._token_views(q=q, k=k, v=v)
-        n = norm._struct(self)
+        dev, s = _here(stream)
+        ptrs, st = self._token_views(dev, ("q", q), ("k", k), ("v", v))
         pe, bf = self.info.packed_elems, torch.bfloat16
         _check(library().vsa_tile_norm_rope_pack_pool(
-            self._h, ctypes.byref(n), pq, pk, pv, st, _ptr(qp, bf, "qp", pe), _ptr(kp, bf, "kp", pe),
-            _ptr(vp, bf, "vp", pe), _ptr(workspace, torch.uint8, "workspace", self.info.workspace_bytes),
-            _stream(stream)), "vsa_tile_norm_rope_pack_pool")
+            self._h, norm._struct(self, dev), *ptrs, st, _addr(qp, bf, "qp", dev, pe), _addr(kp, bf, "kp", dev, pe),
+            _addr(vp, bf, "vp", dev, pe), _addr(workspace, torch.uint8, "workspace", dev, self.info.workspace_bytes),
+            s), "vsa_tile_norm_rope_pack_pool")
 
     def pooled(self, workspace):
         """The descriptors that a pooling call left in the workspace: fp32 views [B, heads, ntv_max, w] of Q and K."""
@@ -634,95 +687,85 @@ class Plan:
                      for p in (pq, pk))
 
     def norm_bwd_workspace_bytes(self):
-        n = ctypes.c_int64()
-        _check(library().vsa_norm_bwd_workspace(self._h, ctypes.byref(n)), "vsa_norm_bwd_workspace")
-        return n.value
+        return self._workspace("vsa_norm_bwd_workspace")
 
-    def _dw_ptrs(self, norm, dw_q, dw_k):
+    def _dw(self, norm, dw_q, dw_k, dev):
         import torch
-        want = (self.desc.heads, self.desc.head_dim) if norm.per_head else (self.desc.head_dim,)
+        _, _, heads, d = self._tokens
+        want = (heads, d) if norm.per_head else (d,)
         for t, name in ((dw_q, "dw_q"), (dw_k, "dw_k")):
-            if t is not None and tuple(t.shape) != want:
+            if t is not None and t.shape != want:
                 raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
-        return _ptr(dw_q, torch.float32, "dw_q"), _ptr(dw_k, torch.float32, "dw_k")
+        return _addr(dw_q, torch.float32, "dw_q", dev), _addr(dw_k, torch.float32, "dw_k", dev)
 
     def qk_norm_rope_bwd(self, dq_out, dk_out, q, k, norm, dq, dk, dw_q, dw_k, workspace, stream=None):
         """Gradient of qk_norm_rope: dq, dk and (unless None) the weights' dw_q, dw_k."""
         import torch
-        ptrs, st = self._token_views(dq_out=dq_out, dk_out=dk_out, q=q, k=k, dq=dq, dk=dk)
-        n = norm._struct(self)
+        dev, s = _here(stream)
+        ptrs, st = self._token_views(dev, ("dq_out", dq_out), ("dk_out", dk_out), ("q", q), ("k", k), ("dq", dq),
+                                     ("dk", dk))
         _check(library().vsa_qk_norm_rope_bwd(
-            self._h, ctypes.byref(n), *ptrs, st, *self._dw_ptrs(norm, dw_q, dw_k),
-            _ptr(workspace, torch.uint8, "workspace", self.norm_bwd_workspace_bytes()), _stream(stream)),
+            self._h, norm._struct(self, dev), *ptrs, st, *self._dw(norm, dw_q, dw_k, dev),
+            _addr(workspace, torch.uint8, "workspace", dev, self.norm_bwd_workspace_bytes()), s),
             "vsa_qk_norm_rope_bwd")
 
     def tile_norm_rope_bwd(self, dqp, dkp, dvp, q, k, norm, dq, dk, dv, dw_q, dw_k, workspace, stream=None):
         """Gradient of tile_norm_rope_pack_pool: packed gradients back to token-major dq, dk, dv and to the weights."""
         import torch
+        dev, s = _here(stream)
         pe, bf = self.info.packed_elems, torch.bfloat16
-        ptrs, st = self._token_views(q=q, k=k, dq=dq, dk=dk, dv=dv)
-        n = norm._struct(self)
+        ptrs, st = self._token_views(dev, ("q", q), ("k", k), ("dq", dq), ("dk", dk), ("dv", dv))
         _check(library().vsa_tile_norm_rope_bwd(
-            self._h, ctypes.byref(n), _ptr(dqp, bf, "dqp", pe), _ptr(dkp, bf, "dkp", pe), _ptr(dvp, bf, "dvp", pe),
-            *ptrs, st, *self._dw_ptrs(norm, dw_q, dw_k),
-            _ptr(workspace, torch.uint8, "workspace", self.norm_bwd_workspace_bytes()), _stream(stream)),
+            self._h, norm._struct(self, dev), _addr(dqp, bf, "dqp", dev, pe), _addr(dkp, bf, "dkp", dev, pe),
+            _addr(dvp, bf, "dvp", dev, pe), *ptrs, st, *self._dw(norm, dw_q, dw_k, dev),
+            _addr(workspace, torch.uint8, "workspace", dev, self.norm_bwd_workspace_bytes()), s),
             "vsa_tile_norm_rope_bwd")
 
     # ---- gradient of the sparse attention --------------------------------------------
     def attn_bwd_workspace_bytes(self):
-        n = ctypes.c_int64()
-        _check(library().vsa_attn_bwd_workspace(self._h, ctypes.byref(n)), "vsa_attn_bwd_workspace")
-        return n.value
+        return self._workspace("vsa_attn_bwd_workspace")
 
-    def _attn_bwd_args(self, qp, kp, vp, op, lse, dop, idx):
+    def _attn_bwd_args(self, dev, qp, kp, vp, op, lse, dop, idx):
         import torch
         pe, bf = self.info.packed_elems, torch.bfloat16
-        return (_ptr(qp, bf, "qp", pe), _ptr(kp, bf, "kp", pe), _ptr(vp, bf, "vp", pe), _ptr(op, bf, "op", pe),
-                _ptr(lse, torch.float32, "lse", self.info.lse_elems), _ptr(dop, bf, "dop", pe),
-                _ptr(idx, torch.int32, "idx", self.info.index_elems))
+        return (_addr(qp, bf, "qp", dev, pe), _addr(kp, bf, "kp", dev, pe), _addr(vp, bf, "vp", dev, pe),
+                _addr(op, bf, "op", dev, pe), _addr(lse, torch.float32, "lse", dev, self.info.lse_elems),
+                _addr(dop, bf, "dop", dev, pe), _addr(idx, torch.int32, "idx", dev, self.info.index_elems))
 
-    def _attn_bwd_outs(self, dqp, dkp, dvp, workspace, stream):
+    def _attn_bwd_outs(self, dev, dqp, dkp, dvp, workspace):
         import torch
         pe, bf = self.info.packed_elems, torch.bfloat16
-        return (_ptr(dqp, bf, "dqp", pe), _ptr(dkp, bf, "dkp", pe), _ptr(dvp, bf, "dvp", pe),
-                _ptr(workspace, torch.uint8, "workspace", self.attn_bwd_workspace_bytes()), _stream(stream))
+        return (_addr(dqp, bf, "dqp", dev, pe), _addr(dkp, bf, "dkp", dev, pe), _addr(dvp, bf, "dvp", dev, pe),
+                _addr(workspace, torch.uint8, "workspace", dev, self.attn_bwd_workspace_bytes()))
 
     def sparse_attn_bwd(self, qp, kp, vp, op, lse, dop, idx, dqp, dkp, dvp, workspace, stream=None, k_per_head=None):
         """Gradient of sparse_attn on packed tiles: dqp, dkp, dvp from dop, the forward's inputs and its op, lse."""
+        dev, s = _here(stream)
         _check(library().vsa_sparse_attn_bwd(
-            self._h, *self._attn_bwd_args(qp, kp, vp, op, lse, dop, idx), _karray(k_per_head, self.desc.heads),
-            *self._attn_bwd_outs(dqp, dkp, dvp, workspace, stream)), "vsa_sparse_attn_bwd")
+            self._h, *self._attn_bwd_args(dev, qp, kp, vp, op, lse, dop, idx), _karray(k_per_head, self.desc.heads),
+            *self._attn_bwd_outs(dev, dqp, dkp, dvp, workspace), s), "vsa_sparse_attn_bwd")
 
     def sparse_attn_ref_bwd(self, qp, kp, vp, op, lse, dop, idx, idx_ref, dqp, dkp, dvp, workspace, stream=None,
                             k_per_head=None):
         """Gradient of sparse_attn_ref (R2VA budgets)."""
         import torch
+        dev, s = _here(stream)
         _check(library().vsa_sparse_attn_ref_bwd(
-            self._h, *self._attn_bwd_args(qp, kp, vp, op, lse, dop, idx),
-            _ptr(idx_ref, torch.int32, "idx_ref", self.info.ref_index_elems),
-            _karray(k_per_head, self.desc.heads), *self._attn_bwd_outs(dqp, dkp, dvp, workspace, stream)),
+            self._h, *self._attn_bwd_args(dev, qp, kp, vp, op, lse, dop, idx),
+            _addr(idx_ref, torch.int32, "idx_ref", dev, self.info.ref_index_elems),
+            _karray(k_per_head, self.desc.heads), *self._attn_bwd_outs(dev, dqp, dkp, dvp, workspace), s),
             "vsa_sparse_attn_ref_bwd")
 
     # ---- linear layer with epilogue, and its gradient ---------------------------------
-    def linear_workspace_bytes(self, rows, n_in, n_out, backward=False, samples=0):
-        """Workspace of :meth:`linear` (or :meth:`linear_bwd`); samples: rows of the gate, 0 without one."""
-        per = rows // samples if samples else 0
-        if samples and rows % samples:
-            raise ValueError(f"{rows} rows do not divide into {samples} samples")
-        n = ctypes.c_int64()
-        _check(library().vsa_linear_workspace(self._h, int(rows), int(n_in), int(n_out), int(bool(backward)), int(per),
-                                              ctypes.byref(n)), "vsa_linear_workspace")
-        return n.value
-
     @staticmethod
-    def _gate(gate, rows, n_out, name="gate"):
+    def _gate(gate, rows, n_out, dev):
         import torch
         if gate is None:
-            return None, 0, 0
+            return None, 0
         if gate.dim() != 2 or gate.shape[1] != n_out or gate.shape[0] < 1 or rows % gate.shape[0]:
-            raise ValueError(f"{name} must be [samples, {n_out}] with samples dividing {rows} rows, "
+            raise ValueError(f"gate must be [samples, {n_out}] with samples dividing {rows} rows, "
                              f"got {tuple(gate.shape)}")
-        return _ptr(gate, torch.float32, name), rows // gate.shape[0], gate.shape[0]
+        return _addr(gate, torch.float32, "gate", dev), rows // gate.shape[0]
 
     @staticmethod
     def _act(act):
@@ -730,62 +773,70 @@ class Plan:
             raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
         return ACTIVATIONS[act]
 
-    def _linear_workspace(self, workspace, need):
-        import torch
-        if need == 0:
-            return None
-        if workspace is None:
-            raise ValueError(f"this size needs a workspace of {need} bytes")
-        return _ptr(workspace, torch.uint8, "workspace", need)
-
-    def linear(self, x, w, y, bias=None, act="none", gate=None, residual=None, pre=None, workspace=None, stream=None):
+    def linear(self, x, w, y, bias=None, act="none", gate=None, residual=None, pre=None, stream=None):
         """y = residual + gate * act(x w^T + bias): x [..., n_in], w [n_out, n_in], y [..., n_out] bf16, bias [n_out]
         and gate [samples, n_out] fp32. pre, if given, receives x w^T + bias for :meth:`linear_bwd`."""
         import torch
+        dev, s = _here(stream)
         if w.dim() != 2:
             raise ValueError(f"w must be [n_out, n_in], got {tuple(w.shape)}")
         n_out, n_in = w.shape
-        px, ld_x, rows = _matrix(x, n_in, "x")
-        py, ld_y, _ = _matrix(y, n_out, "y", rows)
-        pr, ld_r = _matrix(residual, n_out, "residual", rows)[:2] if residual is not None else (None, 0)
-        pp, ld_p = _matrix(pre, n_out, "pre", rows)[:2] if pre is not None else (None, 0)
-        if bias is not None and tuple(bias.shape) != (n_out,):
+        px, ld_x, rows = _matrix(x, n_in, "x", dev)
+        py, ld_y, _ = _matrix(y, n_out, "y", dev, rows)
+        pr, ld_r, _ = _matrix(residual, n_out, "residual", dev, rows) if residual is not None else (None, 0, 0)
+        pp, ld_p, _ = _matrix(pre, n_out, "pre", dev, rows) if pre is not None else (None, 0, 0)
+        if bias is not None and bias.shape != (n_out,):
             raise ValueError(f"bias must be [{n_out}], got {tuple(bias.shape)}")
-        pg, per, _ = self._gate(gate, rows, n_out)
-        a = VsaLinearArgs(rows, n_in, n_out, px, ld_x, _ptr(w, torch.bfloat16, "w"),
-                          _ptr(bias, torch.float32, "bias"), self._act(act), pg, per, pr, ld_r, py, ld_y, pp, ld_p)
-        ws = self._linear_workspace(workspace, self.linear_workspace_bytes(rows, n_in, n_out))
-        _check(library().vsa_linear(self._h, ctypes.byref(a), ws, _stream(stream)), "vsa_linear")
+        pg, per = self._gate(gate, rows, n_out, dev)
+        a = VsaLinearArgs(rows, n_in, n_out, px, ld_x, _addr(w, torch.bfloat16, "w", dev),
+                          _addr(bias, torch.float32, "bias", dev), self._act(act), pg, per, pr, ld_r, py, ld_y, pp, ld_p)
+        status = library().vsa_linear(self._h, a, s)
+        if status:
+            _check(status, "vsa_linear")
+
+    def linear_bwd_workspace_bytes(self, rows, n_in, n_out, samples=0):
+        """Workspace of :meth:`linear_bwd`; samples: rows of the gate, 0 without one."""
+        if samples and rows % samples:
+            raise ValueError(f"{rows} rows do not divide into {samples} samples")
+        n = ctypes.c_int64()
+        _check(library().vsa_linear_bwd_workspace(self._h, int(rows), int(n_in), int(n_out),
+                                                  rows // samples if samples else 0, ctypes.byref(n)),
+               "vsa_linear_bwd_workspace")
+        return n.value
 
     def linear_bwd(self, dy, x, w, dx=None, dw=None, act="none", pre=None, gate=None, dbias=None, dgate=None,
                    workspace=None, stream=None):
         """Gradient of :meth:`linear`: any of dx [..., n_in], dw [n_out, n_in] (bf16), dbias [n_out] and dgate
         [samples, n_out] (fp32); that of the residual is dy itself."""
         import torch
+        dev, s = _here(stream)
         if w.dim() != 2:
             raise ValueError(f"w must be [n_out, n_in], got {tuple(w.shape)}")
         n_out, n_in = w.shape
-        pdy, ld_dy, rows = _matrix(dy, n_out, "dy")
-        px, ld_x = _matrix(x, n_in, "x", rows)[:2] if x is not None else (None, 0)
-        pdx, ld_dx = _matrix(dx, n_in, "dx", rows)[:2] if dx is not None else (None, 0)
-        pp, ld_p = _matrix(pre, n_out, "pre", rows)[:2] if pre is not None else (None, 0)
+        pdy, ld_dy, rows = _matrix(dy, n_out, "dy", dev)
+        px, ld_x, _ = _matrix(x, n_in, "x", dev, rows) if x is not None else (None, 0, 0)
+        pdx, ld_dx, _ = _matrix(dx, n_in, "dx", dev, rows) if dx is not None else (None, 0, 0)
+        pp, ld_p, _ = _matrix(pre, n_out, "pre", dev, rows) if pre is not None else (None, 0, 0)
         if (act != "none" or dgate is not None) and pre is None:
             raise ValueError("an activation's or a gate's gradient needs pre")
         if dw is not None and x is None:
             raise ValueError("dw needs x")
-        pg, per, samples = self._gate(gate, rows, n_out)
+        pg, per = self._gate(gate, rows, n_out, dev)
         if dgate is not None and (gate is None or dgate.shape != gate.shape):
             raise ValueError("dgate comes with a gate of its shape")
         if dw is not None and dw.shape != w.shape:
             raise ValueError(f"dw must be {tuple(w.shape)}, got {tuple(dw.shape)}")
-        if dbias is not None and tuple(dbias.shape) != (n_out,):
+        if dbias is not None and dbias.shape != (n_out,):
             raise ValueError(f"dbias must be [{n_out}], got {tuple(dbias.shape)}")
+        need = self.linear_bwd_workspace_bytes(rows, n_in, n_out, gate.shape[0] if gate is not None else 0)
+        if need and workspace is None:
+            raise ValueError(f"this size needs a workspace of {need} bytes")
         bf, f32 = torch.bfloat16, torch.float32
-        a = VsaLinearGradArgs(rows, n_in, n_out, pdy, ld_dy, px, ld_x, _ptr(w, bf, "w"), self._act(act), pp, ld_p, pg,
-                              per, pdx, ld_dx, _ptr(dw, bf, "dw"), _ptr(dbias, f32, "dbias"),
-                              _ptr(dgate, f32, "dgate"))
-        ws = self._linear_workspace(workspace, self.linear_workspace_bytes(rows, n_in, n_out, True, samples))
-        _check(library().vsa_linear_bwd(self._h, ctypes.byref(a), ws, _stream(stream)), "vsa_linear_bwd")
+        a = VsaLinearGradArgs(rows, n_in, n_out, pdy, ld_dy, px, ld_x, _addr(w, bf, "w", dev), self._act(act), pp, ld_p,
+                              pg, per, pdx, ld_dx, _addr(dw, bf, "dw", dev), _addr(dbias, f32, "dbias", dev),
+                              _addr(dgate, f32, "dgate", dev))
+        _check(library().vsa_linear_bwd(self._h, a, _addr(workspace, torch.uint8, "workspace", dev, need), s),
+               "vsa_linear_bwd")
 
     def set_wait_limit(self, limit_ns: int = 0):
         """Bound of every device-side wait of the plan's tcgen05 kernels (0: the two-second default)."""
