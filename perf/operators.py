@@ -231,9 +231,8 @@ def prepare(case, seed):
             import tile_sparse_video_pack_b200 as T
             st["plan"] = p = T.Plan(T.make_desc(1, 1, 64, 1, 8, 8, [], [(4, 4, 4)], [1]))
             new = lambda *s, t=BF16: torch.empty(*s, dtype=t, device="cuda")
-            bwd = c["op"] == "linear_bwd"
-            st["ws"] = new(p.linear_workspace_bytes(M, K, N, backward=bwd, samples=S if c["gate"] else 0), t=torch.uint8)
-            if bwd:
+            if c["op"] == "linear_bwd":
+                st["ws"] = new(p.linear_bwd_workspace_bytes(M, K, N, samples=S if c["gate"] else 0), t=torch.uint8)
                 st.update(dx=new(M, K), dw=new(N, K), dbias=new(N, t=F32) if c["bias"] else None,
                           dgate=new(S, N, t=F32) if c["gate"] else None)
             else:
@@ -491,7 +490,7 @@ def _run_own(st, c, op):
     p = st["plan"]
     if op == "linear":
         p.linear(st["x"], st["w"], st["y"], bias=st["bias"], act=c["act"], gate=st["gate"], residual=st["residual"],
-                 pre=st["z"], workspace=st["ws"])
+                 pre=st["z"])
         return {"y": st["y"], "pre": st["z"]} if c["pre"] else {"y": st["y"]}
     if op == "linear_bwd":
         p.linear_bwd(st["dy"], st["x"], st["w"], st["dx"], st["dw"], act=c["act"], pre=st["pre"], gate=st["gate"],
