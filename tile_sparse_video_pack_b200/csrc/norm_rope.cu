@@ -22,11 +22,17 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include "tc_sm100.h"
 #include "tile_map.h"
 #include "vsa_internal.h"
 
 namespace vsa {
 namespace {
+
+using tc::f2pack;
+using tc::f2unpack;
+using tc::fadd2;
+using tc::fmul2;
 
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -46,6 +52,15 @@ __device__ __forceinline__ uint4 load_row(const __nv_bfloat16* row, int d, int c
     return make_uint4(a.x, a.y, b.x, b.y);
   }
   return __ldcs(reinterpret_cast<const uint4*>(row) + c);
+}
+template <bool HALVES>
+__device__ __forceinline__ uint4 row_of(const __nv_bfloat16* row, int d, int c) {   // the same of a row in shared memory
+  if (HALVES) {
+    const uint2 a = *reinterpret_cast<const uint2*>(row + 4 * c);
+    const uint2 b = *reinterpret_cast<const uint2*>(row + d / 2 + 4 * c);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+  return reinterpret_cast<const uint4*>(row)[c];
 }
 template <bool HALVES>
 __device__ __forceinline__ void store_row(__nv_bfloat16* row, int d, int c, uint4 v) {
@@ -150,19 +165,23 @@ __device__ __forceinline__ float square_sum(const float (&a)[4], const float (&b
   return s + __shfl_xor_sync(0xffffffffu, s, CPR / 2);
 }
 
-// The normed and turned row as stored (bf16 words). Each product of the rotation
-// is rounded by itself, as the formula is written: with a fused multiply-add one
-// of a pair's two products would be exact and the other not.
+// The normed and turned row as stored (bf16 words), two pairs at a time in packed
+// fp32. Each product of the rotation is rounded by itself, as the formula is
+// written: with a fused multiply-add one of a pair's two products would be
+// exact and the other not.
 template <int CPR, bool HALVES>
 __device__ __forceinline__ uint4 norm_rope_row(uint4 v, const Weights& w, const Turn& t, float eps) {
   float a[4], b[4];
   to_pairs<HALVES>(v, a, b);
   const float r = rsqrtf(square_sum<CPR, HALVES>(a, b) * (1.f / (CPR * 8)) + eps);
+  const uint64_t r2 = f2pack(r, r);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float na = __fmul_rn(__fmul_rn(a[j], r), w.a[j]), nb = __fmul_rn(__fmul_rn(b[j], r), w.b[j]);
-    a[j] = __fsub_rn(__fmul_rn(na, t.c[j]), __fmul_rn(nb, t.s[j]));
-    b[j] = __fadd_rn(__fmul_rn(na, t.s[j]), __fmul_rn(nb, t.c[j]));
+  for (int j = 0; j < 4; j += 2) {
+    const uint64_t na = fmul2(fmul2(f2pack(a[j], a[j + 1]), r2), f2pack(w.a[j], w.a[j + 1]));
+    const uint64_t nb = fmul2(fmul2(f2pack(b[j], b[j + 1]), r2), f2pack(w.b[j], w.b[j + 1]));
+    const uint64_t c = f2pack(t.c[j], t.c[j + 1]), s = f2pack(t.s[j], t.s[j + 1]);
+    f2unpack(fadd2(fmul2(na, c), fmul2(nb, s ^ 0x8000000080000000ull)), a[j], a[j + 1]);   // - nb s
+    f2unpack(fadd2(fmul2(na, s), fmul2(nb, c)), b[j], b[j + 1]);
   }
   return from_pairs<HALVES>(a, b);
 }
@@ -208,136 +227,203 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(NormRopeArgs n, int B, i
   }
 }
 
-// Fused with the pack and the pooling: one CTA of 256 threads per (batch, tile,
-// head), the heads of a tile next to one another so that they find its table
-// rows in L2. Lanes and rows as in the pack kernel; the descriptors are pooled
-// from the rounded rows in the same order as there, so packed tiles and
-// descriptors equal, bit for bit, those of the token-major pass followed by
-// the pack. Tiles past a head's own are zero, their descriptors too.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {   // off: sixteen zero bytes
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Fused with the pack and the pooling: one CTA of 256 threads per (batch, tile, a
+// run of `run` heads). Bound by HBM, and next to it by L2: the table rows of a
+// tile are two thirds of its q, k and v rows' bytes, so a thread keeps its rows'
+// angles in registers for all heads of the run that share a tile shape. The rows
+// of a head (48 KB at d = 128) are requested at once into one of two buffers, the
+// next head's while this one is worked on, so that the bytes in flight do not
+// depend on registers. Unused slots arrive as zeros. Full clip: 0.78 ms with a
+// table read per head; one pass of loads per thread into registers took 1.20 ms. Lanes and rows as in the pack kernel;
+// the descriptors are pooled from the rounded rows in the same order as there, so
+// packed tiles and descriptors equal, bit for bit, those of the token-major pass
+// followed by the pack. Tiles past a head's own are zero, their descriptors too.
+template <int CPR, bool TRIP>
+struct PackSmem {
+  static constexpr int D = CPR * 8, NS = TRIP ? 3 : 1;
+  static constexpr uint32_t kTensor = VSA_TILE * D * 2;
+  static constexpr uint32_t kPart = NS * 2 * 8 * D * 4;        // pooling partials, over the rows once they are read
+  static constexpr uint32_t kBuf = 3 * kTensor > kPart ? 3 * kTensor : kPart;
+  static constexpr uint32_t kBytes = 2 * kBuf;
+};
 template <int CPR, bool HALVES, bool TRIP>
-__global__ void __launch_bounds__(256) norm_rope_pack_kernel(NormRopeArgs n, Geometry g, const __nv_bfloat16* q,
-                                                             const __nv_bfloat16* k, const __nv_bfloat16* v,
-                                                             __nv_bfloat16* qp, __nv_bfloat16* kp, __nv_bfloat16* vp,
-                                                             const int32_t* __restrict__ counts, float* pq, float* pk) {
+__global__ void __launch_bounds__(256, 2)
+    norm_rope_pack_kernel(NormRopeArgs n, Geometry g, int run, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                          const __nv_bfloat16* v, __nv_bfloat16* qp, __nv_bfloat16* kp, __nv_bfloat16* vp,
+                          const int32_t* __restrict__ counts, float* pq, float* pk) {
   constexpr int D = CPR * 8;
   constexpr int KD = TRIP ? 3 * D : D;
   constexpr int RG = 256 / CPR, RPT = 64 / RG;
   constexpr int NS = TRIP ? 3 : 1;
-  __shared__ float part[NS][2][8][D];
-  const int h = int(blockIdx.x % g.Hh);
-  const int64_t bn = blockIdx.x / g.Hh;
+  extern __shared__ __align__(16) uint8_t rows[];              // two of [q, k, v][64][D] bf16
+  __shared__ int32_t toks[2][VSA_TILE];
+  using L = PackSmem<CPR, TRIP>;
+  const int runs = (g.Hh + run - 1) / run;
+  const int h0 = int(blockIdx.x % runs) * run, h1 = min(g.Hh, h0 + run);
+  const int64_t bn = blockIdx.x / runs;
   const int tile_n = int(bn % g.nt_max), b = int(bn / g.nt_max);
-  const int bh = b * g.Hh + h;
-  const int64_t tile = int64_t(bh) * g.nt_max + tile_n;
   const int c = threadIdx.x % CPR, rg = threadIdx.x / CPR;
-  const int vt = tile_n - g.n_pre_tiles;
-  const bool pool = vt >= 0 && vt < g.ntv[h];   // uniform over the CTA
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-
-  int tok[RPT];
-  uint4 xq[RPT], xk[RPT];
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    tok[i] = src_token(g, h, tile_n, rg + RG * i);
-    xq[i] = xk[i] = zero;
-    uint4 xv = zero;
-    if (tok[i] >= 0) {
-      xq[i] = load_row<HALVES>(q + b * n.st[0].batch + tok[i] * n.st[0].token + h * D, D, c);
-      xk[i] = load_row<HALVES>(k + b * n.st[1].batch + tok[i] * n.st[1].token + h * D, D, c);
-      xv = __ldcs(reinterpret_cast<const uint4*>(v + b * n.st[2].batch + tok[i] * n.st[2].token + h * D) + c);
-    }
-    reinterpret_cast<uint4*>(vp + (tile * VSA_TILE + rg + RG * i) * D)[c] = xv;
-  }
-  const int64_t woff = n.per_head ? int64_t(h) * D : 0;
-  const Weights wq = load_weights<HALVES>(n.w_q ? n.w_q + woff : nullptr, D, c);
-  const Weights wk = load_weights<HALVES>(n.w_k ? n.w_k + woff : nullptr, D, c);
-  float st[NS][2][8];                            // [statistic][q, k][pair j: a, then b]
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      st[0][t][e] = 0.f;
-      if (TRIP) {
-        st[NS - 2][t][e] = -INFINITY;
-        st[NS - 1][t][e] = INFINITY;
-      }
-    }
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const Turn t = load_turn(n, tok[i] >= 0 ? tok[i] : 0, D, c);
-    uint4 y[2];
-    y[0] = norm_rope_row<CPR, HALVES>(xq[i], wq, t, n.eps);
-    y[1] = norm_rope_row<CPR, HALVES>(xk[i], wk, t, n.eps);
-    if (tok[i] < 0) y[0] = y[1] = zero;
-    const int64_t row = (tile * VSA_TILE + rg + RG * i) * D;
-    store_row<HALVES>(qp + row, D, c, y[0]);
-    store_row<HALVES>(kp + row, D, c, y[1]);
-    if (pool && tok[i] >= 0) {
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        float a[4], bb[4];
-        to_pairs<HALVES>(y[z], a, bb);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          st[0][z][j] += a[j];
-          st[0][z][4 + j] += bb[j];
-          if (TRIP) {
-            st[NS - 2][z][j] = fmaxf(st[NS - 2][z][j], a[j]);
-            st[NS - 2][z][4 + j] = fmaxf(st[NS - 2][z][4 + j], bb[j]);
-            st[NS - 1][z][j] = fminf(st[NS - 1][z][j], a[j]);
-            st[NS - 1][z][4 + j] = fminf(st[NS - 1][z][4 + j], bb[j]);
-          }
-        }
-      }
-    }
-  }
-  if (vt < 0) return;
-  if (!pool) {                                   // no such tile in this head
-    if (threadIdx.x < 2 * D)
-      for (int z = 0; z < NS; ++z)
-        (threadIdx.x / D ? pk : pq)[(int64_t(bh) * g.ntv_max + vt) * KD + z * D + threadIdx.x % D] = 0.f;
-    return;
-  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int vt = tile_n - g.n_pre_tiles;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint32_t base = tc::smem_u32(rows);
+
+  // Which token list head h uses: a head of another tile shape than the one before it
+  // fills the other list (the divisions cost more than a row's arithmetic: once per slot).
+  int list_next = 0;
+  auto same_tiles = [&](int a, int h) { return g.pt[a] == g.pt[h] && g.ph[a] == g.ph[h] && g.pw[a] == g.pw[h]; };
+  auto make_list = [&](int h) {                  // uniform over the CTA
+    if (h > h0) {
+      if (same_tiles(h - 1, h)) return;
+      list_next ^= 1;
+    }
+    if (threadIdx.x < VSA_TILE) toks[list_next][threadIdx.x] = src_token(g, h, tile_n, threadIdx.x);
+    __syncthreads();
+  };
+  auto request = [&](int h, int buf) {
+    const __nv_bfloat16* src[3] = {q, k, v};
 #pragma unroll
-  for (int o = CPR; o < 32; o <<= 1)
+    for (int z = 0; z < 3; ++z) {
+      const __nv_bfloat16* at = src[z] + b * n.st[z].batch + h * D + 8 * c;
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const int s = rg + RG * i, tok = toks[list_next][s];
+        cp_async16(base + buf * L::kBuf + z * L::kTensor + (s * D + 8 * c) * 2, at + (tok >= 0 ? tok : 0) * n.st[z].token,
+                   tok >= 0);
+      }
+    }
+  };
+  make_list(h0);
+  request(h0, 0);
+  cp_commit();
+  int list = 0;                                  // the list of the head at work
+  Turn turn[RPT];
+  Weights wq = load_weights<HALVES>(n.w_q, D, c), wk = load_weights<HALVES>(n.w_k, D, c);
+  for (int h = h0; h < h1; ++h) {
+    const int buf = (h - h0) & 1;
+    if (h == h0 || !same_tiles(h - 1, h)) {
+      list = list_next;                          // made when this head's rows were requested
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const int tok = toks[list][rg + RG * i];
+        turn[i] = load_turn(n, tok >= 0 ? tok : 0, D, c);
+      }
+    }
+    if (n.per_head) {
+      wq = load_weights<HALVES>(n.w_q ? n.w_q + h * D : nullptr, D, c);
+      wk = load_weights<HALVES>(n.w_k ? n.w_k + h * D : nullptr, D, c);
+    }
+    if (h + 1 < h1) {
+      make_list(h + 1);
+      request(h + 1, buf ^ 1);
+    }
+    cp_commit();
+    cp_wait<1>();                                // this head's rows
+    __syncwarp();                                // a row's chunks were requested by the lanes that share it
+    const int bh = b * g.Hh + h;
+    const int64_t tile = int64_t(bh) * g.nt_max + tile_n;
+    const bool pool = vt >= 0 && vt < g.ntv[h];  // uniform over the CTA
+    float st[NS][2][8];                          // [statistic][q, k][pair j: a, then b]
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        st[0][t][e] += __shfl_xor_sync(0xffffffffu, st[0][t][e], o);
+        st[0][t][e] = 0.f;
         if (TRIP) {
-          st[NS - 2][t][e] = fmaxf(st[NS - 2][t][e], __shfl_xor_sync(0xffffffffu, st[NS - 2][t][e], o));
-          st[NS - 1][t][e] = fminf(st[NS - 1][t][e], __shfl_xor_sync(0xffffffffu, st[NS - 1][t][e], o));
+          st[NS - 2][t][e] = -INFINITY;
+          st[NS - 1][t][e] = INFINITY;
         }
       }
-  if (lane < CPR) {
+    const __nv_bfloat16* sm = reinterpret_cast<const __nv_bfloat16*>(rows + buf * L::kBuf);
 #pragma unroll
-    for (int z = 0; z < NS; ++z)
+    for (int i = 0; i < RPT; ++i) {
+      const int s = rg + RG * i;
+      const bool on = toks[list][s] >= 0;
+      const int64_t row = (tile * VSA_TILE + s) * D;
+      uint4 y[2];
+      y[0] = norm_rope_row<CPR, HALVES>(row_of<HALVES>(sm + s * D, D, c), wq, turn[i], n.eps);
+      y[1] = norm_rope_row<CPR, HALVES>(row_of<HALVES>(sm + (VSA_TILE + s) * D, D, c), wk, turn[i], n.eps);
+      if (!on) y[0] = y[1] = zero;
+      store_row<HALVES>(qp + row, D, c, y[0]);
+      store_row<HALVES>(kp + row, D, c, y[1]);
+      reinterpret_cast<uint4*>(vp + row)[c] = *reinterpret_cast<const uint4*>(sm + (2 * VSA_TILE + s) * D + 8 * c);
+      if (pool && on) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+        for (int z = 0; z < 2; ++z) {
+          float a[4], bb[4];
+          to_pairs<HALVES>(y[z], a, bb);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) part[z][t][warp][channel_of<HALVES>(D, c, e & 3, e >> 2)] = st[z][t][e];
-  }
-  __syncthreads();
-  if (threadIdx.x < 2 * D) {
-    const int t = threadIdx.x / D, ch = threadIdx.x % D;
-    float sum = 0.f, mx = -INFINITY, mn = INFINITY;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      sum += part[0][t][w][ch];
-      if (TRIP) {
-        mx = fmaxf(mx, part[NS - 2][t][w][ch]);
-        mn = fminf(mn, part[NS - 1][t][w][ch]);
+          for (int j = 0; j < 4; ++j) {
+            st[0][z][j] += a[j];
+            st[0][z][4 + j] += bb[j];
+            if (TRIP) {
+              st[NS - 2][z][j] = fmaxf(st[NS - 2][z][j], a[j]);
+              st[NS - 2][z][4 + j] = fmaxf(st[NS - 2][z][4 + j], bb[j]);
+              st[NS - 1][z][j] = fminf(st[NS - 1][z][j], a[j]);
+              st[NS - 1][z][4 + j] = fminf(st[NS - 1][z][4 + j], bb[j]);
+            }
+          }
+        }
       }
     }
-    const float cnt = float(counts[h * g.nt_max + tile_n]);
-    float* out = (t ? pk : pq) + (int64_t(bh) * g.ntv_max + vt) * KD;
-    out[ch] = sum / cnt;
-    if (TRIP) {
-      out[D + ch] = mx;
-      out[2 * D + ch] = mn;
+    if (pool) {
+#pragma unroll
+      for (int o = CPR; o < 32; o <<= 1)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            st[0][t][e] += __shfl_xor_sync(0xffffffffu, st[0][t][e], o);
+            if (TRIP) {
+              st[NS - 2][t][e] = fmaxf(st[NS - 2][t][e], __shfl_xor_sync(0xffffffffu, st[NS - 2][t][e], o));
+              st[NS - 1][t][e] = fminf(st[NS - 1][t][e], __shfl_xor_sync(0xffffffffu, st[NS - 1][t][e], o));
+            }
+          }
+      __syncthreads();                           // every row is read: the partials take their place
+      float* part = reinterpret_cast<float*>(rows + buf * L::kBuf);   // [statistic][q, k][warp][D]
+      if (lane < CPR) {
+#pragma unroll
+        for (int z = 0; z < NS; ++z)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              part[((z * 2 + t) * 8 + warp) * D + channel_of<HALVES>(D, c, e & 3, e >> 2)] = st[z][t][e];
+      }
+      __syncthreads();
+      if (threadIdx.x < 2 * D) {
+        const int t = threadIdx.x / D, ch = threadIdx.x % D;
+        float sum = 0.f, mx = -INFINITY, mn = INFINITY;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          sum += part[(t * 8 + w) * D + ch];
+          if (TRIP) {
+            mx = fmaxf(mx, part[(((NS - 2) * 2 + t) * 8 + w) * D + ch]);
+            mn = fminf(mn, part[(((NS - 1) * 2 + t) * 8 + w) * D + ch]);
+          }
+        }
+        const float cnt = float(counts[h * g.nt_max + tile_n]);
+        float* out = (t ? pk : pq) + (int64_t(bh) * g.ntv_max + vt) * KD;
+        out[ch] = sum / cnt;
+        if (TRIP) {
+          out[D + ch] = mx;
+          out[2 * D + ch] = mn;
+        }
+      }
+    } else if (vt >= 0 && threadIdx.x < 2 * D) { // no such tile in this head
+      for (int z = 0; z < NS; ++z)
+        (threadIdx.x / D ? pk : pq)[(int64_t(bh) * g.ntv_max + vt) * KD + z * D + threadIdx.x % D] = 0.f;
     }
+    __syncthreads();                             // the buffer (and the other token list) may be filled again
   }
 }
 
@@ -513,13 +599,22 @@ cudaError_t launch_norm_rope(const vsa_plan* p, const NormRopeArgs& n, const voi
 cudaError_t launch_norm_rope_pack(const vsa_plan* p, const NormRopeArgs& n, const void* q, const void* k, const void* v,
                                   void* qp, void* kp, void* vp, float* pooled_q, float* pooled_k, cudaStream_t s) {
   const Geometry& g = p->geo;
-  const unsigned grid = unsigned(int64_t(g.B) * g.Hh * g.nt_max);
+  // Heads per CTA: up to eight, while two CTAs per SM still get four rounds of work.
+  int64_t run = int64_t(g.B) * g.Hh * g.nt_max / (int64_t(p->num_sms) * 8);
+  run = run < 1 ? 1 : run > 8 ? 8 : run;
+  const unsigned grid = unsigned(int64_t(g.B) * g.nt_max * ((g.Hh + run - 1) / run));
   const bool trip = p->desc.score_mode == VSA_SCORE_TRIPPOOL;
 #define VSA_RUN(CPR, HV, TR)                                                                                       \
-  norm_rope_pack_kernel<CPR, HV, TR><<<grid, 256, 0, s>>>(                                                          \
-      n, g, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),                            \
-      static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(qp), static_cast<__nv_bfloat16*>(kp),      \
-      static_cast<__nv_bfloat16*>(vp), p->d_tile_count, pooled_q, pooled_k)
+  do {                                                                                                             \
+    constexpr int smem = int(PackSmem<CPR, TR>::kBytes);                                                            \
+    const cudaError_t e = cudaFuncSetAttribute(norm_rope_pack_kernel<CPR, HV, TR>,                                  \
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);                 \
+    if (e != cudaSuccess) return e;                                                                                \
+    norm_rope_pack_kernel<CPR, HV, TR><<<grid, 256, smem, s>>>(                                                     \
+        n, g, int(run), static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),                \
+        static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(qp), static_cast<__nv_bfloat16*>(kp),    \
+        static_cast<__nv_bfloat16*>(vp), p->d_tile_count, pooled_q, pooled_k);                                     \
+  } while (0)
   if (g.d == 128) {
     if (n.halves) {
       if (trip) VSA_RUN(16, true, true);
