@@ -139,6 +139,29 @@ def test_pack_equals_forward_then_pack(name, layout):
     assert np.array_equal(bf16_to_f64(one["qp"]), want)
 
 
+def test_pack_of_many_heads_per_block():
+    """Enough tiles that a block works through several heads, equal and different shapes in turn."""
+    import torch
+    shapes = ((4, 4, 4), (4, 4, 4), (1, 8, 8), (1, 8, 8), (1, 8, 8), (16, 2, 2), (2, 4, 8), (4, 4, 4), (2, 4, 8),
+              (2, 4, 8), (16, 2, 2), (4, 4, 4), (8, 4, 2))
+    cfg = LayerConfig(name="many", batch=1, heads=13, head_dim=64, T=18, H=46, W=78, segments=(77, 512),
+                      tile_shapes=shapes, score_mode="tripool", proj_dim=64, sparsity=(0.5,), seed=6)
+    c = Case(cfg, "interleaved", True)
+    p = c.plan
+    qo, ko = (torch.empty(c.shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    p.qk_norm_rope(c.q, c.k, c.norm, qo, ko)
+    two, one = p.allocate(), p.allocate()
+    two["workspace"].zero_()
+    one["workspace"].fill_(1)
+    p.tile_pack_pool(qo, ko, c.v.contiguous(), two["qp"], two["kp"], two["vp"], two["workspace"])
+    p.tile_norm_rope_pack_pool(c.q, c.k, c.v, c.norm, one["qp"], one["kp"], one["vp"], one["workspace"])
+    p.check()
+    for x in ("qp", "kp", "vp"):
+        assert torch.equal(two[x].view(torch.int16), one[x].view(torch.int16)), x
+    for a, b in zip(p.pooled(two["workspace"]), p.pooled(one["workspace"])):
+        assert torch.equal(a, b)
+
+
 def check_backward(c, i, dy, dx, dw):
     x, d = bf16_to_f64((c.q, c.k)[i]), c.shape[3]
     want, dw_want, dw_abs = BO.norm_rope_grad(dy, x, c.w[i], c.cos, c.sin, c.layout, EPS, c.per_head)

@@ -32,6 +32,7 @@ namespace {
 using tc::f2pack;
 using tc::f2unpack;
 using tc::fadd2;
+using tc::ffma2;
 using tc::fmul2;
 
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
@@ -186,6 +187,15 @@ __device__ __forceinline__ uint4 norm_rope_row(uint4 v, const Weights& w, const 
   return from_pairs<HALVES>(a, b);
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {   // off: sixteen zero bytes
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Token-major to token-major. One warp per token; its 32 / CPR lane groups
 // walk the heads, so the token's table row is loaded once for all heads.
 // Results may overwrite their inputs: a row is read before it is written, by
@@ -225,15 +235,6 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(NormRopeArgs n, int B, i
       }
     }
   }
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {   // off: sixteen zero bytes
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Fused with the pack and the pooling: one CTA of 256 threads per (batch, tile, a
@@ -427,32 +428,38 @@ __global__ void __launch_bounds__(256, 2)
   }
 }
 
-// Gradient rows: dx from dy and x, and the row's share of dw.
+// Gradient rows: dx from dy and x, and the row's share of dw, two pairs at a time in packed fp32.
 template <int CPR, bool HALVES>
 __device__ __forceinline__ uint4 norm_rope_grad_row(uint4 vy, uint4 vx, const Weights& w, const Turn& t, float eps,
-                                                    float (&dwa)[4], float (&dwb)[4]) {
+                                                    uint64_t (&dwa)[2], uint64_t (&dwb)[2]) {
   float xa[4], xb[4], ya[4], yb[4];
   to_pairs<HALVES>(vx, xa, xb);
   to_pairs<HALVES>(vy, ya, yb);
   const float r = rsqrtf(square_sum<CPR, HALVES>(xa, xb) * (1.f / (CPR * 8)) + eps);
-  float dot = 0.f;
+  const uint64_t r2 = f2pack(r, r);
+  uint64_t ra[2], rb[2], ga[2], gb[2], dot = 0ull;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float da = fmaf(ya[j], t.c[j], yb[j] * t.s[j]);
-    const float db = fmaf(yb[j], t.c[j], -ya[j] * t.s[j]);
-    xa[j] *= r;
-    xb[j] *= r;
-    dwa[j] = fmaf(da, xa[j], dwa[j]);
-    dwb[j] = fmaf(db, xb[j], dwb[j]);
-    ya[j] = da * w.a[j];
-    yb[j] = db * w.b[j];
-    dot = fmaf(ya[j], xa[j], fmaf(yb[j], xb[j], dot));
+  for (int j = 0; j < 2; ++j) {
+    const uint64_t c = f2pack(t.c[2 * j], t.c[2 * j + 1]), s = f2pack(t.s[2 * j], t.s[2 * j + 1]);
+    const uint64_t y0 = f2pack(ya[2 * j], ya[2 * j + 1]), y1 = f2pack(yb[2 * j], yb[2 * j + 1]);
+    const uint64_t da = ffma2(y0, c, fmul2(y1, s));
+    const uint64_t db = ffma2(y1, c, fmul2(y0, s) ^ 0x8000000080000000ull);
+    ra[j] = fmul2(f2pack(xa[2 * j], xa[2 * j + 1]), r2);
+    rb[j] = fmul2(f2pack(xb[2 * j], xb[2 * j + 1]), r2);
+    dwa[j] = ffma2(da, ra[j], dwa[j]);
+    dwb[j] = ffma2(db, rb[j], dwb[j]);
+    ga[j] = fmul2(da, f2pack(w.a[2 * j], w.a[2 * j + 1]));
+    gb[j] = fmul2(db, f2pack(w.b[2 * j], w.b[2 * j + 1]));
+    dot = ffma2(ga[j], ra[j], ffma2(gb[j], rb[j], dot));
   }
-  const float m = row_sum<CPR>(dot) * (1.f / (CPR * 8));
+  float d0, d1;
+  f2unpack(dot, d0, d1);
+  const float m = -row_sum<CPR>(d0 + d1) * (1.f / (CPR * 8));
+  const uint64_t m2 = f2pack(m, m);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    ya[j] = r * fmaf(-xa[j], m, ya[j]);
-    yb[j] = r * fmaf(-xb[j], m, yb[j]);
+  for (int j = 0; j < 2; ++j) {
+    f2unpack(fmul2(r2, ffma2(ra[j], m2, ga[j])), ya[2 * j], ya[2 * j + 1]);
+    f2unpack(fmul2(r2, ffma2(rb[j], m2, gb[j])), yb[2 * j], yb[2 * j + 1]);
   }
   return from_pairs<HALVES>(ya, yb);
 }
@@ -463,76 +470,147 @@ __device__ __forceinline__ uint4 norm_rope_grad_row(uint4 vy, uint4 vx, const We
 // PACKED: dy (and dv, which is only moved) come from packed tiles. The blocks'
 // partial sums of dw go to `part` [blockIdx.y][blockIdx.x][q, k][d], summed in
 // block order by the kernel below: no atomics, the same result every time.
+// Bound by HBM: a warp's next step (32 / CPR rows of every input) is requested into
+// shared memory while this one is worked on, across tokens too; with one step's
+// loads in registers the clip took 1.08 ms.
+template <int CPR, bool PACKED>
+struct GradSmem {
+  static constexpr int kIn = PACKED ? 5 : 4;                   // dy_q, dy_k, q, k (, dv)
+  static constexpr uint32_t kStep = kIn * 512;                 // one warp's step: 32 chunks of each input
+  static constexpr uint32_t oRed = 8 * 2 * kStep;
+  static constexpr uint32_t oRow = oRed + 8 * 2 * CPR * 8 * 4;
+  static constexpr uint32_t kBytes = oRow + 8 * 2 * VSA_MAX_HEADS * 4;
+};
 template <int CPR, bool HALVES, bool PACKED, bool PER_HEAD>
-__global__ void __launch_bounds__(256) norm_rope_bwd_kernel(NormRopeArgs n, Geometry g, const __nv_bfloat16* dyq,
-                                                            const __nv_bfloat16* dyk, const __nv_bfloat16* dyv,
-                                                            const __nv_bfloat16* q, const __nv_bfloat16* k,
-                                                            __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv,
-                                                            float* part) {
+__global__ void __launch_bounds__(256, 2) norm_rope_bwd_kernel(NormRopeArgs n, Geometry g, const __nv_bfloat16* dyq,
+                                                               const __nv_bfloat16* dyk, const __nv_bfloat16* dyv,
+                                                               const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                                               __nv_bfloat16* dq, __nv_bfloat16* dk,
+                                                               __nv_bfloat16* dv, float* part) {
   constexpr int D = CPR * 8, G = 32 / CPR;
-  __shared__ float red[8][2][D];
-  __shared__ int32_t prow[PACKED && !PER_HEAD ? 8 : 1][VSA_MAX_HEADS];
+  using L = GradSmem<CPR, PACKED>;
+  extern __shared__ __align__(16) uint8_t sm[];
   const int lane = threadIdx.x & 31, c = lane % CPR, grp = lane / CPR, warp = threadIdx.x >> 5;
+  uint8_t* stage = sm + warp * 2 * L::kStep;
+  int32_t* prow = reinterpret_cast<int32_t*>(sm + L::oRow) + warp * 2 * VSA_MAX_HEADS;   // [token parity][head]
   const int64_t woff = PER_HEAD && n.per_head ? int64_t(blockIdx.y) * D : 0;
   const Weights wq = load_weights<HALVES>(n.w_q ? n.w_q + woff : nullptr, D, c);
   const Weights wk = load_weights<HALVES>(n.w_k ? n.w_k + woff : nullptr, D, c);
-  float acc[2][2][4] = {};                       // [q, k][a, b][pair]
+  uint64_t acc[2][2][2] = {}, tok_acc[2][2][2] = {};   // [q, k][a, b][two pairs]; a token's own sum first: shorter chains
   const int64_t total = int64_t(g.B) * g.n_tokens;
   constexpr int TPW = PER_HEAD ? G : 1;          // tokens per warp and step
-  for (int64_t t0 = (int64_t(blockIdx.x) * 8 + warp) * TPW; t0 < total; t0 += int64_t(gridDim.x) * 8 * TPW) {
-    const int64_t tk = PER_HEAD ? t0 + grp : t0;
-    const bool real = tk < total;
-    const int b = int((real ? tk : 0) / g.n_tokens), tok = int((real ? tk : 0) - int64_t(b) * g.n_tokens);
-    const Turn t = load_turn(n, tok, D, c);
-    if constexpr (PACKED && !PER_HEAD) {
-      __syncwarp();                              // the previous token's rows are read
-      for (int h = lane; h < g.Hh; h += 32) prow[warp][h] = packed_row(g, h, tok);
-      __syncwarp();
+  const int64_t first = (int64_t(blockIdx.x) * 8 + warp) * TPW + (PER_HEAD ? grp : 0);
+  const int dt = int(gridDim.x) * 8 * TPW;
+  const int steps = PER_HEAD ? 1 : (g.Hh + G - 1) / G;         // per token
+
+  // A place in the walk: this lane's token (a lane group's own with PER_HEAD) and, among
+  // its steps, the head. left: tokens of the whole walk from here, which decides
+  // alike for all lanes; on: this lane has a row.
+  struct At {
+    int b, tok, step;
+    int64_t left;
+  };
+  auto advance = [&](At& a) {                    // the next step, or the next token without a division
+    if (++a.step < steps) return;
+    a.step = 0;
+    a.left -= dt;
+    a.tok += dt;
+    while (a.tok >= g.n_tokens) {
+      a.tok -= g.n_tokens;
+      ++a.b;
     }
-    float tok_acc[2][2][4] = {};                 // the token's own sum first: shorter fp32 chains
-    for (int h0 = 0; h0 < (PER_HEAD ? 1 : g.Hh); h0 += G) {
-      const int h = PER_HEAD ? int(blockIdx.y) : h0 + grp;
-      const bool on = real && h < g.Hh;
-      uint4 yq = make_uint4(0, 0, 0, 0), yk = yq, yv = yq, xq = yq, xk = yq;
-      if (on) {
-        if constexpr (PACKED) {
-          const int pr = PER_HEAD ? packed_row(g, h, tok) : prow[PER_HEAD ? 0 : warp][h];
-          const int64_t row = (int64_t(b * g.Hh + h) * g.nt_max * VSA_TILE + pr) * D;
-          yq = load_row<HALVES>(dyq + row, D, c);
-          yk = load_row<HALVES>(dyk + row, D, c);
-          yv = __ldcs(reinterpret_cast<const uint4*>(dyv + row) + c);
-        } else {
-          yq = load_row<HALVES>(dyq + b * n.st[5].batch + tok * n.st[5].token + h * D, D, c);
-          yk = load_row<HALVES>(dyk + b * n.st[6].batch + tok * n.st[6].token + h * D, D, c);
-        }
-        xq = load_row<HALVES>(q + b * n.st[0].batch + tok * n.st[0].token + h * D, D, c);
-        xk = load_row<HALVES>(k + b * n.st[1].batch + tok * n.st[1].token + h * D, D, c);
+  };
+  auto head_of = [&](const At& a) { return PER_HEAD ? int(blockIdx.y) : a.step * G + grp; };
+  auto on = [&](const At& a) { return a.b < g.B && head_of(a) < g.Hh; };
+  auto more = [&](const At& a) { return a.left > 0; };
+  auto request = [&](const At& a, uint32_t parity, int buf) {   // warp-wide
+    const bool is_on = on(a);
+    const int h = is_on ? head_of(a) : 0, bb = is_on ? a.b : 0, tok = is_on ? a.tok : 0;
+    if constexpr (PACKED && !PER_HEAD) {
+      if (a.step == 0) {                         // a new token: every head's packed row
+        for (int i = lane; i < g.Hh; i += 32) prow[parity * VSA_MAX_HEADS + i] = packed_row(g, i, a.tok);
+        __syncwarp();
       }
-      yq = norm_rope_grad_row<CPR, HALVES>(yq, xq, wq, t, n.eps, tok_acc[0][0], tok_acc[0][1]);
-      yk = norm_rope_grad_row<CPR, HALVES>(yk, xk, wk, t, n.eps, tok_acc[1][0], tok_acc[1][1]);
-      if (on) {
-        store_row<HALVES>(dq + b * n.st[2].batch + tok * n.st[2].token + h * D, D, c, yq);
-        store_row<HALVES>(dk + b * n.st[3].batch + tok * n.st[3].token + h * D, D, c, yk);
+    }
+    const __nv_bfloat16* src[5];
+    if constexpr (PACKED) {
+      const int pr = PER_HEAD ? packed_row(g, h, tok) : prow[parity * VSA_MAX_HEADS + h];
+      const int64_t row = (int64_t(bb * g.Hh + h) * g.nt_max * VSA_TILE + pr) * D;
+      src[0] = dyq + row;
+      src[1] = dyk + row;
+      src[4] = dyv + row;
+    } else {
+      src[0] = dyq + bb * n.st[5].batch + tok * n.st[5].token + h * D;
+      src[1] = dyk + bb * n.st[6].batch + tok * n.st[6].token + h * D;
+    }
+    src[2] = q + bb * n.st[0].batch + tok * n.st[0].token + h * D;
+    src[3] = k + bb * n.st[1].batch + tok * n.st[1].token + h * D;
+    const uint32_t dst = tc::smem_u32(stage + buf * L::kStep) + lane * 16;
+#pragma unroll
+    for (int z = 0; z < L::kIn; ++z) cp_async16(dst + z * 512, src[z] + 8 * c, is_on);
+    cp_commit();
+  };
+
+  At now;
+  now.b = int(first / g.n_tokens);
+  now.tok = int(first - int64_t(now.b) * g.n_tokens);
+  now.step = 0;
+  now.left = total - (first - (PER_HEAD ? grp : 0));
+  At next = now;                                 // the step to request next
+  uint32_t parity = 0;
+  auto request_next = [&](int buf) {
+    request(next, parity, buf);
+    advance(next);
+    if (next.step == 0) parity ^= 1;
+  };
+  if (more(next)) request_next(0);
+  int buf = 0;
+  while (more(now)) {
+    const Turn turn = load_turn(n, now.b < g.B ? now.tok : 0, D, c);
+    for (int step = 0; step < steps; ++step, buf ^= 1) {
+      if (more(next)) request_next(buf ^ 1);
+      else cp_commit();                          // empty: the count of groups stays in step
+      cp_wait<1>();
+      __syncwarp();
+      // lane group grp's row of input z: 16 * CPR bytes
+      const uint8_t* in = stage + buf * L::kStep + grp * CPR * 16;
+      auto row = [&](int z) { return row_of<HALVES>(reinterpret_cast<const __nv_bfloat16*>(in + z * 512), D, c); };
+      const uint4 yq = norm_rope_grad_row<CPR, HALVES>(row(0), row(2), wq, turn, n.eps, tok_acc[0][0], tok_acc[0][1]);
+      const uint4 yk = norm_rope_grad_row<CPR, HALVES>(row(1), row(3), wk, turn, n.eps, tok_acc[1][0], tok_acc[1][1]);
+      if (on(now)) {
+        const int off = head_of(now) * D;
+        store_row<HALVES>(dq + now.b * n.st[2].batch + now.tok * n.st[2].token + off, D, c, yq);
+        store_row<HALVES>(dk + now.b * n.st[3].batch + now.tok * n.st[3].token + off, D, c, yk);
         if constexpr (PACKED)
-          reinterpret_cast<uint4*>(dv + b * n.st[4].batch + tok * n.st[4].token + h * D)[c] = yv;
+          reinterpret_cast<uint4*>(dv + now.b * n.st[4].batch + now.tok * n.st[4].token + off)[c] =
+              *reinterpret_cast<const uint4*>(in + 4 * 512 + 16 * c);
       }
+      __syncwarp();                              // the buffer may be filled again
+      advance(now);
     }
 #pragma unroll
     for (int z = 0; z < 2; ++z)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[z][m][j] += tok_acc[z][m][j];
+        for (int j = 0; j < 2; ++j) {
+          acc[z][m][j] = fadd2(acc[z][m][j], tok_acc[z][m][j]);
+          tok_acc[z][m][j] = 0ull;
+        }
   }
+  float(*red)[2][D] = reinterpret_cast<float(*)[2][D]>(sm + L::oRed);
 #pragma unroll
   for (int z = 0; z < 2; ++z)
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        float v[2];
+        f2unpack(acc[z][m][j >> 1], v[0], v[1]);
+        float x = v[j & 1];
 #pragma unroll
-        for (int o = CPR; o < 32; o <<= 1) acc[z][m][j] += __shfl_xor_sync(0xffffffffu, acc[z][m][j], o);
-        if (lane < CPR) red[warp][z][channel_of<HALVES>(D, c, j, m)] = acc[z][m][j];
+        for (int o = CPR; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane < CPR) red[warp][z][channel_of<HALVES>(D, c, j, m)] = x;
       }
   __syncthreads();
   if (threadIdx.x < 2 * D) {
@@ -562,14 +640,15 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
   }
 }
 
-// Blocks along x of the gradient kernel: one step of eight warps at least, four
-// blocks per SM at most (weights per head: shared among the heads).
+// Blocks along x of the gradient kernel: one token for each of eight warps (or their
+// lane groups) at least, what is resident at once, two blocks per SM, at most
+// (weights per head: shared among the heads).
 int bwd_blocks(const vsa_plan* p, bool per_head) {
   const Geometry& g = p->geo;
   const int64_t tokens = int64_t(g.B) * g.n_tokens;
   const int tpb = per_head ? 8 * (32 / (g.d / 8)) : 8;
   const int64_t want = (tokens + tpb - 1) / tpb;
-  const int64_t cap = per_head ? (int64_t(p->num_sms) * 4 + g.Hh - 1) / g.Hh : int64_t(p->num_sms) * 4;
+  const int64_t cap = per_head ? (int64_t(p->num_sms) * 2 + g.Hh - 1) / g.Hh : int64_t(p->num_sms) * 2;
   return int(want < cap ? want : cap);
 }
 
@@ -649,11 +728,17 @@ cudaError_t launch_norm_rope_bwd(const vsa_plan* p, const NormRopeArgs& n, bool 
   const dim3 grid(nb, n.per_head ? g.Hh : 1);
   float* part = static_cast<float*>(workspace);
 #define VSA_RUN(CPR, HV, PK, PH)                                                                                   \
-  norm_rope_bwd_kernel<CPR, HV, PK, PH><<<grid, 256, 0, s>>>(                                                       \
-      n, g, static_cast<const __nv_bfloat16*>(dyq), static_cast<const __nv_bfloat16*>(dyk),                        \
-      static_cast<const __nv_bfloat16*>(dyv), static_cast<const __nv_bfloat16*>(q),                                \
-      static_cast<const __nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk),      \
-      static_cast<__nv_bfloat16*>(dv), part)
+  do {                                                                                                             \
+    constexpr int smem = int(GradSmem<CPR, PK>::kBytes);                                                            \
+    const cudaError_t e = cudaFuncSetAttribute(norm_rope_bwd_kernel<CPR, HV, PK, PH>,                               \
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);                 \
+    if (e != cudaSuccess) return e;                                                                                \
+    norm_rope_bwd_kernel<CPR, HV, PK, PH><<<grid, 256, smem, s>>>(                                                  \
+        n, g, static_cast<const __nv_bfloat16*>(dyq), static_cast<const __nv_bfloat16*>(dyk),                      \
+        static_cast<const __nv_bfloat16*>(dyv), static_cast<const __nv_bfloat16*>(q),                              \
+        static_cast<const __nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk),    \
+        static_cast<__nv_bfloat16*>(dv), part);                                                                    \
+  } while (0)
 #define VSA_RUN2(CPR, HV)                  \
   do {                                     \
     if (packed) {                          \
