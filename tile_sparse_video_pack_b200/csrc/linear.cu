@@ -59,19 +59,25 @@ __device__ __forceinline__ void act_fwd(float (&v)[8], int act) {
     f2unpack(fmul2(z, f2pack(rcp(x0), rcp(x1))), v[i], v[i + 1]);
   }
 }
-// act(z) and act'(z), with the accurate exponential: they go into fp32 sums.
-__device__ __forceinline__ void act_both(float z, int act, float& f, float& df) {
+// act(z) and act'(z) of two elements: with s = sigmoid(u), f = z s and
+// f' = s + f (1 - s) u' (SiLU: u = z; GELU: u the 2u above).
+__device__ __forceinline__ void act_both(uint64_t z, int act, uint64_t& f, uint64_t& df) {
+  const uint64_t one = f2pack(1.f, 1.f);
   if (act == VSA_ACT_NONE) {
     f = z;
-    df = 1.f;
+    df = one;
     return;
   }
   const bool gelu = act == VSA_ACT_GELU_TANH;
-  const float u = gelu ? kGeluB * z * fmaf(0.044715f * z, z, 1.f) : z;
-  const float du = gelu ? kGeluB * fmaf(3.f * 0.044715f * z, z, 1.f) : 1.f;
-  const float s = 1.f / (1.f + expf(-u));
-  f = z * s;
-  df = fmaf(f * (1.f - s), du, s);
+  const float c1 = gelu ? kGeluB : 1.f, c3 = gelu ? 0.044715f * kGeluB : 0.f;
+  const uint64_t z2 = fmul2(z, z), l = f2pack(-kLog2e, -kLog2e);
+  float x0, x1;
+  f2unpack(fmul2(fmul2(z, l), ffma2(z2, f2pack(c3, c3), f2pack(c1, c1))), x0, x1);
+  f2unpack(fadd2(f2pack(ex2(x0), ex2(x1)), one), x0, x1);
+  const uint64_t s = f2pack(rcp(x0), rcp(x1));
+  f = fmul2(z, s);
+  const uint64_t du = ffma2(z2, f2pack(3.f * c3, 3.f * c3), f2pack(c1, c1));
+  df = ffma2(fmul2(f, ffma2(s, f2pack(-1.f, -1.f), one)), du, s);
 }
 
 // -------------------------------------------------------------- epilogue ----
@@ -267,6 +273,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
   constexpr uint32_t kCols = 2 * kBN;            // two accumulators
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < prm.n_prod; ++i) {
+      prefetch_map(&maps.a[i]);
+      prefetch_map(&maps.b[i]);
+    }
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(bar(G_FULL + i), 1);
       mbar_init(bar(G_EMPTY + i), 1);
@@ -288,6 +298,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
+  allow_successor();
+  wait_predecessor();
 
   uint32_t it = 0, n = 0;                        // k blocks and tiles so far, counted alike by every role
   bool ok = true;
@@ -370,15 +382,20 @@ __global__ void __launch_bounds__(kGThreads, 1)
           if (row >= pr.M || col >= pr.N) continue;
           const uint32_t lo = sbase + rr * (kBN * 4) + ((2 * cg) ^ (rr & 7)) * 16;
           const uint32_t hi = sbase + rr * (kBN * 4) + ((2 * cg + 1) ^ (rr & 7)) * 16;
+          float4 x[8], y[8];                     // all loads before the first sum: each takes about a microsecond
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            if (s < splits) {
+              x[s] = ld_cluster(map_to_rank(lo, s));
+              y[s] = ld_cluster(map_to_rank(hi, s));
+            }
           float v[8] = {};
-#pragma unroll 4
-          for (int s = 0; s < splits; ++s) {
-            // a CTA whose share of K is empty has no accumulator
-            if (int64_t(pr.kblocks) * s / splits == int64_t(pr.kblocks) * (s + 1) / splits) continue;
-            const float4 x = ld_cluster(map_to_rank(lo, s)), y = ld_cluster(map_to_rank(hi, s));
-            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-          }
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            if (s < splits) {
+              v[0] += x[s].x; v[1] += x[s].y; v[2] += x[s].z; v[3] += x[s].w;
+              v[4] += y[s].x; v[5] += y[s].y; v[6] += y[s].z; v[7] += y[s].w;
+            }
           store8(pr.ep, row, col, v, b);
         }
       }
@@ -396,7 +413,6 @@ __global__ void __launch_bounds__(kGThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if constexpr (SPLIT) cluster_sync();
   tc_fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
 }
@@ -436,6 +452,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   const bool a_mn = pr.a_mn, b_mn = pr.b_mn;
 
   if (threadIdx.x == 0) {
+    prefetch_map(&maps.a[0]);
+    prefetch_map(&maps.b[0]);
     for (int i = 0; i < kPStages; ++i) {
       mbar_init(bar(G_FULL + i), 1);
       mbar_init(bar(G_EMPTY + i), 1);
@@ -457,6 +475,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   cluster_sync();                                // the pair's barriers and TMEM are ready
   tc_fence_after();
   const uint32_t tmem = misc[0];
+  allow_successor();
+  wait_predecessor();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -547,6 +567,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
+// A few rows (a timestep's conditioning, single tokens): bound by reading W once, which
+// the tensor cores' 128-row tiles do with a few CTAs only. A warp takes F output
+// columns (rows of W) and strides over K, 16 bytes per lane and load, against R
+// rows of x; the products of neighbouring k are kept as packed pairs. KS = 8: the
+// block's eight warps share K instead, for few columns. fp32 throughout.
+template <int R, int F, int KS>
+__global__ void __launch_bounds__(256) skinny_kernel(const __nv_bfloat16* __restrict__ x, int64_t ld_x,
+                                                     const __nv_bfloat16* __restrict__ w, int rows, int K, int N,
+                                                     const __grid_constant__ Epilogue ep) {
+  __shared__ float part[KS > 1 ? 8 : 1][R * F];
+  allow_successor();
+  wait_predecessor();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n0 = (KS > 1 ? int(blockIdx.x) : int(blockIdx.x) * 8 + warp) * F;
+  uint64_t acc[F][R] = {};
+  if (n0 < N) {
+    const __nv_bfloat16* wp[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) wp[f] = w + int64_t(n0 + f < N ? n0 + f : n0) * K;
+    const __nv_bfloat16* xp[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) xp[r] = x + int64_t(r < rows ? r : 0) * ld_x;
+#pragma unroll 2
+    for (int k = (KS > 1 ? warp * 32 + lane : lane) * 8; k < K; k += 256 * KS) {   // K is a multiple of eight
+      uint4 wv[F], xv[R];
+#pragma unroll
+      for (int f = 0; f < F; ++f) wv[f] = __ldcs(reinterpret_cast<const uint4*>(wp[f] + k));
+#pragma unroll
+      for (int r = 0; r < R; ++r) xv[r] = __ldg(reinterpret_cast<const uint4*>(xp[r] + k));
+      float xf[R][8];
+#pragma unroll
+      for (int r = 0; r < R; ++r) bf16x8_to_f32(xv[r], xf[r]);
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        float wf[8];
+        bf16x8_to_f32(wv[f], wf);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < 8; i += 2)
+            acc[f][r] = ffma2(f2pack(wf[i], wf[i + 1]), f2pack(xf[r][i], xf[r][i + 1]), acc[f][r]);
+      }
+    }
+  }
+  // lane f * R + r ends up with the sum of column f and row r
+  float mine = 0.f;
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float lo, hi;
+      f2unpack(acc[f][r], lo, hi);
+      float s = lo + hi;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == f * R + r) mine = s;
+    }
+  if constexpr (KS > 1) {
+    if (lane < R * F) part[warp][lane] = mine;
+    __syncthreads();
+    if (warp != 0) return;
+    mine = 0.f;
+    if (lane < R * F)
+      for (int i = 0; i < 8; ++i) mine += part[i][lane];
+  }
+  const int col = n0 + lane / R, row = lane % R;
+  if (lane >= R * F || col >= N || row >= rows) return;
+  float v[8] = {mine + (ep.bias ? __ldg(ep.bias + col) : 0.f)};
+  if (ep.pre) ep.pre[row * ep.ld_pre + col] = __float2bfloat16_rn(v[0]);
+  act_fwd(v, ep.act);
+  if (ep.gate) v[0] *= __ldg(ep.gate + (row / ep.rows_per_gate) * ep.ld_gate + col);
+  if (ep.residual) v[0] += __bfloat162float(ep.residual[row * ep.ld_res + col]);
+  ep.out[row * ep.ld_out + col] = __float2bfloat16_rn(v[0]);
+}
+
 // ----------------------------------------------------- gradient of the rest ----
 
 struct GradParams {
@@ -560,9 +655,12 @@ struct GradParams {
 
 // dz and the column sums in one pass. A block takes 256 columns (32 lanes of
 // eight) of one chunk of rows, which lies in one sample; its eight warps take
-// every eighth row and meet in shared memory.
+// every eighth row, four at a time so that enough loads are in flight (one row at a time
+// and the library's exponential and division: 238 us at 9,280 x 8192, where the bytes take 70),
+// and meet in shared memory.
 __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ GradParams p) {
   __shared__ float red[2][8][256];
+  allow_successor();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = int(blockIdx.y) * 256 + lane * 8;
   const int64_t sample = blockIdx.x / p.chunks_per_sample;
@@ -571,37 +669,56 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
   int64_t r1 = r0 + p.chunk;
   if (r1 > end) r1 = end;
   if (r1 > p.rows) r1 = p.rows;
-  float sz[8] = {}, sg[8] = {}, gt[8];
+  uint64_t sz[4] = {}, sg[4] = {}, gt[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) gt[i] = 1.f;
+  for (int i = 0; i < 4; ++i) gt[i] = f2pack(1.f, 1.f);
   const bool on = col < p.N;
-  if (on && p.gate) load8(p.gate + sample * p.N + col, gt);
+  if (on && p.gate) {
+    float g[8];
+    load8(p.gate + sample * p.N + col, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gt[i] = f2pack(g[2 * i], g[2 * i + 1]);
+  }
   if (on) {
-    for (int64_t r = r0 + warp; r < r1; r += 8) {
-      float dy[8], z[8];
-      bf16x8_to_f32(__ldcs(reinterpret_cast<const uint4*>(p.dy + r * p.ld_dy + col)), dy);
-      if (p.pre) {
-        bf16x8_to_f32(__ldcs(reinterpret_cast<const uint4*>(p.pre + r * p.ld_pre + col)), z);
+    constexpr int U = 4;
+    for (int64_t r = r0 + warp; r < r1; r += 8 * U) {
+      uint4 vy[U], vz[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float f, df;
-          act_both(z[i], p.act, f, df);
-          sg[i] = fmaf(dy[i], f, sg[i]);
-          dy[i] *= gt[i] * df;
+      for (int u = 0; u < U; ++u) {
+        const int64_t rr = r + 8 * u;
+        if (rr < r1) {
+          vy[u] = __ldcs(reinterpret_cast<const uint4*>(p.dy + rr * p.ld_dy + col));
+          if (p.pre) vz[u] = __ldcs(reinterpret_cast<const uint4*>(p.pre + rr * p.ld_pre + col));
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dy[i] *= gt[i];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sz[i] += dy[i];
-      if (p.dz) *reinterpret_cast<uint4*>(p.dz + r * p.N + col) = to_bf16x8(dy);
+      for (int u = 0; u < U; ++u) {
+        const int64_t rr = r + 8 * u;
+        if (rr >= r1) break;
+        float dy[8], z[8];
+        bf16x8_to_f32(vy[u], dy);
+        if (p.pre) bf16x8_to_f32(vz[u], z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint64_t d = f2pack(dy[2 * i], dy[2 * i + 1]), f, df;
+          if (p.pre) {
+            act_both(f2pack(z[2 * i], z[2 * i + 1]), p.act, f, df);
+            sg[i] = ffma2(d, f, sg[i]);
+            d = fmul2(fmul2(d, gt[i]), df);
+          } else {
+            d = fmul2(d, gt[i]);
+          }
+          sz[i] = fadd2(sz[i], d);
+          f2unpack(d, dy[2 * i], dy[2 * i + 1]);
+        }
+        if (p.dz) *reinterpret_cast<uint4*>(p.dz + rr * p.N + col) = to_bf16x8(dy);
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    red[0][warp][lane * 8 + i] = sz[i];
-    red[1][warp][lane * 8 + i] = sg[i];
+  for (int i = 0; i < 4; ++i) {
+    f2unpack(sz[i], red[0][warp][lane * 8 + 2 * i], red[0][warp][lane * 8 + 2 * i + 1]);
+    f2unpack(sg[i], red[1][warp][lane * 8 + 2 * i], red[1][warp][lane * 8 + 2 * i + 1]);
   }
   __syncthreads();
   const int c = int(blockIdx.y) * 256 + threadIdx.x;
@@ -625,6 +742,8 @@ __global__ void __launch_bounds__(256) linear_colsum_kernel(const float* __restr
   __shared__ double red[8][32];
   const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
   const int col = int(blockIdx.y) * 32 + lane;
+  allow_successor();
+  wait_predecessor();
   const bool is_bias = int(blockIdx.x) == samples;
   const float* src = is_bias ? part_z : part_g;
   float* dst = is_bias ? dbias : dgate;
@@ -714,7 +833,9 @@ cudaError_t run_products(const vsa_plan* p, const Problem* q, int n, cudaStream_
     const cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int most = p->num_sms / 2;
-    gemm_pair_kernel<<<2 * (prm.units < most ? prm.units : most), kGThreads, smem, s>>>(maps, prm);
+    const cudaError_t r = launch_after(gemm_pair_kernel, dim3(2 * unsigned(prm.units < most ? prm.units : most)), kGThreads,
+                                       size_t(smem), s, 1, maps, prm);
+    if (r != cudaSuccess) return r;
   }
   start();
   int kb = 1 << 30;                              // k blocks of the shortest product
@@ -734,23 +855,38 @@ cudaError_t run_products(const vsa_plan* p, const Problem* q, int n, cudaStream_
   if (prm.splits == 1) {
     const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    gemm_kernel<false><<<prm.units < p->num_sms ? prm.units : p->num_sms, kGThreads, smem, s>>>(maps, prm);
-    return cudaGetLastError();
+    return launch_after(gemm_kernel<false>, dim3(unsigned(prm.units < p->num_sms ? prm.units : p->num_sms)), kGThreads,
+                        size_t(smem), s, 1, maps, prm);
   }
   const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = unsigned(prm.splits);
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(prm.units * prm.splits));
-  cfg.blockDim = dim3(kGThreads);
-  cfg.dynamicSmemBytes = size_t(smem);
-  cfg.stream = s;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<true>, maps, prm);
+  return launch_after(gemm_kernel<true>, dim3(unsigned(prm.units * prm.splits)), kGThreads, size_t(smem), s,
+                      unsigned(prm.splits), maps, prm);
+}
+
+template <int R, int F>
+cudaError_t run_skinny(const Problem& q, int ks, cudaStream_t s) {
+  auto* x = static_cast<const __nv_bfloat16*>(q.a);
+  auto* w = static_cast<const __nv_bfloat16*>(q.b);
+  const unsigned cols = unsigned(cdiv64(q.N, F));
+  if (ks > 1)
+    return launch_after(skinny_kernel<R, F, 8>, dim3(cols), 256u, 0, s, 1, x, q.ld_a, w, int(q.M), int(q.K), int(q.N), q.ep);
+  return launch_after(skinny_kernel<R, F, 1>, dim3((cols + 7) / 8), 256u, 0, s, 1, x, q.ld_a, w, int(q.M), int(q.K),
+                      int(q.N), q.ep);
+}
+
+// Up to eight rows. Four columns per warp where that leaves sixteen warps for every SM, one
+// otherwise, and K shared by a block's warps where even that leaves fewer than eight.
+cudaError_t run_skinny(const vsa_plan* p, const Problem& q, cudaStream_t s) {
+  const int64_t sms = p->num_sms;
+  const bool wide = q.N >= sms * 64;
+  const int ks = q.N < sms * 8 && q.K >= 512 ? 8 : 1;
+#define VSA_SKINNY(R) (wide ? run_skinny<R, 4>(q, 1, s) : run_skinny<R, 1>(q, ks, s))
+  if (q.M == 1) return VSA_SKINNY(1);
+  if (q.M == 2) return VSA_SKINNY(2);
+  if (q.M <= 4) return VSA_SKINNY(4);
+  return VSA_SKINNY(8);
+#undef VSA_SKINNY
 }
 
 struct GradPlan {
@@ -806,7 +942,7 @@ cudaError_t launch_linear(const vsa_plan* p, const vsa_linear_args& a, cudaStrea
   q.ep.pre = static_cast<__nv_bfloat16*>(a.pre);
   q.ep.ld_pre = a.ld_pre;
   q.ep.act = a.act;
-  return run_products(p, &q, 1, s);
+  return q.M <= 8 ? run_skinny(p, q, s) : run_products(p, &q, 1, s);
 }
 
 cudaError_t launch_linear_bwd(const vsa_plan* p, const vsa_linear_grad_args& a, void* workspace, cudaStream_t s) {
@@ -835,8 +971,8 @@ cudaError_t launch_linear_bwd(const vsa_plan* p, const vsa_linear_grad_args& a, 
     const dim3 grid(unsigned(g.samples) * unsigned(g.chunks_per_sample), unsigned(cdiv64(a.n_out, 256)));
     linear_dz_kernel<<<grid, 256, 0, s>>>(gp);
     if (a.dbias || a.dgate)
-      linear_colsum_kernel<<<dim3(unsigned(g.samples) + 1, unsigned(cdiv64(a.n_out, 32))), 256, 0, s>>>(
-          part_z, part_g, g.samples, g.chunks_per_sample, a.n_out, a.dbias, a.dgate);
+      launch_after(linear_colsum_kernel, dim3(unsigned(g.samples) + 1, unsigned(cdiv64(a.n_out, 32))), 256u, 0, s, 1,
+                   part_z, part_g, g.samples, g.chunks_per_sample, a.n_out, a.dbias, a.dgate);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }

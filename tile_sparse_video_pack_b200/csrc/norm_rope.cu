@@ -622,19 +622,20 @@ __global__ void __launch_bounds__(256, 2) norm_rope_bwd_kernel(NormRopeArgs n, G
   }
 }
 
-// dw[row][z][ch] = sum over the nb partials of that row: eight interleaved
-// chains per channel in fp64, joined in a fixed order. Grid (rows, 2).
+// dw[row][z][ch] = sum over the nb partials of that row: 32 interleaved chains per
+// channel in fp64, joined in a fixed order. Grid (rows, 2, d / 32).
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int nb, int D, float* dw_q,
                                                        float* dw_k) {
-  __shared__ double red[8][128];
-  const int ch = threadIdx.x & 127, sl = threadIdx.x >> 7, z = blockIdx.y;
+  __shared__ double red[32][32];
+  tc::wait_predecessor();
+  const int lane = threadIdx.x & 31, ch = int(blockIdx.z) * 32 + lane, sl = threadIdx.x >> 5, z = blockIdx.y;
   double s = 0.0;
-  if (ch < D)
-    for (int i = sl; i < nb; i += 8) s += double(part[((int64_t(blockIdx.x) * nb + i) * 2 + z) * D + ch]);
-  red[sl][ch] = s;
+#pragma unroll 4
+  for (int i = sl; i < nb; i += 32) s += double(part[((int64_t(blockIdx.x) * nb + i) * 2 + z) * D + ch]);
+  red[sl][lane] = s;
   __syncthreads();
-  if (sl == 0 && ch < D) {
-    for (int i = 1; i < 8; ++i) s += red[i][ch];
+  if (sl == 0) {
+    for (int i = 1; i < 32; ++i) s += red[i][lane];
     float* out = z ? dw_k : dw_q;
     if (out) out[int64_t(blockIdx.x) * D + ch] = float(s);
   }
@@ -760,8 +761,7 @@ cudaError_t launch_norm_rope_bwd(const vsa_plan* p, const NormRopeArgs& n, bool 
 #undef VSA_RUN
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!dw_q && !dw_k)) return e;
-  norm_dw_kernel<<<dim3(grid.y, 2), 1024, 0, s>>>(part, nb, g.d, dw_q, dw_k);
-  return cudaGetLastError();
+  return tc::launch_after(norm_dw_kernel, dim3(grid.y, 2, unsigned(g.d / 32)), 1024u, 0, s, 1, part, nb, g.d, dw_q, dw_k);
 }
 
 }  // namespace vsa

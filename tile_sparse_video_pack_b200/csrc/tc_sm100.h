@@ -89,6 +89,17 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a_tmem, uint64_t 
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// Programmatic dependent launch: a kernel launched with launch_after starts while its
+// predecessor on the stream drains, and waits here -- before its first access to global memory,
+// in every thread that makes one -- until the predecessor has completed and its
+// writes are visible. Without the launch attribute it returns at once.
+__device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets a dependent kernel's blocks be scheduled as this kernel's finish.
+__device__ __forceinline__ void allow_successor() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // ---- CTA pairs (cta_group::2): two CTAs of a cluster share one M = 256 product ----
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -267,6 +278,27 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
 
 
 // --------------------------------------------------------------- host ----
+
+// Launch with programmatic dependence on the stream's previous kernel (the kernel calls
+// wait_predecessor); cluster > 1: that many CTAs per cluster along x.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s,
+                                unsigned cluster, A&&... args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
