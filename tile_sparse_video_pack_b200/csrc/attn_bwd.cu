@@ -59,17 +59,23 @@ constexpr uint32_t kBox = 64 * 64 * 2;           // one 64 x 64 bf16 TMA box
 
 // ------------------------------------------------------------ preparation ----
 
+struct BitParams {
+  const int32_t *idx, *idx_ref, *ref_tiles, *prefix_ref;
+  uint32_t *bits, *bits_t;   // [B * heads][words * 32][words]: query-major and its transpose
+  uint32_t* state;
+  int32_t heads, nt_max, ntv_max, k_max, n_pre, n_ref, k_ref_max, words;
+  int32_t ntv[VSA_MAX_HEADS], k[VSA_MAX_HEADS], k_ref[VSA_MAX_HEADS];
+};
+
 // Per packed row: log-sum-exp in log2 units, and delta = sum of do * o. Rows of
 // unused slots (and of tiles past a head's own) get +inf, so that P is 0.
 template <int CPR>
-__global__ void __launch_bounds__(256) bwd_rows_kernel(Geometry g, const uint4* __restrict__ o,
-                                                       const uint4* __restrict__ dO, const float* __restrict__ lse,
-                                                       const int32_t* __restrict__ counts, float* __restrict__ lse2,
-                                                       float* __restrict__ delta) {
+__device__ __forceinline__ void prepare_rows(const Geometry& g, int block, int blocks, const uint4* o, const uint4* dO,
+                                             const float* lse, const int32_t* counts, float* lse2, float* delta) {
   const int64_t rows = int64_t(g.B) * g.Hh * g.nt_max * VSA_TILE;
   const int c = threadIdx.x % CPR;
   constexpr int R = 256 / CPR;
-  for (int64_t r0 = int64_t(blockIdx.x) * R; r0 < rows; r0 += int64_t(gridDim.x) * R) {
+  for (int64_t r0 = int64_t(block) * R; r0 < rows; r0 += int64_t(blocks) * R) {
     const int64_t row = r0 + threadIdx.x / CPR;  // rows is a multiple of R: every lane has one
     const int64_t tile = row / VSA_TILE;
     const int h = int((tile / g.nt_max) % g.Hh);
@@ -77,8 +83,8 @@ __global__ void __launch_bounds__(256) bwd_rows_kernel(Geometry g, const uint4* 
     float s = 0.f;
     if (valid) {
       float a[8], b[8];
-      bf16x8_to_f32(o[row * CPR + c], a);
-      bf16x8_to_f32(dO[row * CPR + c], b);
+      bf16x8_to_f32(__ldcs(o + row * CPR + c), a);
+      bf16x8_to_f32(__ldcs(dO + row * CPR + c), b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
     }
@@ -91,24 +97,12 @@ __global__ void __launch_bounds__(256) bwd_rows_kernel(Geometry g, const uint4* 
   }
 }
 
-struct BitParams {
-  const int32_t *idx, *idx_ref, *ref_tiles, *prefix_ref;
-  uint32_t *bits, *bits_t;   // [B * heads][words * 32][words]: query-major and its transpose
-  uint32_t* state;
-  int32_t heads, nt_max, ntv_max, k_max, n_pre, n_ref, k_ref_max, words;
-  int32_t ntv[VSA_MAX_HEADS], k[VSA_MAX_HEADS], k_ref[VSA_MAX_HEADS];
-};
-
 // One warp per (batch, head, query tile): its row of the bit matrix. A list out
 // of range or not ascending latches the error and leaves the row empty.
-__global__ void __launch_bounds__(128) bwd_bits_kernel(const __grid_constant__ BitParams p) {
-  extern __shared__ uint32_t sm[];
+__device__ __forceinline__ void prepare_bits(const BitParams& p, int64_t index, uint32_t* row) {
   const int lane = threadIdx.x & 31;
-  uint32_t* row = sm + (threadIdx.x >> 5) * p.words;
   const int rows = p.words * 32;
-  const int i = int(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int bh = blockIdx.y, h = bh % p.heads;
-  if (i >= rows) return;
+  const int bh = int(index / rows), i = int(index - int64_t(bh) * rows), h = bh % p.heads;
   const int nt = p.n_pre + p.ntv[h];
   for (int w = lane; w < p.words; w += 32) row[w] = 0u;
   __syncwarp();
@@ -136,13 +130,35 @@ __global__ void __launch_bounds__(128) bwd_bits_kernel(const __grid_constant__ B
   bad = __any_sync(0xffffffffu, bad);
   if (bad && lane == 0) atomicOr(p.state, kErrBadIndex);
   __syncwarp();
-  uint32_t* out = p.bits + (int64_t(bh) * rows + i) * p.words;
+  uint32_t* out = p.bits + index * p.words;
   for (int w = lane; w < p.words; w += 32) out[w] = bad ? 0u : row[w];
+}
+
+// Both in one launch: the first `row_blocks` blocks the rows, the others eight rows of
+// the bit matrix each; block 0 also clears the two work counters.
+template <int CPR>
+__global__ void __launch_bounds__(256)
+    bwd_prepare_kernel(const __grid_constant__ Geometry g, int row_blocks, const uint4* __restrict__ o,
+                       const uint4* __restrict__ dO, const float* __restrict__ lse,
+                       const int32_t* __restrict__ counts, float* __restrict__ lse2, float* __restrict__ delta,
+                       uint32_t* __restrict__ counters, const __grid_constant__ BitParams p, int64_t bit_rows) {
+  extern __shared__ uint32_t sm[];               // [8][words]
+  allow_successor();
+  if (blockIdx.x == 0 && threadIdx.x < 2) counters[threadIdx.x] = 0u;
+  if (int(blockIdx.x) < row_blocks) {
+    prepare_rows<CPR>(g, blockIdx.x, row_blocks, o, dO, lse, counts, lse2, delta);
+    return;
+  }
+  const int warp = threadIdx.x >> 5;
+  const int64_t index = (int64_t(blockIdx.x) - row_blocks) * 8 + warp;
+  if (index < bit_rows) prepare_bits(p, index, sm + warp * p.words);
 }
 
 // Transpose by 32 x 32 blocks: one warp per block.
 __global__ void __launch_bounds__(256) bwd_transpose_kernel(const uint32_t* __restrict__ bits,
                                                             uint32_t* __restrict__ bits_t, int words, int64_t blocks) {
+  allow_successor();
+  wait_predecessor();
   const int lane = threadIdx.x & 31;
   const int64_t blk = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (blk >= blocks) return;
@@ -181,8 +197,7 @@ struct BSmem {
   static constexpr uint32_t oDs = oStat + 2 * kStat;
   static constexpr uint32_t oP = oDs + kPd;                    // key pass
   static constexpr uint32_t oBar = oP + (KEY ? 1 : 0) * kPd;
-  static constexpr uint32_t oMisc = oBar + 40 * 8;
-  static constexpr uint32_t oItem = oMisc + 16;
+  static constexpr uint32_t oItem = oBar + 40 * 8;
   static constexpr uint32_t oPair = oItem + 2 * sizeof(BwdItem);
   static constexpr uint32_t oCol = oPair + 4 * sizeof(BwdPair);              // query pass: lse2, delta of the tile
   static constexpr uint32_t oEnd = oCol + (KEY ? 0 : 2 * 2 * 64 * 4);        // two items' worth
@@ -213,29 +228,31 @@ static_assert(Q_COUNT <= 40, "barrier slots");
 
 struct BwdParams {
   const uint32_t* bits;             // this pass's bit matrix (rows = stationary tiles)
-  const float *lse2, *delta;        // [B * heads][nt_max][64]
-  const int32_t* counts;            // [heads][nt_max]
   __nv_bfloat16 *out0, *out1;       // key pass: dV, dK; query pass: out1 = dQ
-  uint32_t* state;                  // [0] error word
   uint32_t* counter;                // work counter of this pass
+};
+struct BwdCommon {
+  uint32_t* state;                  // [0] error word
   uint64_t wait_ns;
   int64_t n_items;
-  int32_t heads, bh_total, nt_max, words;
+  const float *lse2, *delta;        // [B * heads][nt_max][64]
+  const int32_t* counts;            // [heads][nt_max]
+  int32_t heads, bh_total, nt_max, words, key_ctas;
   float scale_log2, scale;
 };
+struct BwdMaps {
+  CUtensorMap q, k, v, dO;
+};
 
+// One pass, from this CTA's first item to the end of the pass's queue. Returns with every
+// role done and its copies and products finished.
 template <int D, bool KEY>
-__global__ void __launch_bounds__(kBThreads, 1)
-    attn_bwd_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
-                    const __grid_constant__ CUtensorMap txs, const __grid_constant__ CUtensorMap tys,
-                    const __grid_constant__ BwdParams prm) {
+__device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMap& ty, const CUtensorMap& txs,
+                                         const CUtensorMap& tys, const BwdCommon& prm, const BwdParams& pass,
+                                         uint8_t* smem, uint32_t tmem, volatile uint32_t* abort_flag) {
   using L = BSmem<D, KEY>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + L::oBar + 8u * uint32_t(i); };
-  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::oMisc);
-  volatile uint32_t* abort_flag = misc + 1;
   BwdItem* items = reinterpret_cast<BwdItem*>(smem + L::oItem);
   BwdPair* pairs = reinterpret_cast<BwdPair*>(smem + L::oPair);
   uint32_t* gerr = prm.state;
@@ -262,17 +279,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
     mbar_init(bar(Q_ACCFREE), 8);
     mbar_init(bar(Q_COLS), 8);
     mbar_init(bar(Q_DRAIN), kIssuers);
-    misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sbase + L::oMisc));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = misc[0];
   // TMEM: buffer b at columns 128 b: S [0, 64), dP [64, 128); acc0 (dV^T) at 256, acc1 (dK^T / dQ^T) at 320
 
   if (warp == 0) {
@@ -286,7 +295,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
       uint32_t item = 0;
-      if (lane == 0) item = atomicAdd(prm.counter, 1u);
+      if (lane == 0) item = atomicAdd(pass.counter, 1u);
       item = __shfl_sync(0xffffffffu, item, 0);
       if (int64_t(item) >= prm.n_items) {
         if (lane == 0) {
@@ -298,7 +307,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       // tile-major order: prefix tiles, which meet every tile, come first
       const int tile = int(item / uint32_t(prm.bh_total)), bh = int(item % uint32_t(prm.bh_total));
       const int h = bh % prm.heads;
-      const uint32_t* row = prm.bits + (int64_t(bh) * prm.words * 32 + tile) * prm.words;
+      const uint32_t* row = pass.bits + (int64_t(bh) * prm.words * 32 + tile) * prm.words;
       int n = 0;
       for (int w = lane; w < prm.words; w += 32) n += __popc(row[w]);
 #pragma unroll
@@ -568,7 +577,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const bool is_v = KEY && wg == 0;
       const int ch = D == 128 ? r : (is_v ? r : r - 64);
       const bool mine = ch >= 0 && ch < D;
-      __nv_bfloat16* out = (is_v ? prm.out0 : prm.out1) + (base + inf.tile) * 64 * D + (mine ? ch : 0);
+      __nv_bfloat16* out = (is_v ? pass.out0 : pass.out1) + (base + inf.tile) * 64 * D + (mine ? ch : 0);
       const float f = is_v ? 1.f : prm.scale;
 #pragma unroll 1
       for (int c = KEY ? 0 : c0; c < (KEY ? 64 : c0 + 32); c += 32) {
@@ -591,6 +600,47 @@ __global__ void __launch_bounds__(kBThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (threadIdx.x == 0)                          // the other pass lays out shared memory anew
+    for (int i = 0; i < Q_COUNT; ++i) mbar_inval(bar(i));
+}
+
+// The two passes in one launch: the first key_ctas CTAs begin with the key pass, the others
+// with the query pass, and each goes on to the other pass's queue when its own is empty.
+template <int D>
+__global__ void __launch_bounds__(kBThreads, 1)
+    attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdCommon prm,
+                    const __grid_constant__ BwdParams key, const __grid_constant__ BwdParams qry) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint32_t misc[2];                   // TMEM base, abort flag
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    misc[1] = 0u;
+    prefetch_map(&maps.q);
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.v);
+    prefetch_map(&maps.dO);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(misc)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  volatile uint32_t* abort_flag = misc + 1;
+  wait_predecessor();
+  const bool key_first = int(blockIdx.x) < prm.key_ctas;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if ((i == 0) == key_first)
+      bwd_pass<D, true>(maps.q, maps.dO, maps.k, maps.v, prm, key, smem, tmem, abort_flag);
+    else
+      bwd_pass<D, false>(maps.k, maps.v, maps.q, maps.dO, prm, qry, smem, tmem, abort_flag);
+    if (*abort_flag) break;                      // uniform: every role has passed the barrier at the pass's end
+  }
+  __syncthreads();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
@@ -616,16 +666,32 @@ BwdLayout bwd_layout(const Geometry& g) {
   return l;
 }
 
-template <int D, bool KEY>
-cudaError_t bwd_pass(const vsa_plan* p, const CUtensorMap& tx, const CUtensorMap& ty, const CUtensorMap& txs,
-                     const CUtensorMap& tys, const BwdParams& prm, cudaStream_t s) {
-  using L = BSmem<D, KEY>;
-  const int smem = 1024 + int(L::oEnd);
-  static_assert(1024 + L::oEnd <= 227 * 1024, "shared memory of one CTA");
-  cudaError_t e = cudaFuncSetAttribute(attn_bwd_kernel<D, KEY>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <int D>
+cudaError_t run_passes(const vsa_plan* p, const BwdMaps& maps, const BwdCommon& prm, const BwdParams& key,
+                       const BwdParams& qry, cudaStream_t s) {
+  constexpr uint32_t end = BSmem<D, true>::oEnd > BSmem<D, false>::oEnd ? BSmem<D, true>::oEnd : BSmem<D, false>::oEnd;
+  static_assert(1024 + end + 64 <= 227 * 1024, "shared memory of one CTA");
+  const int smem = 1024 + int(end);
+  const cudaError_t e = cudaFuncSetAttribute(attn_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int grid = int(prm.n_items < p->num_sms ? prm.n_items : p->num_sms);
-  attn_bwd_kernel<D, KEY><<<grid, kBThreads, smem, s>>>(tx, ty, txs, tys, prm);
+  const int64_t items = 2 * prm.n_items;
+  return launch_after(attn_bwd_kernel<D>, dim3(unsigned(items < p->num_sms ? items : p->num_sms)), unsigned(kBThreads),
+                      size_t(smem), s, 1, maps, prm, key, qry);
+}
+
+template <int CPR>
+cudaError_t run_prepare(const vsa_plan* p, const void* op, const void* dop, const float* lse, float* lse2, float* delta,
+                        uint32_t* counters, const BitParams& bp, int64_t bit_rows, cudaStream_t s) {
+  const Geometry& g = p->geo;
+  const int64_t rows = int64_t(g.B) * g.Hh * g.nt_max * VSA_TILE, per = 256 / CPR;
+  const int64_t want = (rows + per - 1) / per, cap = int64_t(p->num_sms) * 8;
+  const int row_blocks = int(want < cap ? want : cap);
+  const int smem = 8 * bp.words * 4;
+  const cudaError_t e = cudaFuncSetAttribute(bwd_prepare_kernel<CPR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  bwd_prepare_kernel<CPR><<<unsigned(row_blocks + (bit_rows + 7) / 8), 256, size_t(smem), s>>>(
+      g, row_blocks, static_cast<const uint4*>(op), static_cast<const uint4*>(dop), lse, p->d_tile_count, lse2, delta,
+      counters, bp, bit_rows);
   return cudaGetLastError();
 }
 
@@ -640,24 +706,13 @@ cudaError_t launch_attn_bwd(const vsa_plan* p, const void* qp, const void* kp, c
   const BwdLayout l = bwd_layout(g);
   char* ws = static_cast<char*>(workspace);
   const int64_t rows = int64_t(g.B) * g.Hh * g.nt_max * VSA_TILE;
-  CUtensorMap tq, tk, tv, tdo;
-  if (!make_map(&tq, qp, rows, g.d) || !make_map(&tk, kp, rows, g.d) || !make_map(&tv, vp, rows, g.d) ||
-      !make_map(&tdo, dop, rows, g.d))
+  BwdMaps maps;
+  if (!make_map(&maps.q, qp, rows, g.d) || !make_map(&maps.k, kp, rows, g.d) || !make_map(&maps.v, vp, rows, g.d) ||
+      !make_map(&maps.dO, dop, rows, g.d))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, s);
-  if (e != cudaSuccess) return e;
-
   float* lse2 = reinterpret_cast<float*>(ws + l.oLse);
   float* delta = reinterpret_cast<float*>(ws + l.oDelta);
-  const int rpb = 256 / (g.d / 8);
-  const int64_t want = (rows + rpb - 1) / rpb, cap = int64_t(p->num_sms) * 8;
-  const unsigned grid = unsigned(want < cap ? want : cap);
-  auto* o4 = static_cast<const uint4*>(op);
-  auto* do4 = static_cast<const uint4*>(dop);
-  if (g.d == 128)
-    bwd_rows_kernel<16><<<grid, 256, 0, s>>>(g, o4, do4, lse, p->d_tile_count, lse2, delta);
-  else
-    bwd_rows_kernel<8><<<grid, 256, 0, s>>>(g, o4, do4, lse, p->d_tile_count, lse2, delta);
+  uint32_t* counters = reinterpret_cast<uint32_t*>(ws);
 
   BitParams bp;
   bp.idx = idx;
@@ -681,41 +736,41 @@ cudaError_t launch_attn_bwd(const vsa_plan* p, const void* qp, const void* kp, c
     bp.k_ref[h] = h < g.Hh ? g.k_ref[h] : 0;
   }
   const int bh = g.B * g.Hh;
-  bwd_bits_kernel<<<dim3(unsigned(l.words) * 8, unsigned(bh)), 128, size_t(4) * l.words * 4, s>>>(bp);
+  const int64_t bit_rows = int64_t(bh) * l.words * 32;
+  cudaError_t e = g.d == 128 ? run_prepare<16>(p, op, dop, lse, lse2, delta, counters, bp, bit_rows, s)
+                             : run_prepare<8>(p, op, dop, lse, lse2, delta, counters, bp, bit_rows, s);
+  if (e != cudaSuccess) return e;
   const int64_t blocks = int64_t(bh) * l.words * l.words;
-  bwd_transpose_kernel<<<unsigned((blocks + 7) / 8), 256, 0, s>>>(bp.bits, bp.bits_t, l.words, blocks);
-  e = cudaGetLastError();
+  e = launch_after(bwd_transpose_kernel, dim3(unsigned((blocks + 7) / 8)), 256u, 0, s, 1, bp.bits, bp.bits_t, l.words,
+                   blocks);
   if (e != cudaSuccess) return e;
 
-  BwdParams prm;
-  prm.lse2 = lse2;
-  prm.delta = delta;
-  prm.counts = p->d_tile_count;
+  BwdCommon prm;
   prm.state = p->d_state;
   prm.wait_ns = p->wait_ns;
   prm.n_items = int64_t(bh) * g.nt_max;
+  prm.lse2 = lse2;
+  prm.delta = delta;
+  prm.counts = p->d_tile_count;
   prm.heads = g.Hh;
   prm.bh_total = bh;
   prm.nt_max = g.nt_max;
   prm.words = l.words;
   prm.scale = p->desc.softmax_scale;
   prm.scale_log2 = p->desc.softmax_scale * 1.4426950408889634f;
-
-  BwdParams key = prm, qry = prm;
+  // the key pass takes about 1.45 times the query pass's time
+  const int64_t ctas = 2 * prm.n_items < p->num_sms ? 2 * prm.n_items : p->num_sms;
+  prm.key_ctas = int32_t((ctas * 3 + 4) / 5);
+  BwdParams key, qry;
   key.bits = bp.bits_t;
-  key.counter = reinterpret_cast<uint32_t*>(ws);
+  key.counter = counters;
   key.out0 = static_cast<__nv_bfloat16*>(dvp);
   key.out1 = static_cast<__nv_bfloat16*>(dkp);
   qry.bits = bp.bits;
-  qry.counter = reinterpret_cast<uint32_t*>(ws) + 1;
+  qry.counter = counters + 1;
   qry.out0 = nullptr;
   qry.out1 = static_cast<__nv_bfloat16*>(dqp);
-  if (g.d == 128) {
-    e = bwd_pass<128, true>(p, tq, tdo, tk, tv, key, s);
-    return e != cudaSuccess ? e : bwd_pass<128, false>(p, tk, tv, tq, tdo, qry, s);
-  }
-  e = bwd_pass<64, true>(p, tq, tdo, tk, tv, key, s);
-  return e != cudaSuccess ? e : bwd_pass<64, false>(p, tk, tv, tq, tdo, qry, s);
+  return g.d == 128 ? run_passes<128>(p, maps, prm, key, qry, s) : run_passes<64>(p, maps, prm, key, qry, s);
 }
 
 }  // namespace vsa
