@@ -166,10 +166,10 @@ __device__ __forceinline__ float square_sum(const float (&a)[4], const float (&b
   return s + __shfl_xor_sync(0xffffffffu, s, CPR / 2);
 }
 
-// The normed and turned row as stored (bf16 words), two pairs at a time in packed
-// fp32. Each product of the rotation is rounded by itself, as the formula is
-// written: with a fused multiply-add one of a pair's two products would be
-// exact and the other not.
+// The normed and turned row as stored (bf16 words). Each product of the rotation
+// is rounded by itself, as the formula is written: with a fused multiply-add one
+// of a pair's two products would be exact and the other not (packed multiplies
+// and adds get fused, so the rotation is in scalars).
 template <int CPR, bool HALVES>
 __device__ __forceinline__ uint4 norm_rope_row(uint4 v, const Weights& w, const Turn& t, float eps) {
   float a[4], b[4];
@@ -178,11 +178,14 @@ __device__ __forceinline__ uint4 norm_rope_row(uint4 v, const Weights& w, const 
   const uint64_t r2 = f2pack(r, r);
 #pragma unroll
   for (int j = 0; j < 4; j += 2) {
-    const uint64_t na = fmul2(fmul2(f2pack(a[j], a[j + 1]), r2), f2pack(w.a[j], w.a[j + 1]));
-    const uint64_t nb = fmul2(fmul2(f2pack(b[j], b[j + 1]), r2), f2pack(w.b[j], w.b[j + 1]));
-    const uint64_t c = f2pack(t.c[j], t.c[j + 1]), s = f2pack(t.s[j], t.s[j + 1]);
-    f2unpack(fadd2(fmul2(na, c), fmul2(nb, s ^ 0x8000000080000000ull)), a[j], a[j + 1]);   // - nb s
-    f2unpack(fadd2(fmul2(na, s), fmul2(nb, c)), b[j], b[j + 1]);
+    f2unpack(fmul2(fmul2(f2pack(a[j], a[j + 1]), r2), f2pack(w.a[j], w.a[j + 1])), a[j], a[j + 1]);
+    f2unpack(fmul2(fmul2(f2pack(b[j], b[j + 1]), r2), f2pack(w.b[j], w.b[j + 1])), b[j], b[j + 1]);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float na = a[j], nb = b[j];
+    a[j] = __fsub_rn(__fmul_rn(na, t.c[j]), __fmul_rn(nb, t.s[j]));
+    b[j] = __fadd_rn(__fmul_rn(na, t.s[j]), __fmul_rn(nb, t.c[j]));
   }
   return from_pairs<HALVES>(a, b);
 }
