@@ -141,29 +141,71 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// Sum of squares of a row: a pairwise tree over its d / 4 channel quads, the same
-// in either layout -- a chain inside a quad, then quads d / 8, d / 16, .., 1 apart --
-// so that every term passes through at most eight roundings. Halves: a lane
-// holds quads c and c + d / 8, so the first step needs no exchange. Interleaved: a
-// lane holds quads 2c and 2c + 1; the first step trades one of its two sums for
-// the other lane's, so that the tree costs one shuffle more, not twice as many.
+// One level of a summing tree over lanes, of 2 n values per lane: the lane gives the
+// half of them that its partner keeps and keeps the sums of the other half, so
+// that the level costs n exchanges and leaves n values, different ones in the
+// two lanes.
+template <int N>
+__device__ __forceinline__ void halve(float (&v)[2 * N], float (&out)[N], int lane_bit) {
+  const bool upper = threadIdx.x & lane_bit;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    out[i] = (upper ? v[N + i] : v[i]) + __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[N + i], lane_bit);
+}
+
+// Sum of squares of a row by halving: channels d / 2, d / 4, .. apart are added, the
+// same tree in either layout, so that every term passes through few roundings. At
+// d = 128 four neighbouring channels are first added in a chain (one value per lane of
+// a full warp). Squares of bf16 values are exact in fp32. Between levels in one lane
+// and levels across lanes, halve() keeps the exchanges at 4 to 10 per row.
 template <int CPR, bool HALVES>
 __device__ __forceinline__ float square_sum(const float (&a)[4], const float (&b)[4]) {
-  // squares of bf16 values are exact in fp32, so the fused chains round like plain ones
-  if (HALVES) {
-    float s = fmaf(a[3], a[3], fmaf(a[2], a[2], fmaf(a[1], a[1], a[0] * a[0]))) +
-              fmaf(b[3], b[3], fmaf(b[2], b[2], fmaf(b[1], b[1], b[0] * b[0])));
+  float s;
+  if constexpr (CPR == 16) {
+    float q[2];                                  // two quads: halves c and c + 16, interleaved 2c and 2c + 1
+    if constexpr (HALVES) {
+      q[0] = fmaf(a[3], a[3], fmaf(a[2], a[2], fmaf(a[1], a[1], a[0] * a[0])));
+      q[1] = fmaf(b[3], b[3], fmaf(b[2], b[2], fmaf(b[1], b[1], b[0] * b[0])));
+      s = q[0] + q[1];                           // quads 16 apart
 #pragma unroll
-    for (int o = CPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
+      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    } else {
+      q[0] = fmaf(b[1], b[1], fmaf(a[1], a[1], fmaf(b[0], b[0], a[0] * a[0])));
+      q[1] = fmaf(b[3], b[3], fmaf(a[3], a[3], fmaf(b[2], b[2], a[2] * a[2])));
+      float one[1];
+      halve<1>(q, one, 8);                       // quads 16 apart; the lane keeps one of its two
+      s = one[0];
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      s += __shfl_xor_sync(0xffffffffu, s, 8);   // neighbouring quads
+    }
+  } else {
+    float two[2], one[1];
+    if constexpr (HALVES) {                      // channels 4c + j and 32 + 4c + j
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = fmaf(a[j], a[j], b[j] * b[j]);   // 32 apart
+      halve<2>(v, two, 4);                       // 16
+      halve<1>(two, one, 2);                     // 8
+      s = one[0] + __shfl_xor_sync(0xffffffffu, one[0], 1);               // 4
+      s += __shfl_xor_sync(0xffffffffu, s, 4);   // 2
+      s += __shfl_xor_sync(0xffffffffu, s, 2);   // 1
+    } else {                                     // channels 8c .. 8c + 7
+      float v[8], four[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = a[j] * a[j];
+        v[2 * j + 1] = b[j] * b[j];
+      }
+      halve<4>(v, four, 4);                      // 32
+      halve<2>(four, two, 2);                    // 16
+      halve<1>(two, one, 1);                     // 8
+      s = one[0] + __shfl_xor_sync(0xffffffffu, one[0], 4);               // 4
+      s += __shfl_xor_sync(0xffffffffu, s, 2);   // 2
+      s += __shfl_xor_sync(0xffffffffu, s, 1);   // 1
+    }
   }
-  const float even = fmaf(b[1], b[1], fmaf(a[1], a[1], fmaf(b[0], b[0], a[0] * a[0])));
-  const float odd = fmaf(b[3], b[3], fmaf(a[3], a[3], fmaf(b[2], b[2], a[2] * a[2])));
-  const bool upper = threadIdx.x & (CPR / 2);
-  float s = (upper ? odd : even) + __shfl_xor_sync(0xffffffffu, upper ? even : odd, CPR / 2);
-#pragma unroll
-  for (int o = CPR / 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s + __shfl_xor_sync(0xffffffffu, s, CPR / 2);
+  return s;
 }
 
 // The normed and turned row as stored (bf16 words). Each product of the rotation
