@@ -14,4 +14,4 @@ from .vsa import (  # noqa: F401
     library,
     make_desc,
 )
-from .layer import TileSparseAttention  # noqa: F401
+from .layer import FeedForward, TileSparseAttention, TileSparseBlock, axial_rope_table  # noqa: F401

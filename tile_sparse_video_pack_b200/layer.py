@@ -1,7 +1,8 @@
-"""One tile-sparse attention layer: a plan, its device buffers and its score weights."""
+"""One tile-sparse attention layer -- a plan, its device buffers and its score weights -- and the parts of a
+transformer block around it: projections, norm and rotation, feed-forward, and their gradients."""
 from __future__ import annotations
 
-from .vsa import Plan, make_desc, k_from_sparsity
+from .vsa import NormRope, Plan, make_desc, k_from_sparsity
 
 
 class TileSparseAttention:
@@ -51,6 +52,11 @@ class TileSparseAttention:
             p.sparse_attn_direct(q, k, v, b["idx"], out, b["lse"], stream)
             return out
         p.tile_pack_pool(q, k, v, b["qp"], b["kp"], b["vp"], b["workspace"], stream)
+        return self.attend(out, stream)
+
+    def attend(self, out, stream=None):
+        """The stages after packing, from the packed tiles and descriptors in the layer's buffers."""
+        b, p = self.bufs, self.plan
         p.tile_score_pooled(self.proj_q, self.proj_k, b["scores"], b["workspace"], stream)
         p.topk_select(b["scores"], b["idx"], stream)
         if p.info.n_ref_tiles:
@@ -63,4 +69,188 @@ class TileSparseAttention:
         return out
 
 
-__all__ = ["TileSparseAttention", "Plan", "make_desc", "k_from_sparsity"]
+def axial_rope_table(plan, theta: float = 10000.0, split=None, device=None):
+    """cos, sin (fp32 [n_tokens, head_dim / 2], for :class:`NormRope`) of a rotation along t, h and w: the channel
+    pairs are divided among the three axes (``split``; by default h and w a third each, t the rest) and pair j
+    of an axis with n pairs turns by position * theta^(-j / n). Prefix tokens are not rotated. Angles in fp64."""
+    import torch
+    d = plan.desc
+    half = d.head_dim // 2
+    split = (half - 2 * (half // 3), half // 3, half // 3) if split is None else tuple(split)
+    if len(split) != 3 or sum(split) != half or min(split) < 0:
+        raise ValueError(f"split must be three counts with sum {half}, got {split}")
+    dev = torch.device("cuda") if device is None else torch.device(device)
+    f64 = dict(dtype=torch.float64, device=dev)
+    n_pre = sum(d.seg_len[i] for i in range(d.n_segments))
+    angles = []
+    for axis, (size, n) in enumerate(zip((d.T, d.H, d.W), split)):
+        if n == 0:
+            continue
+        a = torch.arange(size, **f64)[:, None] * theta ** (-torch.arange(n, **f64) / n)
+        shape = [1, 1, 1, n]
+        shape[axis] = size
+        angles.append(a.view(shape).expand(d.T, d.H, d.W, n).reshape(-1, n))
+    video = torch.cat(angles, 1)
+    table = torch.cat([torch.zeros(n_pre, half, **f64), video])
+    return table.cos().float().contiguous(), table.sin().float().contiguous()
+
+
+def _new(like, *shape, dtype=None):
+    import torch
+    return torch.empty(*shape, dtype=dtype or torch.bfloat16, device=like.device)
+
+
+def _workspace(like, n):
+    import torch
+    return torch.empty(n, dtype=torch.uint8, device=like.device)
+
+
+class TileSparseBlock:
+    """The attention half of a transformer block: y = residual + gate * (attention(norm, rotation(x w_qkv^T + b_qkv))
+    w_out^T + b_out), with its gradient.
+
+    ``layer``: a :class:`TileSparseAttention`. ``w_qkv`` [3 heads head_dim, channels] and ``w_out`` [channels,
+    heads head_dim] bf16, biases fp32 or None, ``norm`` a :class:`NormRope`. q, k and v are written by one
+    product and read in place by the norm-and-pack pass; with ``layer.direct`` each has its own product and the
+    norm runs token-major. ``forward(..., save=True)`` keeps what :meth:`backward` needs (the gradient follows
+    the selected tiles as given; not with ``layer.direct``). The buffers belong to the block: the next forward
+    overwrites them.
+    """
+
+    def __init__(self, layer: TileSparseAttention, w_qkv, w_out, norm: NormRope, b_qkv=None, b_out=None):
+        p = layer.plan
+        d = p.desc
+        width = d.heads * d.head_dim
+        if w_qkv.dim() != 2 or w_qkv.shape[0] != 3 * width:
+            raise ValueError(f"w_qkv must be [{3 * width}, channels], got {tuple(w_qkv.shape)}")
+        if w_out.dim() != 2 or w_out.shape[1] != width:
+            raise ValueError(f"w_out must be [channels, {width}], got {tuple(w_out.shape)}")
+        self.layer, self.norm = layer, norm
+        self.w_qkv, self.b_qkv, self.w_out, self.b_out = w_qkv, b_qkv, w_out, b_out
+        self._saved = None
+
+    def forward(self, x, residual=None, gate=None, out=None, save=False, stream=None):
+        """x [B, N, channels] bf16, residual [B, N, out channels], gate [B, out channels] fp32 -> y."""
+        import torch
+        L, b = self.layer, self.layer.bufs
+        p = L.plan
+        B, N, heads, d = p.shapes()["tokens"]
+        if tuple(x.shape) != (B, N, self.w_qkv.shape[1]):
+            raise ValueError(f"x must be {(B, N, self.w_qkv.shape[1])}, got {tuple(x.shape)}")
+        if save and L.direct:
+            raise ValueError("the direct path keeps no packed tiles: its gradient is not available")
+        width = heads * d
+        o = _new(x, B, N, heads, d)
+        if L.direct:
+            q, k, v = (_new(x, B, N, heads, d) for _ in range(3))
+            for i, t in enumerate((q, k, v)):
+                bias = None if self.b_qkv is None else self.b_qkv[i * width:(i + 1) * width]
+                p.linear(x, self.w_qkv[i * width:(i + 1) * width], t.view(B, N, width), bias=bias, stream=stream)
+            p.qk_norm_rope(q, k, self.norm, q, k, stream=stream)
+            L.stages(q, k, v, o, stream)
+            qkv = None
+        else:
+            qkv = _new(x, B, N, 3, heads, d)
+            p.linear(x, self.w_qkv, qkv.view(B, N, 3 * width), bias=self.b_qkv, stream=stream)
+            p.tile_norm_rope_pack_pool(qkv[:, :, 0], qkv[:, :, 1], qkv[:, :, 2], self.norm, b["qp"], b["kp"], b["vp"],
+                                       b["workspace"], stream)
+            if save and b["lse"] is None:
+                b["lse"] = torch.empty(p.shapes()["lse"], dtype=torch.float32, device=x.device)
+            L.attend(o, stream)
+        y = _new(x, B, N, self.w_out.shape[0]) if out is None else out
+        pre = _new(x, B, N, self.w_out.shape[0]) if save and gate is not None else None
+        p.linear(o.view(B, N, width), self.w_out, y, bias=self.b_out, gate=gate, residual=residual, pre=pre,
+                 stream=stream)
+        self._saved = (x, qkv, o, gate, pre) if save else None
+        return y
+
+    __call__ = forward
+
+    def backward(self, dy, stream=None):
+        """Gradients of the last ``forward(..., save=True)`` from dy: a dict with "x", "w_qkv", "b_qkv", "w_out",
+        "b_out", "gate", "w_q", "w_k" (None where the forward had none); the residual's is dy itself."""
+        import torch
+        if self._saved is None:
+            raise ValueError("backward follows a forward with save=True")
+        x, qkv, o, gate, pre = self._saved
+        L, b = self.layer, self.layer.bufs
+        p = L.plan
+        B, N, heads, d = p.shapes()["tokens"]
+        width, f32 = heads * d, torch.float32
+        samples = gate.shape[0] if gate is not None else 0
+        g = {"x": torch.empty_like(x), "w_qkv": torch.empty_like(self.w_qkv), "w_out": torch.empty_like(self.w_out),
+             "b_qkv": None if self.b_qkv is None else torch.empty_like(self.b_qkv),
+             "b_out": None if self.b_out is None else torch.empty_like(self.b_out),
+             "gate": None if gate is None else torch.empty_like(gate),
+             "w_q": None if self.norm.w_q is None else torch.empty_like(self.norm.w_q),
+             "w_k": None if self.norm.w_k is None else torch.empty_like(self.norm.w_k)}
+        rows = B * N
+        ws = _workspace(x, max(p.linear_bwd_workspace_bytes(rows, width, self.w_out.shape[0], samples),
+                               p.linear_bwd_workspace_bytes(rows, x.shape[2], 3 * width),
+                               p.attn_bwd_workspace_bytes(), p.norm_bwd_workspace_bytes()))
+        do = torch.empty_like(o)
+        p.linear_bwd(dy, o.view(B, N, width), self.w_out, dx=do.view(B, N, width), dw=g["w_out"], pre=pre, gate=gate,
+                     dbias=g["b_out"], dgate=g["gate"], workspace=ws, stream=stream)
+        packed = p.shapes()["packed"]
+        dop, dqp, dkp, dvp = (_new(x, *packed) for _ in range(4))
+        p.tile_pack(do, None, None, dop, None, None, stream)
+        args = (b["qp"], b["kp"], b["vp"], b["op"], b["lse"], dop, b["idx"])
+        if p.info.n_ref_tiles:
+            p.sparse_attn_ref_bwd(*args, b["idx_ref"], dqp, dkp, dvp, ws, stream)
+        else:
+            p.sparse_attn_bwd(*args, dqp, dkp, dvp, ws, stream)
+        dqkv = torch.empty_like(qkv)
+        p.tile_norm_rope_bwd(dqp, dkp, dvp, qkv[:, :, 0], qkv[:, :, 1], self.norm, dqkv[:, :, 0], dqkv[:, :, 1],
+                             dqkv[:, :, 2], g["w_q"], g["w_k"], ws, stream)
+        p.linear_bwd(dqkv.view(B, N, 3 * width), x, self.w_qkv, dx=g["x"], dw=g["w_qkv"], dbias=g["b_qkv"],
+                     workspace=ws, stream=stream)
+        return g
+
+
+class FeedForward:
+    """The other half of the block: y = residual + gate * (act(x w_up^T + b_up) w_down^T + b_down), with its gradient.
+    ``plan`` names the device; weights bf16, biases and gate [samples, channels] fp32 (or None)."""
+
+    def __init__(self, plan: Plan, w_up, w_down, b_up=None, b_down=None, act="gelu_tanh"):
+        if w_up.dim() != 2 or w_down.dim() != 2 or w_up.shape[0] != w_down.shape[1]:
+            raise ValueError(f"w_up {tuple(w_up.shape)} and w_down {tuple(w_down.shape)} do not follow each other")
+        self.plan, self.act = plan, act
+        self.w_up, self.b_up, self.w_down, self.b_down = w_up, b_up, w_down, b_down
+        self._saved = None
+
+    def forward(self, x, residual=None, gate=None, out=None, save=False, stream=None):
+        p, lead = self.plan, x.shape[:-1]
+        h = _new(x, *lead, self.w_up.shape[0])
+        hidden = _new(x, *lead, self.w_up.shape[0]) if save else None
+        p.linear(x, self.w_up, h, bias=self.b_up, act=self.act, pre=hidden, stream=stream)
+        y = _new(x, *lead, self.w_down.shape[0]) if out is None else out
+        pre = _new(x, *lead, self.w_down.shape[0]) if save and gate is not None else None
+        p.linear(h, self.w_down, y, bias=self.b_down, gate=gate, residual=residual, pre=pre, stream=stream)
+        self._saved = (x, hidden, h, gate, pre) if save else None
+        return y
+
+    __call__ = forward
+
+    def backward(self, dy, stream=None):
+        """Gradients of the last ``forward(..., save=True)``: "x", "w_up", "b_up", "w_down", "b_down", "gate"."""
+        import torch
+        if self._saved is None:
+            raise ValueError("backward follows a forward with save=True")
+        x, hidden, h, gate, pre = self._saved
+        p = self.plan
+        like = lambda t: None if t is None else torch.empty_like(t)
+        g = {"x": torch.empty_like(x), "w_up": torch.empty_like(self.w_up), "w_down": torch.empty_like(self.w_down),
+             "b_up": like(self.b_up), "b_down": like(self.b_down), "gate": like(gate)}
+        rows, n_mid, n_out = x.numel() // x.shape[-1], self.w_up.shape[0], self.w_down.shape[0]
+        ws = _workspace(x, max(p.linear_bwd_workspace_bytes(rows, n_mid, n_out, gate.shape[0] if gate is not None else 0),
+                               p.linear_bwd_workspace_bytes(rows, x.shape[-1], n_mid)))
+        dh = torch.empty_like(h)
+        p.linear_bwd(dy, h, self.w_down, dx=dh, dw=g["w_down"], pre=pre, gate=gate, dbias=g["b_down"], dgate=g["gate"],
+                     workspace=ws, stream=stream)
+        p.linear_bwd(dh, x, self.w_up, dx=g["x"], dw=g["w_up"], act=self.act, pre=hidden, dbias=g["b_up"], workspace=ws,
+                     stream=stream)
+        return g
+
+
+__all__ = ["TileSparseAttention", "TileSparseBlock", "FeedForward", "axial_rope_table", "NormRope", "Plan", "make_desc",
+           "k_from_sparsity"]
