@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(256)
                        uint32_t* __restrict__ counters, const __grid_constant__ BitParams p, int64_t bit_rows) {
   extern __shared__ uint32_t sm[];               // [8][words]
   allow_successor();
+  wait_predecessor();
   if (blockIdx.x == 0 && threadIdx.x < 2) counters[threadIdx.x] = 0u;
   if (int(blockIdx.x) < row_blocks) {
     prepare_rows<CPR>(g, blockIdx.x, row_blocks, o, dO, lse, counts, lse2, delta);
@@ -237,7 +238,7 @@ struct BwdCommon {
   int64_t n_items;
   const float *lse2, *delta;        // [B * heads][nt_max][64]
   const int32_t* counts;            // [heads][nt_max]
-  int32_t heads, nt_max, words, key_ctas;
+  int32_t heads, bh_total, nt_max, words, key_ctas, by_head;
   float scale_log2, scale;
 };
 struct BwdMaps {
@@ -304,9 +305,10 @@ __device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMa
         }
         break;
       }
-      // head by head, so that a head's tiles stay in L2 (115 MB at the clip; three heads side by side
-      // took 30.9 ms, one after the other 26.8); its prefix tiles, which meet every tile, first
-      const int bh = int(item / uint32_t(prm.nt_max)), tile = int(item % uint32_t(prm.nt_max));
+      // prefix tiles, which meet every tile, first: of all heads, or head by head
+      const uint32_t per = prm.by_head ? prm.nt_max : prm.bh_total;
+      const int hi = int(item / per), lo = int(item % per);
+      const int bh = prm.by_head ? hi : lo, tile = prm.by_head ? lo : hi;
       const int h = bh % prm.heads;
       const uint32_t* row = pass.bits + (int64_t(bh) * prm.words * 32 + tile) * prm.words;
       int n = 0;
@@ -668,16 +670,17 @@ BwdLayout bwd_layout(const Geometry& g) {
 }
 
 template <int D>
+constexpr int kBwdSmem =
+    1024 + int(BSmem<D, true>::oEnd > BSmem<D, false>::oEnd ? BSmem<D, true>::oEnd : BSmem<D, false>::oEnd);
+static_assert(kBwdSmem<64> <= kBwdSmem<128> && kBwdSmem<128> + 1024 <= 227 * 1024, "shared memory of one CTA");
+constexpr int kMaxBitSmem = 8 * (65536 / 32) * 4;   // eight rows of the largest bit matrix
+
+template <int D>
 cudaError_t run_passes(const vsa_plan* p, const BwdMaps& maps, const BwdCommon& prm, const BwdParams& key,
                        const BwdParams& qry, cudaStream_t s) {
-  constexpr uint32_t end = BSmem<D, true>::oEnd > BSmem<D, false>::oEnd ? BSmem<D, true>::oEnd : BSmem<D, false>::oEnd;
-  static_assert(1024 + end + 64 <= 227 * 1024, "shared memory of one CTA");
-  const int smem = 1024 + int(end);
-  const cudaError_t e = cudaFuncSetAttribute(attn_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   const int64_t items = 2 * prm.n_items;
   return launch_after(attn_bwd_kernel<D>, dim3(unsigned(items < p->num_sms ? items : p->num_sms)), unsigned(kBThreads),
-                      size_t(smem), s, 1, maps, prm, key, qry);
+                      size_t(kBwdSmem<D>), s, 1, maps, prm, key, qry);
 }
 
 template <int CPR>
@@ -688,15 +691,22 @@ cudaError_t run_prepare(const vsa_plan* p, const void* op, const void* dop, cons
   const int64_t want = (rows + per - 1) / per, cap = int64_t(p->num_sms) * 8;
   const int row_blocks = int(want < cap ? want : cap);
   const int smem = 8 * bp.words * 4;
-  const cudaError_t e = cudaFuncSetAttribute(bwd_prepare_kernel<CPR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  bwd_prepare_kernel<CPR><<<unsigned(row_blocks + (bit_rows + 7) / 8), 256, size_t(smem), s>>>(
-      g, row_blocks, static_cast<const uint4*>(op), static_cast<const uint4*>(dop), lse, p->d_tile_count, lse2, delta,
-      counters, bp, bit_rows);
-  return cudaGetLastError();
+  return launch_after(bwd_prepare_kernel<CPR>, dim3(unsigned(row_blocks + (bit_rows + 7) / 8)), 256u, size_t(smem), s, 1,
+                      g, row_blocks, static_cast<const uint4*>(op), static_cast<const uint4*>(dop), lse,
+                      p->d_tile_count, lse2, delta, counters, bp, bit_rows);
 }
 
 }  // namespace
+
+// Shared-memory limits of the kernels, once per device (plan creation).
+cudaError_t prepare_attn_bwd() {
+  const auto at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_kernel<128>, at, kBwdSmem<128>);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_bwd_kernel<64>, at, kBwdSmem<64>);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(bwd_prepare_kernel<16>, at, kMaxBitSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(bwd_prepare_kernel<8>, at, kMaxBitSmem);
+  return e;
+}
 
 int64_t attn_bwd_workspace_bytes(const vsa_plan* p) { return bwd_layout(p->geo).total; }
 
@@ -759,10 +769,14 @@ cudaError_t launch_attn_bwd(const vsa_plan* p, const void* qp, const void* kp, c
   prm.scale = p->desc.softmax_scale;
   prm.scale_log2 = p->desc.softmax_scale * 1.4426950408889634f;
   // Few items: both passes at once, three fifths of the CTAs on the key pass, which takes about
-  // 1.45 times the query pass's time (ragged case 66 -> 42 us). Many: the key pass first, so
-  // that only one pair of streams is in L2 (clip 29.1 -> 26.8 ms; 24 medium heads: no difference).
+  // 1.45 times the query pass's time, and the heavy items of all heads first (ragged case: 66 -> 42 us;
+  // 48 head by head). Many: head by head and the key pass first, so that one head's pair of streams
+  // stays in L2 (clip, three heads: 32.8 ms the first way, 29.1 head by head, 26.8 one pass
+  // after the other as well; 24 medium heads: no difference).
+  prm.bh_total = bh;
   const int64_t ctas = 2 * prm.n_items < p->num_sms ? 2 * prm.n_items : p->num_sms;
-  prm.key_ctas = int32_t(prm.n_items < 4 * ctas ? (ctas * 3 + 4) / 5 : ctas);
+  prm.by_head = prm.n_items >= 4 * ctas;
+  prm.key_ctas = int32_t(prm.by_head ? ctas : (ctas * 3 + 4) / 5);
   BwdParams key, qry;
   key.bits = bp.bits_t;
   key.counter = counters;

@@ -101,18 +101,25 @@ __device__ __forceinline__ uint4 to_bf16x8(const float (&v)[8]) {
   return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
 }
 
-// Eight columns of one row: v holds the accumulator, b the columns' bias.
-__device__ __forceinline__ void store8(const Epilogue& e, int64_t row, int col, float (&v)[8], const float (&b)[8]) {
-  // the loads first: they do not wait for the arithmetic
-  uint4 res = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ uint4 load_residual(const Epilogue& e, int64_t row, int col) {
+  return e.residual ? __ldcs(reinterpret_cast<const uint4*>(e.residual + row * e.ld_res + col)) : make_uint4(0, 0, 0, 0);
+}
+// The gate row of an output row (rows fit 32 bits).
+__device__ __forceinline__ const float* gate_row(const Epilogue& e, int64_t row) {
+  return e.gate ? e.gate + int64_t(uint32_t(row) / uint32_t(e.rows_per_gate)) * e.ld_gate : nullptr;
+}
+
+// Eight columns of one row: v holds the accumulator, b the columns' bias, res the
+// residual's eight values, loaded before (y may overwrite the residual).
+__device__ __forceinline__ void store8(const Epilogue& e, int64_t row, int col, float (&v)[8], const float (&b)[8],
+                                       uint4 res, const float* gate) {
   float g[8];
-  if (e.residual) res = __ldcs(reinterpret_cast<const uint4*>(e.residual + row * e.ld_res + col));
-  if (e.gate) load8(e.gate + (row / e.rows_per_gate) * e.ld_gate + col, g);
+  if (gate) load8(gate + col, g);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] += b[i];
   if (e.pre) __stcs(reinterpret_cast<uint4*>(e.pre + row * e.ld_pre + col), to_bf16x8(v));
   act_fwd(v, e.act);
-  if (e.gate) {
+  if (gate) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= g[i];
   }
@@ -133,12 +140,45 @@ __device__ __forceinline__ void load_bias(const Epilogue& e, int col, float (&b)
   }
 }
 
+// The rows of a warp's 32-row strip that this lane stores (four lanes share a row,
+// four rows each) and their gate rows: fixed for a tile.
+struct StripRows {
+  int64_t row0;
+  int n;                           // how many of the four are inside the matrix
+  const float* gate[4];
+};
+__device__ __forceinline__ StripRows strip_rows(const Epilogue& e, int64_t M, int64_t row0, int lane) {
+  StripRows r;
+  r.row0 = row0 + (lane >> 2);
+  r.n = 0;
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int64_t row = r.row0 + it * 8;
+    r.gate[it] = row < M ? gate_row(e, row) : nullptr;
+    r.n += row < M;
+  }
+  return r;
+}
+// The residual of a 32-column chunk of the strip: requested ahead of the chunk (one at a
+// time before its store, each load held up the next: 164 us for the output projection).
+struct Chunk {
+  uint4 res[4];
+};
+__device__ __forceinline__ Chunk load_chunk(const Epilogue& e, const StripRows& rows, int N, int col0, int lane) {
+  Chunk c;
+  const int col = col0 + 8 * (lane & 3);
+#pragma unroll
+  for (int it = 0; it < 4; ++it)
+    c.res[it] = it < rows.n && col < N ? load_residual(e, rows.row0 + it * 8, col) : make_uint4(0, 0, 0, 0);
+  return c;
+}
+
 // 32 rows by 32 columns of an accumulator, from one warp's TMEM lanes (lane =
 // row; r: this lane's 32 columns) to the output: through 4 KB of shared memory,
 // so that four lanes share a row and every global access moves 64 bytes of a row
 // instead of 16. The 16-byte chunks of a staged row are swizzled by the row, which
 // keeps both sides free of bank conflicts.
-__device__ __forceinline__ void store_chunk(const Epilogue& e, int64_t M, int N, int64_t row0, int col0,
+__device__ __forceinline__ void store_chunk(const Epilogue& e, const StripRows& rows, const Chunk& in, int N, int col0,
                                             const uint32_t (&r)[32], uint8_t* stage, int lane) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -153,12 +193,11 @@ __device__ __forceinline__ void store_chunk(const Epilogue& e, int64_t M, int N,
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int rr = it * 8 + (lane >> 2);
-      const int64_t row = row0 + rr;
-      if (row >= M) continue;
+      if (it >= rows.n) continue;
       const float4 lo = *reinterpret_cast<const float4*>(stage + rr * 128 + (((2 * c8) ^ (rr & 7)) * 16));
       const float4 hi = *reinterpret_cast<const float4*>(stage + rr * 128 + (((2 * c8 + 1) ^ (rr & 7)) * 16));
       float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      store8(e, row, col, v, b);
+      store8(e, rows.row0 + it * 8, col, v, b, in.res[it], rows.gate[it]);
     }
   }
   __syncwarp();                                  // the stage is rewritten for the next chunk
@@ -343,6 +382,12 @@ __global__ void __launch_bounds__(kGThreads, 1)
       __syncwarp();
     } else if (ok) {
       const int ew = warp - 2, q4 = warp & 3, c0 = (ew >> 2) * (kBN / 2);   // my lanes and columns
+      StripRows rows;
+      Chunk next;
+      if constexpr (!SPLIT) {                    // while the products run
+        rows = strip_rows(pr.ep, pr.M, int64_t(t.m) * kBM + q4 * 32, lane);
+        next = load_chunk(pr.ep, rows, pr.N, t.n * kBN + c0, lane);
+      }
       ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
@@ -363,8 +408,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
               *reinterpret_cast<uint4*>(row + (((c >> 2) + i) ^ (lane & 7)) * 16) =
                   make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
           } else {
-            store_chunk(pr.ep, pr.M, pr.N, int64_t(t.m) * kBM + q4 * 32, t.n * kBN + c, r,
-                        smem + L::oOut + ew * 4096, lane);
+            const Chunk in = next;
+            if (c + 32 < c0 + kBN / 2) next = load_chunk(pr.ep, rows, pr.N, t.n * kBN + c + 32, lane);
+            store_chunk(pr.ep, rows, in, pr.N, t.n * kBN + c, r, smem + L::oOut + ew * 4096, lane);
           }
         }
       }
@@ -380,6 +426,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
         for (int rr = r0 + (warp - 2) * 2 + (lane >> 4); rr < r1; rr += 2 * kEWarps) {
           const int64_t row = int64_t(t.m) * kBM + rr;
           if (row >= pr.M || col >= pr.N) continue;
+          const uint4 res = load_residual(pr.ep, row, col);
           const uint32_t lo = sbase + rr * (kBN * 4) + ((2 * cg) ^ (rr & 7)) * 16;
           const uint32_t hi = sbase + rr * (kBN * 4) + ((2 * cg + 1) ^ (rr & 7)) * 16;
           float4 x[8], y[8];                     // all loads before the first sum: each takes about a microsecond
@@ -396,7 +443,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
               v[0] += x[s].x; v[1] += x[s].y; v[2] += x[s].z; v[3] += x[s].w;
               v[4] += y[s].x; v[5] += y[s].y; v[6] += y[s].z; v[7] += y[s].w;
             }
-          store8(pr.ep, row, col, v, b);
+          store8(pr.ep, row, col, v, b, res, gate_row(pr.ep, row));
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the stages are loaded again after these accesses
@@ -542,10 +589,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     for (int u = pair; u < units; u += pairs, ++n) {
       const Tile t = tile_of(prm, u);
       const int ab = n & 1;
+      // while the products run
+      const StripRows rows = strip_rows(pr.ep, pr.M, int64_t(t.m) * 256 + rank * 128 + q4 * 32, lane);
+      Chunk next = load_chunk(pr.ep, rows, pr.N, t.n * 256 + c0, lane);
       const bool ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const int64_t row0 = int64_t(t.m) * 256 + rank * 128 + q4 * 32;
 #pragma unroll 1
       for (int c = c0; c < c0 + 128; c += 32) {
         uint32_t r[32];
@@ -556,7 +605,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to_rank(bar(G_AEMPTY + ab), 0));
         }
-        store_chunk(pr.ep, pr.M, pr.N, row0, t.n * 256 + c, r, stage, lane);
+        const Chunk in = next;
+        if (c + 32 < c0 + 128) next = load_chunk(pr.ep, rows, pr.N, t.n * 256 + c + 32, lane);
+        store_chunk(pr.ep, rows, in, pr.N, t.n * 256 + c, r, stage, lane);
       }
     }
   }
@@ -661,6 +712,7 @@ struct GradParams {
 __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ GradParams p) {
   __shared__ float red[2][8][256];
   allow_successor();
+  wait_predecessor();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = int(blockIdx.y) * 256 + lane * 8;
   const int64_t sample = blockIdx.x / p.chunks_per_sample;
@@ -830,8 +882,6 @@ cudaError_t run_products(const vsa_plan* p, const Problem* q, int n, cudaStream_
     start();
     if (!add_product(maps, prm, q[i], 256)) return cudaErrorInvalidValue;
     const int smem = 1024 + int(PSmem::oEnd);
-    const cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     const int most = p->num_sms / 2;
     const cudaError_t r = launch_after(gemm_pair_kernel, dim3(2 * unsigned(prm.units < most ? prm.units : most)), kGThreads,
                                        size_t(smem), s, 1, maps, prm);
@@ -853,13 +903,9 @@ cudaError_t run_products(const vsa_plan* p, const Problem* q, int n, cudaStream_
     prm.splits *= 2;
   const int smem = 1024 + int(GSmem::oEnd);
   if (prm.splits == 1) {
-    const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     return launch_after(gemm_kernel<false>, dim3(unsigned(prm.units < p->num_sms ? prm.units : p->num_sms)), kGThreads,
                         size_t(smem), s, 1, maps, prm);
   }
-  const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   return launch_after(gemm_kernel<true>, dim3(unsigned(prm.units * prm.splits)), kGThreads, size_t(smem), s,
                       unsigned(prm.splits), maps, prm);
 }
@@ -902,7 +948,7 @@ GradPlan grad_plan(const vsa_plan* p, int64_t rows, int64_t N, int act, bool gat
   g.rows_per_sample = gate ? rows_per_gate : rows;
   g.samples = int32_t(cdiv64(rows, g.rows_per_sample));
   const int64_t blocks_y = cdiv64(N, 256);
-  int64_t want = cdiv64(int64_t(p->num_sms) * 4, blocks_y);
+  int64_t want = cdiv64(int64_t(p->num_sms) * 16, blocks_y);   // many small blocks: no long last round
   int64_t chunk = cdiv64(rows, want);
   if (chunk < 32) chunk = 32;
   if (chunk > g.rows_per_sample) chunk = g.rows_per_sample;
@@ -914,6 +960,15 @@ GradPlan grad_plan(const vsa_plan* p, int64_t rows, int64_t N, int act, bool gat
 }
 
 }  // namespace
+
+// Shared-memory limits of the products, once per device (plan creation).
+cudaError_t prepare_linear() {
+  const auto at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel, at, 1024 + int(PSmem::oEnd));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_kernel<false>, at, 1024 + int(GSmem::oEnd));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_kernel<true>, at, 1024 + int(GSmem::oEnd));
+  return e;
+}
 
 int64_t linear_bwd_workspace_bytes(const vsa_plan* p, int64_t rows, int64_t n_out, int64_t rows_per_gate) {
   if (rows == 0) return 0;
@@ -969,11 +1024,10 @@ cudaError_t launch_linear_bwd(const vsa_plan* p, const vsa_linear_grad_args& a, 
     gp.chunk = g.chunk;
     gp.chunks_per_sample = g.chunks_per_sample;
     const dim3 grid(unsigned(g.samples) * unsigned(g.chunks_per_sample), unsigned(cdiv64(a.n_out, 256)));
-    linear_dz_kernel<<<grid, 256, 0, s>>>(gp);
-    if (a.dbias || a.dgate)
-      launch_after(linear_colsum_kernel, dim3(unsigned(g.samples) + 1, unsigned(cdiv64(a.n_out, 32))), 256u, 0, s, 1,
-                   part_z, part_g, g.samples, g.chunks_per_sample, a.n_out, a.dbias, a.dgate);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_after(linear_dz_kernel, grid, 256u, 0, s, 1, gp);
+    if (e == cudaSuccess && (a.dbias || a.dgate))
+      e = launch_after(linear_colsum_kernel, dim3(unsigned(g.samples) + 1, unsigned(cdiv64(a.n_out, 32))), 256u, 0, s, 1,
+                       part_z, part_g, g.samples, g.chunks_per_sample, a.n_out, a.dbias, a.dgate);
     if (e != cudaSuccess) return e;
   }
   const void* zsrc = g.needs_dz ? static_cast<const void*>(dz) : a.dy;

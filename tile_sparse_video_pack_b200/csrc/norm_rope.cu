@@ -250,6 +250,8 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(NormRopeArgs n, int B, i
                                                         const __nv_bfloat16* q, const __nv_bfloat16* k,
                                                         __nv_bfloat16* qo, __nv_bfloat16* ko) {
   constexpr int D = CPR * 8, G = 32 / CPR;
+  tc::allow_successor();
+  tc::wait_predecessor();
   const int lane = threadIdx.x & 31, c = lane % CPR, grp = lane / CPR;
   Weights wq = load_weights<HALVES>(n.w_q, D, c), wk = load_weights<HALVES>(n.w_k, D, c);
   const int64_t total = int64_t(B) * n_tok;
@@ -322,6 +324,8 @@ __global__ void __launch_bounds__(256, 2)
   const int vt = tile_n - g.n_pre_tiles;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const uint32_t base = tc::smem_u32(rows);
+  tc::allow_successor();
+  tc::wait_predecessor();
 
   // Which token list head h uses: a head of another tile shape than the one before it
   // fills the other list (the divisions cost more than a row's arithmetic: once per slot).
@@ -515,16 +519,19 @@ __device__ __forceinline__ uint4 norm_rope_grad_row(uint4 vy, uint4 vx, const We
 // PACKED: dy (and dv, which is only moved) come from packed tiles. The blocks'
 // partial sums of dw go to `part` [blockIdx.y][blockIdx.x][q, k][d], summed in
 // block order by the kernel below: no atomics, the same result every time.
-// Bound by HBM: a warp's next step (32 / CPR rows of every input) is requested into
-// shared memory while this one is worked on, across tokens too; with one step's
-// loads in registers the clip took 1.08 ms.
-template <int CPR, bool PACKED>
+// Bound by HBM: a warp's next steps (32 / CPR rows of every input each) are
+// requested into shared memory ahead of the one at work, across tokens too; with
+// one step's loads in registers the clip took 1.08 ms. With PER_HEAD a step is a
+// token, so its table rows are requested along with it.
+template <int CPR, bool PACKED, bool PER_HEAD>
 struct GradSmem {
-  static constexpr int kIn = PACKED ? 5 : 4;                   // dy_q, dy_k, q, k (, dv)
+  static constexpr int kStages = PER_HEAD ? 3 : 2;
+  static constexpr int kRows = PACKED ? 5 : 4;                 // dy_q, dy_k, q, k (, dv)
+  static constexpr int kIn = kRows + (PER_HEAD ? 2 : 0);       // (, cos, sin)
   static constexpr uint32_t kStep = kIn * 512;                 // one warp's step: 32 chunks of each input
-  static constexpr uint32_t oRed = 8 * 2 * kStep;
+  static constexpr uint32_t oRed = 8 * kStages * kStep;
   static constexpr uint32_t oRow = oRed + 8 * 2 * CPR * 8 * 4;
-  static constexpr uint32_t kBytes = oRow + 8 * 2 * VSA_MAX_HEADS * 4;
+  static constexpr uint32_t kBytes = oRow + 8 * VSA_MAX_HEADS * 4;
 };
 template <int CPR, bool HALVES, bool PACKED, bool PER_HEAD>
 __global__ void __launch_bounds__(256, 2) norm_rope_bwd_kernel(NormRopeArgs n, Geometry g, const __nv_bfloat16* dyq,
@@ -533,11 +540,13 @@ __global__ void __launch_bounds__(256, 2) norm_rope_bwd_kernel(NormRopeArgs n, G
                                                                __nv_bfloat16* dq, __nv_bfloat16* dk,
                                                                __nv_bfloat16* dv, float* part) {
   constexpr int D = CPR * 8, G = 32 / CPR;
-  using L = GradSmem<CPR, PACKED>;
+  using L = GradSmem<CPR, PACKED, PER_HEAD>;
   extern __shared__ __align__(16) uint8_t sm[];
+  tc::allow_successor();
+  tc::wait_predecessor();
   const int lane = threadIdx.x & 31, c = lane % CPR, grp = lane / CPR, warp = threadIdx.x >> 5;
-  uint8_t* stage = sm + warp * 2 * L::kStep;
-  int32_t* prow = reinterpret_cast<int32_t*>(sm + L::oRow) + warp * 2 * VSA_MAX_HEADS;   // [token parity][head]
+  uint8_t* stage = sm + warp * L::kStages * L::kStep;
+  int32_t* prow = reinterpret_cast<int32_t*>(sm + L::oRow) + warp * VSA_MAX_HEADS;   // the requested token's, by head
   const int64_t woff = PER_HEAD && n.per_head ? int64_t(blockIdx.y) * D : 0;
   const Weights wq = load_weights<HALVES>(n.w_q ? n.w_q + woff : nullptr, D, c);
   const Weights wk = load_weights<HALVES>(n.w_k ? n.w_k + woff : nullptr, D, c);
@@ -568,18 +577,19 @@ __global__ void __launch_bounds__(256, 2) norm_rope_bwd_kernel(NormRopeArgs n, G
   auto head_of = [&](const At& a) { return PER_HEAD ? int(blockIdx.y) : a.step * G + grp; };
   auto on = [&](const At& a) { return a.b < g.B && head_of(a) < g.Hh; };
   auto more = [&](const At& a) { return a.left > 0; };
-  auto request = [&](const At& a, uint32_t parity, int buf) {   // warp-wide
+  auto request = [&](const At& a, uint32_t buf) {   // warp-wide
     const bool is_on = on(a);
     const int h = is_on ? head_of(a) : 0, bb = is_on ? a.b : 0, tok = is_on ? a.tok : 0;
     if constexpr (PACKED && !PER_HEAD) {
       if (a.step == 0) {                         // a new token: every head's packed row
-        for (int i = lane; i < g.Hh; i += 32) prow[parity * VSA_MAX_HEADS + i] = packed_row(g, i, a.tok);
+        __syncwarp();                            // the previous token's rows are read
+        for (int i = lane; i < g.Hh; i += 32) prow[i] = packed_row(g, i, a.tok);
         __syncwarp();
       }
     }
     const __nv_bfloat16* src[5];
     if constexpr (PACKED) {
-      const int pr = PER_HEAD ? packed_row(g, h, tok) : prow[parity * VSA_MAX_HEADS + h];
+      const int pr = PER_HEAD ? packed_row(g, h, tok) : prow[h];
       const int64_t row = (int64_t(bb * g.Hh + h) * g.nt_max * VSA_TILE + pr) * D;
       src[0] = dyq + row;
       src[1] = dyk + row;
@@ -592,8 +602,13 @@ __global__ void __launch_bounds__(256, 2) norm_rope_bwd_kernel(NormRopeArgs n, G
     src[3] = k + bb * n.st[1].batch + tok * n.st[1].token + h * D;
     const uint32_t dst = tc::smem_u32(stage + buf * L::kStep) + lane * 16;
 #pragma unroll
-    for (int z = 0; z < L::kIn; ++z) cp_async16(dst + z * 512, src[z] + 8 * c, is_on);
-    cp_commit();
+    for (int z = 0; z < L::kRows; ++z) cp_async16(dst + z * 512, src[z] + 8 * c, is_on);
+    if constexpr (PER_HEAD) {
+      if (n.cos) {
+        cp_async16(dst + L::kRows * 512, n.cos + int64_t(tok) * (D / 2) + 4 * c, is_on);
+        cp_async16(dst + (L::kRows + 1) * 512, n.sin + int64_t(tok) * (D / 2) + 4 * c, is_on);
+      }
+    }
   };
 
   At now;
@@ -602,24 +617,35 @@ __global__ void __launch_bounds__(256, 2) norm_rope_bwd_kernel(NormRopeArgs n, G
   now.step = 0;
   now.left = total - (first - (PER_HEAD ? grp : 0));
   At next = now;                                 // the step to request next
-  uint32_t parity = 0;
-  auto request_next = [&](int buf) {
-    request(next, parity, buf);
-    advance(next);
-    if (next.step == 0) parity ^= 1;
+  uint32_t issued = 0, done = 0;                 // steps, which take the stages in turn
+  auto request_next = [&] {                      // one group of copies for every step, past the end an empty one
+    if (more(next)) {
+      request(next, issued % L::kStages);
+      advance(next);
+    }
+    cp_commit();
+    ++issued;
   };
-  if (more(next)) request_next(0);
-  int buf = 0;
+#pragma unroll
+  for (int i = 0; i < L::kStages - 1; ++i) request_next();
   while (more(now)) {
-    const Turn turn = load_turn(n, now.b < g.B ? now.tok : 0, D, c);
-    for (int step = 0; step < steps; ++step, buf ^= 1) {
-      if (more(next)) request_next(buf ^ 1);
-      else cp_commit();                          // empty: the count of groups stays in step
-      cp_wait<1>();
+    Turn turn = {};
+    if (!PER_HEAD || !n.cos) turn = load_turn(n, now.b < g.B ? now.tok : 0, D, c);
+    for (int step = 0; step < steps; ++step, ++done) {
+      request_next();
+      cp_wait<L::kStages - 1>();
       __syncwarp();
+      const uint32_t buf = done % L::kStages;
       // lane group grp's row of input z: 16 * CPR bytes
       const uint8_t* in = stage + buf * L::kStep + grp * CPR * 16;
       auto row = [&](int z) { return row_of<HALVES>(reinterpret_cast<const __nv_bfloat16*>(in + z * 512), D, c); };
+      if constexpr (PER_HEAD) {
+        if (n.cos) {                             // this lane's own chunks
+          const float4 cs = *reinterpret_cast<const float4*>(in + L::kRows * 512 + 16 * c);
+          const float4 sn = *reinterpret_cast<const float4*>(in + (L::kRows + 1) * 512 + 16 * c);
+          turn = Turn{{cs.x, cs.y, cs.z, cs.w}, {sn.x, sn.y, sn.z, sn.w}};
+        }
+      }
       const uint4 yq = norm_rope_grad_row<CPR, HALVES>(row(0), row(2), wq, turn, n.eps, tok_acc[0][0], tok_acc[0][1]);
       const uint4 yk = norm_rope_grad_row<CPR, HALVES>(row(1), row(3), wk, turn, n.eps, tok_acc[1][0], tok_acc[1][1]);
       if (on(now)) {
@@ -700,6 +726,27 @@ int bwd_blocks(const vsa_plan* p, bool per_head) {
 
 }  // namespace
 
+// Shared-memory limits of the kernels above, once per device (plan creation).
+cudaError_t prepare_norm_rope() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto* kernel, uint32_t bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  };
+#define VSA_SET(CPR, HV)                                                                 \
+  set(norm_rope_pack_kernel<CPR, HV, false>, PackSmem<CPR, false>::kBytes);              \
+  set(norm_rope_pack_kernel<CPR, HV, true>, PackSmem<CPR, true>::kBytes);                \
+  set(norm_rope_bwd_kernel<CPR, HV, false, false>, GradSmem<CPR, false, false>::kBytes);        \
+  set(norm_rope_bwd_kernel<CPR, HV, false, true>, GradSmem<CPR, false, true>::kBytes);         \
+  set(norm_rope_bwd_kernel<CPR, HV, true, false>, GradSmem<CPR, true, false>::kBytes);          \
+  set(norm_rope_bwd_kernel<CPR, HV, true, true>, GradSmem<CPR, true, true>::kBytes)
+  VSA_SET(16, true);
+  VSA_SET(16, false);
+  VSA_SET(8, true);
+  VSA_SET(8, false);
+#undef VSA_SET
+  return e;
+}
+
 cudaError_t launch_norm_rope(const vsa_plan* p, const NormRopeArgs& n, const void* q, const void* k, void* qo, void* ko,
                              cudaStream_t s) {
   const Geometry& g = p->geo;
@@ -709,7 +756,8 @@ cudaError_t launch_norm_rope(const vsa_plan* p, const NormRopeArgs& n, const voi
   auto* k2 = static_cast<const __nv_bfloat16*>(k);
   auto* qo2 = static_cast<__nv_bfloat16*>(qo);
   auto* ko2 = static_cast<__nv_bfloat16*>(ko);
-#define VSA_RUN(CPR, HV) norm_rope_kernel<CPR, HV><<<grid, 256, 0, s>>>(n, g.B, g.n_tokens, g.Hh, q2, k2, qo2, ko2)
+#define VSA_RUN(CPR, HV) \
+  return tc::launch_after(norm_rope_kernel<CPR, HV>, dim3(grid), 256u, 0, s, 1, n, g.B, g.n_tokens, g.Hh, q2, k2, qo2, ko2)
   if (g.d == 128) {
     if (n.halves) VSA_RUN(16, true);
     else VSA_RUN(16, false);
@@ -718,7 +766,6 @@ cudaError_t launch_norm_rope(const vsa_plan* p, const NormRopeArgs& n, const voi
     else VSA_RUN(8, false);
   }
 #undef VSA_RUN
-  return cudaGetLastError();
 }
 
 cudaError_t launch_norm_rope_pack(const vsa_plan* p, const NormRopeArgs& n, const void* q, const void* k, const void* v,
@@ -730,16 +777,11 @@ cudaError_t launch_norm_rope_pack(const vsa_plan* p, const NormRopeArgs& n, cons
   const unsigned grid = unsigned(int64_t(g.B) * g.nt_max * ((g.Hh + run - 1) / run));
   const bool trip = p->desc.score_mode == VSA_SCORE_TRIPPOOL;
 #define VSA_RUN(CPR, HV, TR)                                                                                       \
-  do {                                                                                                             \
-    constexpr int smem = int(PackSmem<CPR, TR>::kBytes);                                                            \
-    const cudaError_t e = cudaFuncSetAttribute(norm_rope_pack_kernel<CPR, HV, TR>,                                  \
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);                 \
-    if (e != cudaSuccess) return e;                                                                                \
-    norm_rope_pack_kernel<CPR, HV, TR><<<grid, 256, smem, s>>>(                                                     \
-        n, g, int(run), static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),                \
-        static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(qp), static_cast<__nv_bfloat16*>(kp),    \
-        static_cast<__nv_bfloat16*>(vp), p->d_tile_count, pooled_q, pooled_k);                                     \
-  } while (0)
+  return tc::launch_after(norm_rope_pack_kernel<CPR, HV, TR>, dim3(grid), 256u, size_t(PackSmem<CPR, TR>::kBytes), s, \
+                          1, n, g, int(run), static_cast<const __nv_bfloat16*>(q),                                 \
+                          static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),              \
+                          static_cast<__nv_bfloat16*>(qp), static_cast<__nv_bfloat16*>(kp),                        \
+                          static_cast<__nv_bfloat16*>(vp), p->d_tile_count, pooled_q, pooled_k)
   if (g.d == 128) {
     if (n.halves) {
       if (trip) VSA_RUN(16, true, true);
@@ -758,7 +800,6 @@ cudaError_t launch_norm_rope_pack(const vsa_plan* p, const NormRopeArgs& n, cons
     }
   }
 #undef VSA_RUN
-  return cudaGetLastError();
 }
 
 int64_t norm_bwd_workspace_bytes(const vsa_plan* p) {
@@ -773,18 +814,13 @@ cudaError_t launch_norm_rope_bwd(const vsa_plan* p, const NormRopeArgs& n, bool 
   const int nb = bwd_blocks(p, n.per_head);
   const dim3 grid(nb, n.per_head ? g.Hh : 1);
   float* part = static_cast<float*>(workspace);
+  cudaError_t e = cudaSuccess;
 #define VSA_RUN(CPR, HV, PK, PH)                                                                                   \
-  do {                                                                                                             \
-    constexpr int smem = int(GradSmem<CPR, PK>::kBytes);                                                            \
-    const cudaError_t e = cudaFuncSetAttribute(norm_rope_bwd_kernel<CPR, HV, PK, PH>,                               \
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);                 \
-    if (e != cudaSuccess) return e;                                                                                \
-    norm_rope_bwd_kernel<CPR, HV, PK, PH><<<grid, 256, smem, s>>>(                                                  \
-        n, g, static_cast<const __nv_bfloat16*>(dyq), static_cast<const __nv_bfloat16*>(dyk),                      \
-        static_cast<const __nv_bfloat16*>(dyv), static_cast<const __nv_bfloat16*>(q),                              \
-        static_cast<const __nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk),    \
-        static_cast<__nv_bfloat16*>(dv), part);                                                                    \
-  } while (0)
+  e = tc::launch_after(norm_rope_bwd_kernel<CPR, HV, PK, PH>, grid, 256u, size_t(GradSmem<CPR, PK, PH>::kBytes), s, 1, n, \
+                       g, static_cast<const __nv_bfloat16*>(dyq), static_cast<const __nv_bfloat16*>(dyk),          \
+                       static_cast<const __nv_bfloat16*>(dyv), static_cast<const __nv_bfloat16*>(q),               \
+                       static_cast<const __nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(dq),                      \
+                       static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), part)
 #define VSA_RUN2(CPR, HV)                  \
   do {                                     \
     if (packed) {                          \
@@ -804,7 +840,6 @@ cudaError_t launch_norm_rope_bwd(const vsa_plan* p, const NormRopeArgs& n, bool 
   }
 #undef VSA_RUN2
 #undef VSA_RUN
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!dw_q && !dw_k)) return e;
   return tc::launch_after(norm_dw_kernel, dim3(grid.y, 2, unsigned(g.d / 32)), 1024u, 0, s, 1, part, nb, g.d, dw_q, dw_k);
 }

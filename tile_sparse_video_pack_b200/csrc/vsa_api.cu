@@ -338,6 +338,9 @@ vsa_status vsa_plan_create(const vsa_desc* desc, vsa_plan** out) {
   // (re)resolve this device's address of the fixed scratch of vsa_tile_score_static, so
   // that a plan made after a device reset never uses the address of a discarded module
   if (e == cudaSuccess) e = vsa::refresh_static_scratch_address(p->device);
+  if (e == cudaSuccess) e = vsa::prepare_norm_rope();
+  if (e == cudaSuccess) e = vsa::prepare_linear();
+  if (e == cudaSuccess) e = vsa::prepare_attn_bwd();
   if (e != cudaSuccess) {
     cudaGetLastError();
     vsa_status r = (e == cudaErrorMemoryAllocation) ? VSA_ERR_NO_MEMORY : VSA_ERR_CUDA;

@@ -143,4 +143,9 @@ cudaError_t launch_attn_bwd(const vsa_plan* p, const void* qp, const void* kp, c
                             const float* lse, const void* dop, const int32_t* idx, const int32_t* idx_ref,
                             const int32_t* k, void* dqp, void* dkp, void* dvp, void* workspace, cudaStream_t s);
 
+// Shared-memory limits of the kernels around the layer, on the current device: set by plan creation.
+cudaError_t prepare_norm_rope();
+cudaError_t prepare_linear();
+cudaError_t prepare_attn_bwd();
+
 }  // namespace vsa

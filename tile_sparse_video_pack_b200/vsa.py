@@ -108,6 +108,7 @@ class VsaError(RuntimeError):
 
 
 _lib = None
+_torch = _BF16 = _F32 = _I32T = _U8 = None      # torch and the dtypes the calls take, set when the library is loaded
 
 
 def library() -> ctypes.CDLL:
@@ -163,6 +164,9 @@ def library() -> ctypes.CDLL:
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
+    import torch
+    global _torch, _BF16, _F32, _I32T, _U8
+    _torch, _BF16, _F32, _I32T, _U8 = torch, torch.bfloat16, torch.float32, torch.int32, torch.uint8
     _lib = lib
     return lib
 
@@ -238,8 +242,7 @@ def _addr(t, dtype, name, dev, min_numel=0):
 
 def _strided_addr(t, dtype, name, dev):
     """Address of a tensor of any strides on device `dev`, the current one."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, but cuda:{dev} is the current device")
@@ -250,8 +253,7 @@ def _strided_addr(t, dtype, name, dev):
 
 def _matrix(t, cols, name, dev, rows=None):
     """(address, row stride, rows) of a bf16 [..., cols] tensor whose leading dimensions form one row axis."""
-    import torch
-    p = _strided_addr(t, torch.bfloat16, name, dev)
+    p = _strided_addr(t, _BF16, name, dev)
     shape = t.shape
     if not shape or shape[-1] != cols:
         raise ValueError(f"{name} must be [..., {cols}], got {tuple(shape)}")
@@ -300,8 +302,6 @@ class NormRope:
         return w is not None and w.dim() == 2
 
     def _struct(self, plan, dev):
-        import torch
-        f32 = torch.float32
         per_head = self.per_head
         _, n, heads, d = plan._tokens
         want_w, want_t = ((heads, d) if per_head else (d,)), (n, d // 2)
@@ -310,7 +310,7 @@ class NormRope:
                               (self.sin, "sin", want_t)):
             if t is not None and t.shape != want:
                 raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
-            at.append(_addr(t, f32, name, dev))
+            at.append(_addr(t, _F32, name, dev))
         key = (*at, per_head, self.layout, self.eps)
         made = self._made
         if made[0] != key:
@@ -337,9 +337,9 @@ def _stream(stream):
 
 def _here(stream):
     """(current device, raw stream) of a call."""
-    import torch
-    dev = torch._C._cuda_getDevice()
-    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    c = _torch._C
+    dev = c._cuda_getDevice()
+    return dev, c._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 class Plan:
@@ -354,7 +354,11 @@ class Plan:
         inf = VsaPlanInfo()
         _check(lib.vsa_plan_query(h, ctypes.byref(inf)), "vsa_plan_query")
         self.info = inf
+        # what the calls around the layer check against, as plain numbers
+        self._lib = lib
         self._tokens = (desc.batch, inf.n_tokens, desc.heads, desc.head_dim)
+        self._pe, self._ws_bytes, self._lse, self._idx = (inf.packed_elems, inf.workspace_bytes, inf.lse_elems,
+                                                          inf.index_elems)
         self._bytes = {}               # workspace sizes of this plan, by call
 
     @classmethod
@@ -623,12 +627,11 @@ class Plan:
     def _token_views(self, dev, *views):
         """(addresses, strides) of bf16 [B, N, heads, head_dim] views with contiguous heads and channels; strides
         None when all are contiguous."""
-        import torch
-        bf, want = torch.bfloat16, self._tokens
+        want = self._tokens
         B, n, heads, d = want
         ptrs, strides, plain = [], [], True
         for name, t in views:
-            ptrs.append(_strided_addr(t, bf, name, dev))
+            ptrs.append(_strided_addr(t, _BF16, name, dev))
             if t.shape != want:
                 raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
             if t.is_contiguous():
@@ -647,7 +650,7 @@ class Plan:
         n = self._bytes.get(call)
         if n is None:
             out = ctypes.c_int64()
-            _check(getattr(library(), call)(self._h, ctypes.byref(out)), call)
+            _check(getattr(self._lib, call)(self._h, ctypes.byref(out)), call)
             n = self._bytes[call] = out.value
         return n
 
@@ -656,19 +659,18 @@ class Plan:
         (an output may be its own input)."""
         dev, s = _here(stream)
         ptrs, st = self._token_views(dev, ("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))
-        status = library().vsa_qk_norm_rope(self._h, norm._struct(self, dev), *ptrs, st, s)
+        status = self._lib.vsa_qk_norm_rope(self._h, norm._struct(self, dev), *ptrs, st, s)
         if status:
             _check(status, "vsa_qk_norm_rope")
 
     def tile_norm_rope_pack_pool(self, q, k, v, norm, qp, kp, vp, workspace, stream=None):
         """qk_norm_rope and tile_pack_pool in one pass; follow with tile_score_pooled."""
-        import torch
         dev, s = _here(stream)
         ptrs, st = self._token_views(dev, ("q", q), ("k", k), ("v", v))
-        pe, bf = self.info.packed_elems, torch.bfloat16
-        _check(library().vsa_tile_norm_rope_pack_pool(
+        pe, bf = self._pe, _BF16
+        _check(self._lib.vsa_tile_norm_rope_pack_pool(
             self._h, norm._struct(self, dev), *ptrs, st, _addr(qp, bf, "qp", dev, pe), _addr(kp, bf, "kp", dev, pe),
-            _addr(vp, bf, "vp", dev, pe), _addr(workspace, torch.uint8, "workspace", dev, self.info.workspace_bytes),
+            _addr(vp, bf, "vp", dev, pe), _addr(workspace, _U8, "workspace", dev, self._ws_bytes),
             s), "vsa_tile_norm_rope_pack_pool")
 
     def pooled(self, workspace):
@@ -690,35 +692,32 @@ class Plan:
         return self._workspace("vsa_norm_bwd_workspace")
 
     def _dw(self, norm, dw_q, dw_k, dev):
-        import torch
         _, _, heads, d = self._tokens
         want = (heads, d) if norm.per_head else (d,)
         for t, name in ((dw_q, "dw_q"), (dw_k, "dw_k")):
             if t is not None and t.shape != want:
                 raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
-        return _addr(dw_q, torch.float32, "dw_q", dev), _addr(dw_k, torch.float32, "dw_k", dev)
+        return _addr(dw_q, _F32, "dw_q", dev), _addr(dw_k, _F32, "dw_k", dev)
 
     def qk_norm_rope_bwd(self, dq_out, dk_out, q, k, norm, dq, dk, dw_q, dw_k, workspace, stream=None):
         """Gradient of qk_norm_rope: dq, dk and (unless None) the weights' dw_q, dw_k."""
-        import torch
         dev, s = _here(stream)
         ptrs, st = self._token_views(dev, ("dq_out", dq_out), ("dk_out", dk_out), ("q", q), ("k", k), ("dq", dq),
                                      ("dk", dk))
-        _check(library().vsa_qk_norm_rope_bwd(
+        _check(self._lib.vsa_qk_norm_rope_bwd(
             self._h, norm._struct(self, dev), *ptrs, st, *self._dw(norm, dw_q, dw_k, dev),
-            _addr(workspace, torch.uint8, "workspace", dev, self.norm_bwd_workspace_bytes()), s),
+            _addr(workspace, _U8, "workspace", dev, self.norm_bwd_workspace_bytes()), s),
             "vsa_qk_norm_rope_bwd")
 
     def tile_norm_rope_bwd(self, dqp, dkp, dvp, q, k, norm, dq, dk, dv, dw_q, dw_k, workspace, stream=None):
         """Gradient of tile_norm_rope_pack_pool: packed gradients back to token-major dq, dk, dv and to the weights."""
-        import torch
         dev, s = _here(stream)
-        pe, bf = self.info.packed_elems, torch.bfloat16
+        pe, bf = self._pe, _BF16
         ptrs, st = self._token_views(dev, ("q", q), ("k", k), ("dq", dq), ("dk", dk), ("dv", dv))
-        _check(library().vsa_tile_norm_rope_bwd(
+        _check(self._lib.vsa_tile_norm_rope_bwd(
             self._h, norm._struct(self, dev), _addr(dqp, bf, "dqp", dev, pe), _addr(dkp, bf, "dkp", dev, pe),
             _addr(dvp, bf, "dvp", dev, pe), *ptrs, st, *self._dw(norm, dw_q, dw_k, dev),
-            _addr(workspace, torch.uint8, "workspace", dev, self.norm_bwd_workspace_bytes()), s),
+            _addr(workspace, _U8, "workspace", dev, self.norm_bwd_workspace_bytes()), s),
             "vsa_tile_norm_rope_bwd")
 
     # ---- gradient of the sparse attention --------------------------------------------
@@ -726,46 +725,42 @@ class Plan:
         return self._workspace("vsa_attn_bwd_workspace")
 
     def _attn_bwd_args(self, dev, qp, kp, vp, op, lse, dop, idx):
-        import torch
-        pe, bf = self.info.packed_elems, torch.bfloat16
+        pe, bf = self._pe, _BF16
         return (_addr(qp, bf, "qp", dev, pe), _addr(kp, bf, "kp", dev, pe), _addr(vp, bf, "vp", dev, pe),
-                _addr(op, bf, "op", dev, pe), _addr(lse, torch.float32, "lse", dev, self.info.lse_elems),
-                _addr(dop, bf, "dop", dev, pe), _addr(idx, torch.int32, "idx", dev, self.info.index_elems))
+                _addr(op, bf, "op", dev, pe), _addr(lse, _F32, "lse", dev, self._lse),
+                _addr(dop, bf, "dop", dev, pe), _addr(idx, _I32T, "idx", dev, self._idx))
 
     def _attn_bwd_outs(self, dev, dqp, dkp, dvp, workspace):
-        import torch
-        pe, bf = self.info.packed_elems, torch.bfloat16
+        pe, bf = self._pe, _BF16
         return (_addr(dqp, bf, "dqp", dev, pe), _addr(dkp, bf, "dkp", dev, pe), _addr(dvp, bf, "dvp", dev, pe),
-                _addr(workspace, torch.uint8, "workspace", dev, self.attn_bwd_workspace_bytes()))
+                _addr(workspace, _U8, "workspace", dev, self.attn_bwd_workspace_bytes()))
 
     def sparse_attn_bwd(self, qp, kp, vp, op, lse, dop, idx, dqp, dkp, dvp, workspace, stream=None, k_per_head=None):
         """Gradient of sparse_attn on packed tiles: dqp, dkp, dvp from dop, the forward's inputs and its op, lse."""
         dev, s = _here(stream)
-        _check(library().vsa_sparse_attn_bwd(
+        _check(self._lib.vsa_sparse_attn_bwd(
             self._h, *self._attn_bwd_args(dev, qp, kp, vp, op, lse, dop, idx), _karray(k_per_head, self.desc.heads),
             *self._attn_bwd_outs(dev, dqp, dkp, dvp, workspace), s), "vsa_sparse_attn_bwd")
 
     def sparse_attn_ref_bwd(self, qp, kp, vp, op, lse, dop, idx, idx_ref, dqp, dkp, dvp, workspace, stream=None,
                             k_per_head=None):
         """Gradient of sparse_attn_ref (R2VA budgets)."""
-        import torch
         dev, s = _here(stream)
-        _check(library().vsa_sparse_attn_ref_bwd(
+        _check(self._lib.vsa_sparse_attn_ref_bwd(
             self._h, *self._attn_bwd_args(dev, qp, kp, vp, op, lse, dop, idx),
-            _addr(idx_ref, torch.int32, "idx_ref", dev, self.info.ref_index_elems),
+            _addr(idx_ref, _I32T, "idx_ref", dev, self.info.ref_index_elems),
             _karray(k_per_head, self.desc.heads), *self._attn_bwd_outs(dev, dqp, dkp, dvp, workspace), s),
             "vsa_sparse_attn_ref_bwd")
 
     # ---- linear layer with epilogue, and its gradient ---------------------------------
     @staticmethod
     def _gate(gate, rows, n_out, dev):
-        import torch
         if gate is None:
             return None, 0
         if gate.dim() != 2 or gate.shape[1] != n_out or gate.shape[0] < 1 or rows % gate.shape[0]:
             raise ValueError(f"gate must be [samples, {n_out}] with samples dividing {rows} rows, "
                              f"got {tuple(gate.shape)}")
-        return _addr(gate, torch.float32, "gate", dev), rows // gate.shape[0]
+        return _addr(gate, _F32, "gate", dev), rows // gate.shape[0]
 
     @staticmethod
     def _act(act):
@@ -776,7 +771,6 @@ class Plan:
     def linear(self, x, w, y, bias=None, act="none", gate=None, residual=None, pre=None, stream=None):
         """y = residual + gate * act(x w^T + bias): x [..., n_in], w [n_out, n_in], y [..., n_out] bf16, bias [n_out]
         and gate [samples, n_out] fp32. pre, if given, receives x w^T + bias for :meth:`linear_bwd`."""
-        import torch
         dev, s = _here(stream)
         if w.dim() != 2:
             raise ValueError(f"w must be [n_out, n_in], got {tuple(w.shape)}")
@@ -788,9 +782,9 @@ class Plan:
         if bias is not None and bias.shape != (n_out,):
             raise ValueError(f"bias must be [{n_out}], got {tuple(bias.shape)}")
         pg, per = self._gate(gate, rows, n_out, dev)
-        a = VsaLinearArgs(rows, n_in, n_out, px, ld_x, _addr(w, torch.bfloat16, "w", dev),
-                          _addr(bias, torch.float32, "bias", dev), self._act(act), pg, per, pr, ld_r, py, ld_y, pp, ld_p)
-        status = library().vsa_linear(self._h, a, s)
+        a = VsaLinearArgs(rows, n_in, n_out, px, ld_x, _addr(w, _BF16, "w", dev),
+                          _addr(bias, _F32, "bias", dev), self._act(act), pg, per, pr, ld_r, py, ld_y, pp, ld_p)
+        status = self._lib.vsa_linear(self._h, a, s)
         if status:
             _check(status, "vsa_linear")
 
@@ -799,7 +793,7 @@ class Plan:
         if samples and rows % samples:
             raise ValueError(f"{rows} rows do not divide into {samples} samples")
         n = ctypes.c_int64()
-        _check(library().vsa_linear_bwd_workspace(self._h, int(rows), int(n_in), int(n_out),
+        _check(self._lib.vsa_linear_bwd_workspace(self._h, int(rows), int(n_in), int(n_out),
                                                   rows // samples if samples else 0, ctypes.byref(n)),
                "vsa_linear_bwd_workspace")
         return n.value
@@ -808,7 +802,6 @@ class Plan:
                    workspace=None, stream=None):
         """Gradient of :meth:`linear`: any of dx [..., n_in], dw [n_out, n_in] (bf16), dbias [n_out] and dgate
         [samples, n_out] (fp32); that of the residual is dy itself."""
-        import torch
         dev, s = _here(stream)
         if w.dim() != 2:
             raise ValueError(f"w must be [n_out, n_in], got {tuple(w.shape)}")
@@ -831,11 +824,11 @@ class Plan:
         need = self.linear_bwd_workspace_bytes(rows, n_in, n_out, gate.shape[0] if gate is not None else 0)
         if need and workspace is None:
             raise ValueError(f"this size needs a workspace of {need} bytes")
-        bf, f32 = torch.bfloat16, torch.float32
+        bf, f32 = _BF16, _F32
         a = VsaLinearGradArgs(rows, n_in, n_out, pdy, ld_dy, px, ld_x, _addr(w, bf, "w", dev), self._act(act), pp, ld_p,
                               pg, per, pdx, ld_dx, _addr(dw, bf, "dw", dev), _addr(dbias, f32, "dbias", dev),
                               _addr(dgate, f32, "dgate", dev))
-        _check(library().vsa_linear_bwd(self._h, a, _addr(workspace, torch.uint8, "workspace", dev, need), s),
+        _check(self._lib.vsa_linear_bwd(self._h, a, _addr(workspace, _U8, "workspace", dev, need), s),
                "vsa_linear_bwd")
 
     def set_wait_limit(self, limit_ns: int = 0):
