@@ -198,6 +198,27 @@ def test_block_on_a_stream_and_in_a_graph():
         assert torch.equal(t, g2[k]), k
 
 
+def test_stream_argument_and_shared_layer():
+    """stream=: the call's own allocations are that stream's; a layer that has run again refuses the older backward."""
+    import torch
+    c = Block(ragged_gpu_config(128))
+    want = c.run(save=True)
+    g0 = c.block.backward(c.dy)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        y = c.block(c.x, residual=c.residual, gate=c.gate, save=True, stream=s)
+        g1 = c.block.backward(c.dy, stream=s)
+        torch.empty(1 << 20, device="cuda").fill_(7)      # the current stream's allocations meanwhile
+    c.layer.plan.check()
+    assert torch.equal(want, y) and all(torch.equal(t, g1[k]) for k, t in g0.items())
+    q = torch.randn(*c.layer.plan.shapes()["tokens"], device="cuda").to(torch.bfloat16)
+    c.layer(q, q, q)
+    with pytest.raises(ValueError, match="run again"):
+        c.block.backward(c.dy)
+    c.layer.plan.check()
+
+
 def test_two_plans_on_two_streams():
     """Blocks with a plan each, at once on two streams: each gives what it gives alone."""
     import torch

@@ -183,6 +183,46 @@ def test_special_values_stay_in_their_rows(plan):
         check_forward(t, y[:4], None, act, dict(bias=False, gate=False, residual=False))
 
 
+@pytest.mark.parametrize("M,K,N", [(64, 2048, 128), (1200, 192, 2304), (3000, 1024, 1304)])
+def test_timeout_is_reported(M, K, N):
+    """A wait limit of a microsecond runs out (clusters that share K, single CTAs, CTA pairs): the call returns,
+    check reports it, and the next call is right."""
+    import torch
+    import tile_sparse_video_pack_b200 as T
+    plan = T.Plan(T.make_desc(1, 1, 64, 1, 8, 8, [], [(4, 4, 4)], [1]))
+    t = tensors(M, K, N, 1)
+    y = torch.empty_like(t["residual"])
+    plan.set_wait_limit(1000)
+    plan.linear(t["x"], t["w"], y)
+    try:
+        plan.check()
+    except T.VsaError as e:
+        assert "TIMEOUT" in str(e)
+    plan.set_wait_limit(0)
+    plan.linear(t["x"], t["w"], y)
+    plan.check()
+    check_forward(t, y, None, "none", dict(bias=False, gate=False, residual=False))
+
+
+def test_two_streams_share_a_plan(plan):
+    """Calls on one plan keep nothing in it: two streams at once give what one gives."""
+    import torch
+    cases = [tensors(300, 512, 1024, 1, seed=i) for i in range(2)]
+    want = []
+    for t in cases:
+        want.append(torch.empty_like(t["residual"]))
+        plan.linear(t["x"], t["w"], want[-1], bias=t["bias"], act="silu")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[torch.empty_like(w) for _ in range(8)] for w in want]
+    for i in range(8):
+        for t, s, g in zip(cases, streams, got):
+            plan.linear(t["x"], t["w"], g[i], bias=t["bias"], act="silu", stream=s)
+    plan.check()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, x) for x in g)
+
+
 def test_refusals(plan):
     import torch
     import tile_sparse_video_pack_b200 as T

@@ -300,7 +300,9 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block,
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  if (e != cudaSuccess) cudaGetLastError();   // reported here: not again by a later call
+  return e;
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

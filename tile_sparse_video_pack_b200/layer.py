@@ -23,6 +23,7 @@ class TileSparseAttention:
         if direct and not plan.info.direct_attn:
             raise ValueError("this plan's tiles are not boxes of the token-major tensors (info.direct_attn == 0)")
         self.direct = direct
+        self.runs = 0        # forwards so far: whose tiles the buffers hold
         self.bufs = plan.allocate(device, with_lse=with_lse, packed=not direct)
 
     @classmethod
@@ -36,6 +37,7 @@ class TileSparseAttention:
             out = torch.empty_like(q)
         if self.plan.info.n_ref_tiles or self.direct:
             return self.stages(q, k, v, out, stream)   # R2VA budgets, or tiles straight from q, k, v
+        self.runs += 1
         self.plan.layer_forward(q, k, v, self.proj_q, self.proj_k, self.bufs, out, stream=stream)
         return out
 
@@ -46,6 +48,7 @@ class TileSparseAttention:
         the reference tiles are scored and selected and the attention uses that selection."""
         b, p = self.bufs, self.plan
         if self.direct:
+            self.runs += 1
             p.tile_pool(q, k, b["workspace"], stream)
             p.tile_score_pooled(self.proj_q, self.proj_k, b["scores"], b["workspace"], stream)
             p.topk_select(b["scores"], b["idx"], stream)
@@ -56,6 +59,7 @@ class TileSparseAttention:
 
     def attend(self, out, stream=None):
         """The stages after packing, from the packed tiles and descriptors in the layer's buffers."""
+        self.runs += 1
         b, p = self.bufs, self.plan
         p.tile_score_pooled(self.proj_q, self.proj_k, b["scores"], b["workspace"], stream)
         p.topk_select(b["scores"], b["idx"], stream)
@@ -113,8 +117,9 @@ class TileSparseBlock:
     heads head_dim] bf16, biases fp32 or None, ``norm`` a :class:`NormRope`. q, k and v are written by one
     product and read in place by the norm-and-pack pass; with ``layer.direct`` each has its own product and the
     norm runs token-major. ``forward(..., save=True)`` keeps what :meth:`backward` needs (the gradient follows
-    the selected tiles as given; not with ``layer.direct``). The buffers belong to the block: the next forward
-    overwrites them.
+    the selected tiles as given; not with ``layer.direct``). The packed tiles stay in the layer's buffers, which
+    its next forward overwrites: backward refuses then, so blocks that are trained need a layer each. With
+    ``stream`` the whole call, its allocations too, is that stream's.
     """
 
     def __init__(self, layer: TileSparseAttention, w_qkv, w_out, norm: NormRope, b_qkv=None, b_out=None):
@@ -132,6 +137,9 @@ class TileSparseBlock:
     def forward(self, x, residual=None, gate=None, out=None, save=False, stream=None):
         """x [B, N, channels] bf16, residual [B, N, out channels], gate [B, out channels] fp32 -> y."""
         import torch
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, residual, gate, out, save)
         L, b = self.layer, self.layer.bufs
         p = L.plan
         B, N, heads, d = p.shapes()["tokens"]
@@ -145,23 +153,22 @@ class TileSparseBlock:
             q, k, v = (_new(x, B, N, heads, d) for _ in range(3))
             for i, t in enumerate((q, k, v)):
                 bias = None if self.b_qkv is None else self.b_qkv[i * width:(i + 1) * width]
-                p.linear(x, self.w_qkv[i * width:(i + 1) * width], t.view(B, N, width), bias=bias, stream=stream)
-            p.qk_norm_rope(q, k, self.norm, q, k, stream=stream)
-            L.stages(q, k, v, o, stream)
+                p.linear(x, self.w_qkv[i * width:(i + 1) * width], t.view(B, N, width), bias=bias)
+            p.qk_norm_rope(q, k, self.norm, q, k)
+            L.stages(q, k, v, o)
             qkv = None
         else:
             qkv = _new(x, B, N, 3, heads, d)
-            p.linear(x, self.w_qkv, qkv.view(B, N, 3 * width), bias=self.b_qkv, stream=stream)
+            p.linear(x, self.w_qkv, qkv.view(B, N, 3 * width), bias=self.b_qkv)
             p.tile_norm_rope_pack_pool(qkv[:, :, 0], qkv[:, :, 1], qkv[:, :, 2], self.norm, b["qp"], b["kp"], b["vp"],
-                                       b["workspace"], stream)
+                                       b["workspace"])
             if save and b["lse"] is None:
                 b["lse"] = torch.empty(p.shapes()["lse"], dtype=torch.float32, device=x.device)
-            L.attend(o, stream)
+            L.attend(o)
         y = _new(x, B, N, self.w_out.shape[0]) if out is None else out
         pre = _new(x, B, N, self.w_out.shape[0]) if save and gate is not None else None
-        p.linear(o.view(B, N, width), self.w_out, y, bias=self.b_out, gate=gate, residual=residual, pre=pre,
-                 stream=stream)
-        self._saved = (x, qkv, o, gate, pre) if save else None
+        p.linear(o.view(B, N, width), self.w_out, y, bias=self.b_out, gate=gate, residual=residual, pre=pre)
+        self._saved = (x, qkv, o, gate, pre, L.runs) if save else None
         return y
 
     __call__ = forward
@@ -172,8 +179,13 @@ class TileSparseBlock:
         import torch
         if self._saved is None:
             raise ValueError("backward follows a forward with save=True")
-        x, qkv, o, gate, pre = self._saved
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(dy)
+        x, qkv, o, gate, pre, run = self._saved
         L, b = self.layer, self.layer.bufs
+        if L.runs != run:
+            raise ValueError("the layer has run again since this block's forward: its tiles are another's")
         p = L.plan
         B, N, heads, d = p.shapes()["tokens"]
         width, f32 = heads * d, torch.float32
@@ -190,20 +202,20 @@ class TileSparseBlock:
                                p.attn_bwd_workspace_bytes(), p.norm_bwd_workspace_bytes()))
         do = torch.empty_like(o)
         p.linear_bwd(dy, o.view(B, N, width), self.w_out, dx=do.view(B, N, width), dw=g["w_out"], pre=pre, gate=gate,
-                     dbias=g["b_out"], dgate=g["gate"], workspace=ws, stream=stream)
+                     dbias=g["b_out"], dgate=g["gate"], workspace=ws)
         packed = p.shapes()["packed"]
         dop, dqp, dkp, dvp = (_new(x, *packed) for _ in range(4))
-        p.tile_pack(do, None, None, dop, None, None, stream)
+        p.tile_pack(do, None, None, dop, None, None)
         args = (b["qp"], b["kp"], b["vp"], b["op"], b["lse"], dop, b["idx"])
         if p.info.n_ref_tiles:
-            p.sparse_attn_ref_bwd(*args, b["idx_ref"], dqp, dkp, dvp, ws, stream)
+            p.sparse_attn_ref_bwd(*args, b["idx_ref"], dqp, dkp, dvp, ws)
         else:
-            p.sparse_attn_bwd(*args, dqp, dkp, dvp, ws, stream)
+            p.sparse_attn_bwd(*args, dqp, dkp, dvp, ws)
         dqkv = torch.empty_like(qkv)
         p.tile_norm_rope_bwd(dqp, dkp, dvp, qkv[:, :, 0], qkv[:, :, 1], self.norm, dqkv[:, :, 0], dqkv[:, :, 1],
-                             dqkv[:, :, 2], g["w_q"], g["w_k"], ws, stream)
+                             dqkv[:, :, 2], g["w_q"], g["w_k"], ws)
         p.linear_bwd(dqkv.view(B, N, 3 * width), x, self.w_qkv, dx=g["x"], dw=g["w_qkv"], dbias=g["b_qkv"],
-                     workspace=ws, stream=stream)
+                     workspace=ws)
         return g
 
 
@@ -219,13 +231,17 @@ class FeedForward:
         self._saved = None
 
     def forward(self, x, residual=None, gate=None, out=None, save=False, stream=None):
+        if stream is not None:
+            import torch
+            with torch.cuda.stream(stream):
+                return self.forward(x, residual, gate, out, save)
         p, lead = self.plan, x.shape[:-1]
         h = _new(x, *lead, self.w_up.shape[0])
         hidden = _new(x, *lead, self.w_up.shape[0]) if save else None
-        p.linear(x, self.w_up, h, bias=self.b_up, act=self.act, pre=hidden, stream=stream)
+        p.linear(x, self.w_up, h, bias=self.b_up, act=self.act, pre=hidden)
         y = _new(x, *lead, self.w_down.shape[0]) if out is None else out
         pre = _new(x, *lead, self.w_down.shape[0]) if save and gate is not None else None
-        p.linear(h, self.w_down, y, bias=self.b_down, gate=gate, residual=residual, pre=pre, stream=stream)
+        p.linear(h, self.w_down, y, bias=self.b_down, gate=gate, residual=residual, pre=pre)
         self._saved = (x, hidden, h, gate, pre) if save else None
         return y
 
@@ -236,6 +252,9 @@ class FeedForward:
         import torch
         if self._saved is None:
             raise ValueError("backward follows a forward with save=True")
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(dy)
         x, hidden, h, gate, pre = self._saved
         p = self.plan
         like = lambda t: None if t is None else torch.empty_like(t)
@@ -246,9 +265,8 @@ class FeedForward:
                                p.linear_bwd_workspace_bytes(rows, x.shape[-1], n_mid)))
         dh = torch.empty_like(h)
         p.linear_bwd(dy, h, self.w_down, dx=dh, dw=g["w_down"], pre=pre, gate=gate, dbias=g["b_down"], dgate=g["gate"],
-                     workspace=ws, stream=stream)
-        p.linear_bwd(dh, x, self.w_up, dx=g["x"], dw=g["w_up"], act=self.act, pre=hidden, dbias=g["b_up"], workspace=ws,
-                     stream=stream)
+                     workspace=ws)
+        p.linear_bwd(dh, x, self.w_up, dx=g["x"], dw=g["w_up"], act=self.act, pre=hidden, dbias=g["b_up"], workspace=ws)
         return g
 
 
