@@ -228,12 +228,13 @@ struct GemmMaps {
   CUtensorMap a[2], b[2];
 };
 
-constexpr int kBM = 128, kBN = 128;
+constexpr int kBM = 128;
+template <bool SPLIT, int BN>
 struct GSmem {
-  static constexpr uint32_t kA = kBM * 128, kB = kBN * 128, kStage = kA + kB;   // 64 of K
-  static constexpr int kStages = 6;
-  static constexpr uint32_t oOut = kStages * kStage;           // the epilogue warps' 4 KB each
-  static constexpr uint32_t oBar = oOut + kEWarps * 4096;
+  static constexpr uint32_t kA = kBM * 128, kB = BN * 128, kStage = kA + kB;   // 64 of K
+  static constexpr int kStages = BN == 64 && !SPLIT ? 8 : 6;
+  static constexpr uint32_t oOut = kStages * kStage;           // the epilogue warps' 4 KB each, or the shares of my rows
+  static constexpr uint32_t oBar = oOut + (SPLIT ? kBM * BN * 4 : kEWarps * 4096);
   static constexpr uint32_t oMisc = oBar + 24 * 8;
   static constexpr uint32_t oEnd = oMisc + 16;
 };
@@ -258,9 +259,9 @@ __device__ __forceinline__ Tile tile_of(const GemmParams& p, int u) {
   return r;
 }
 
-// Loads of one k block: 128 rows of a K-major operand are one box of 64 of K by
-// 128 rows, of an MN-major one two boxes of 64 columns by 64 of K.
-template <bool PAIR>
+// Loads of one k block: 128 (64) rows of a K-major operand are one box of 64 of K by
+// that many rows, of an MN-major one two boxes (one) of 64 columns by 64 of K.
+template <bool PAIR, int ROWS>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, bool mn, int row0, int kb, uint32_t fb) {
   auto load = [&](uint32_t d, int x, int y) {
     if (PAIR) tma_load_2d_pair(d, map, x, y, fb);
@@ -268,7 +269,7 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
   };
   if (mn) {
     load(dst, row0, kb * 64);
-    load(dst + 8192, row0 + 64, kb * 64);
+    if (ROWS == 128) load(dst + 8192, row0 + 64, kb * 64);
   } else {
     load(dst, kb * 64, row0);
   }
@@ -279,25 +280,24 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
 }
 __device__ __forceinline__ uint32_t operand_step(bool mn) { return (mn ? 2048u : 32u) >> 4; }
 
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {   // addr: an address mapped into a CTA of the cluster
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+__device__ __forceinline__ void st_cluster(uint32_t addr, const uint32_t* v) {   // addr: mapped into a CTA of the cluster
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                : "memory");
-  return v;
 }
 
 // SPLIT = false: every CTA works through tiles on its own, the epilogue of one tile
 // under the products of the next. SPLIT = true, for problems with few tiles: the
-// `splits` CTAs of a cluster take a share of a tile's K each, leave their fp32
-// accumulators in their own shared memory (the stages, all consumed by then), and
-// each joins 1 / splits of the rows from all of them, in rank order -- one launch,
-// no partial sums in global memory, the same result every time.
-template <bool SPLIT>
+// `splits` CTAs of a cluster (2, 4 or 8) take a share of a tile's K each and write
+// their fp32 accumulators, 128 / splits rows to each CTA, into that CTA's shared
+// memory; each joins its rows' shares in rank order -- one launch, no partial sums
+// in global memory, the same result every time. Writing to the joining CTA takes
+// the remote latency once, before the barrier; reading from the others took it
+// again for every row. The exchange runs at some 13 bytes a cycle and CTA, so a split
+// tile has 64 columns, and rows past the matrix are not sent.
+template <bool SPLIT, int BN>
 __global__ void __launch_bounds__(kGThreads, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams prm) {
-  using L = GSmem;
+  using L = GSmem<SPLIT, BN>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
   const int splits = SPLIT ? prm.splits : 1;
   const int rank = SPLIT ? int(cluster_rank()) : 0;
   const int u0 = int(blockIdx.x) / splits, du = int(gridDim.x) / splits;
-  constexpr uint32_t kCols = 2 * kBN;            // two accumulators
+  constexpr uint32_t kCols = 2 * BN;            // two accumulators
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < prm.n_prod; ++i) {
@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
+  if constexpr (SPLIT) cluster_sync();           // the others' shared memory exists from here on
   allow_successor();
   wait_predecessor();
 
@@ -356,14 +357,14 @@ __global__ void __launch_bounds__(kGThreads, 1)
           if (!(ok = wait_bar(bar(G_EMPTY + st), ((it / L::kStages) & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
           const uint32_t sa = sbase + st * L::kStage;
           mbar_expect_tx(bar(G_FULL + st), L::kStage);
-          load_operand<false>(sa, ta, pr.a_mn, t.m * kBM, kb, bar(G_FULL + st));
-          load_operand<false>(sa + L::kA, tb, pr.b_mn, t.n * kBN, kb, bar(G_FULL + st));
+          load_operand<false, 128>(sa, ta, pr.a_mn, t.m * kBM, kb, bar(G_FULL + st));
+          load_operand<false, BN>(sa + L::kA, tb, pr.b_mn, t.n * BN, kb, bar(G_FULL + st));
         }
       }
       __syncwarp();
     } else if (warp == 1) {
       if (lane == 0 && ok) {
-        const uint32_t idesc = idesc_bf16(kBM, kBN, pr.a_mn, pr.b_mn);
+        const uint32_t idesc = idesc_bf16(kBM, BN, pr.a_mn, pr.b_mn);
         const uint32_t as = operand_step(pr.a_mn), bs = operand_step(pr.b_mn);
         ok = wait_bar(bar(G_AEMPTY + ab), ((n >> 1) & 1) ^ 1, abort_flag, gerr, prm.wait_ns);
         for (int kb = k0; kb < k1 && ok; ++kb, ++it) {
@@ -374,80 +375,79 @@ __global__ void __launch_bounds__(kGThreads, 1)
           const uint64_t da = operand_desc(sa, pr.a_mn), db = operand_desc(sa + L::kA, pr.b_mn);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)         // 16 of K per instruction
-            tc_mma(tmem + ab * kBN, da + kk * as, db + kk * bs, idesc, (kb > k0 || kk > 0) ? 1u : 0u);
+            tc_mma(tmem + ab * BN, da + kk * as, db + kk * bs, idesc, (kb > k0 || kk > 0) ? 1u : 0u);
           tc_commit(bar(G_EMPTY + st));
         }
         if (ok) tc_commit(bar(G_AFULL + ab));
       }
       __syncwarp();
     } else if (ok) {
-      const int ew = warp - 2, q4 = warp & 3, c0 = (ew >> 2) * (kBN / 2);   // my lanes and columns
+      const int ew = warp - 2, q4 = warp & 3, c0 = (ew >> 2) * (BN / 2);   // my lanes and columns
       StripRows rows;
       Chunk next;
       if constexpr (!SPLIT) {                    // while the products run
         rows = strip_rows(pr.ep, pr.M, int64_t(t.m) * kBM + q4 * 32, lane);
-        next = load_chunk(pr.ep, rows, pr.N, t.n * kBN + c0, lane);
+        next = load_chunk(pr.ep, rows, pr.N, t.n * BN + c0, lane);
       }
       ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after();
 #pragma unroll 1
-        for (int c = c0; c < c0 + kBN / 2; c += 32) {
+        for (int c = c0; c < c0 + BN / 2; c += 32) {
           uint32_t r[32];
-          tmem_ld32(tmem + ab * kBN + (uint32_t(q4 * 32) << 16) + c, r);
+          tmem_ld32(tmem + ab * BN + (uint32_t(q4 * 32) << 16) + c, r);
           tmem_wait_ld(r);
-          if (c + 32 >= c0 + kBN / 2) {          // the accumulator is read: the next tile may use it
+          if (c + 32 >= c0 + BN / 2) {          // the accumulator is read: the next tile may use it
             tc_fence_before();
             warp_arrive(bar(G_AEMPTY + ab));
           }
-          if constexpr (SPLIT) {                 // row q4 * 32 + lane of 512 bytes, 16-byte chunks swizzled by the row
-            uint8_t* row = smem + (q4 * 32 + lane) * (kBN * 4);
+          if constexpr (SPLIT) {
+            // share `rank` at the CTA that joins this row: rows of BN floats, 16-byte chunks swizzled by the row
+            const int row = q4 * 32 + lane, per = kBM / splits, owner = row / per;
+            const uint32_t to = map_to_rank(sbase + L::oOut + uint32_t(rank * per + row % per) * (BN * 4), owner);
+            if (int64_t(t.m) * kBM + row < pr.M) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(row + (((c >> 2) + i) ^ (lane & 7)) * 16) =
-                  make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+              for (int i = 0; i < 8; ++i) st_cluster(to + (((c >> 2) + i) ^ (row & 7)) * 16, r + 4 * i);
+            }
           } else {
             const Chunk in = next;
-            if (c + 32 < c0 + kBN / 2) next = load_chunk(pr.ep, rows, pr.N, t.n * kBN + c + 32, lane);
-            store_chunk(pr.ep, rows, in, pr.N, t.n * kBN + c, r, smem + L::oOut + ew * 4096, lane);
+            if (c + 32 < c0 + BN / 2) next = load_chunk(pr.ep, rows, pr.N, t.n * BN + c + 32, lane);
+            store_chunk(pr.ep, rows, in, pr.N, t.n * BN + c, r, smem + L::oOut + ew * 4096, lane);
           }
         }
       }
     }
     if constexpr (SPLIT) {
-      cluster_sync();                            // every CTA's accumulator is in its shared memory
+      // what the join needs besides the shares, before the barrier
+      constexpr int LPR = BN / 8, RPW = 32 / LPR;     // lanes to a row (eight columns each), rows per warp and step
+      const int per = kBM / splits, cg = lane % LPR;  // rows this CTA joins
+      const int col = t.n * BN + 8 * cg;
+      float bias[8] = {};
+      if (warp >= 2 && ok && col < pr.N) load_bias(pr.ep, col, bias);
+      cluster_sync();                            // every share is where it is joined
       if (warp >= 2 && ok) {
-        const int r0 = kBM * rank / splits, r1 = kBM * (rank + 1) / splits;
-        const int cg = lane & 15;                // eight columns, sixteen lanes to a row
-        const int col = t.n * kBN + 8 * cg;
-        float b[8];
-        if (col < pr.N) load_bias(pr.ep, col, b);
-        for (int rr = r0 + (warp - 2) * 2 + (lane >> 4); rr < r1; rr += 2 * kEWarps) {
-          const int64_t row = int64_t(t.m) * kBM + rr;
+        for (int rr = (warp - 2) * RPW + lane / LPR; rr < per; rr += RPW * kEWarps) {
+          const int in_tile = rank * per + rr;
+          const int64_t row = int64_t(t.m) * kBM + in_tile;
           if (row >= pr.M || col >= pr.N) continue;
           const uint4 res = load_residual(pr.ep, row, col);
-          const uint32_t lo = sbase + rr * (kBN * 4) + ((2 * cg) ^ (rr & 7)) * 16;
-          const uint32_t hi = sbase + rr * (kBN * 4) + ((2 * cg + 1) ^ (rr & 7)) * 16;
-          float4 x[8], y[8];                     // all loads before the first sum: each takes about a microsecond
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-            if (s < splits) {
-              x[s] = ld_cluster(map_to_rank(lo, s));
-              y[s] = ld_cluster(map_to_rank(hi, s));
-            }
           float v[8] = {};
 #pragma unroll
           for (int s = 0; s < 8; ++s)
             if (s < splits) {
-              v[0] += x[s].x; v[1] += x[s].y; v[2] += x[s].z; v[3] += x[s].w;
-              v[4] += y[s].x; v[5] += y[s].y; v[6] += y[s].z; v[7] += y[s].w;
+              const uint8_t* at = smem + L::oOut + (s * per + rr) * (BN * 4);
+              const float4 x = *reinterpret_cast<const float4*>(at + ((2 * cg) ^ (in_tile & 7)) * 16);
+              const float4 y = *reinterpret_cast<const float4*>(at + ((2 * cg + 1) ^ (in_tile & 7)) * 16);
+              v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+              v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
             }
-          store8(pr.ep, row, col, v, b, res, gate_row(pr.ep, row));
+          store8(pr.ep, row, col, v, bias, res, gate_row(pr.ep, row));
         }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the stages are loaded again after these accesses
-      cluster_sync();                            // every CTA has read: the shared memory may be reused or released
+      // every CTA has read its shares before any is written again; a CTA whose shares are all
+      // in may end
+      if (u + du < prm.units) cluster_sync();
     }
   }
   if (warp == 0 && lane == 0 && *abort_flag)     // let the copies land before shared memory is released
@@ -538,8 +538,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           const uint32_t fb = map_to_rank(bar(G_FULL + st), 0);
           const uint32_t sa = sbase + st * L::kStage, sb = sa + L::kA;
           if (rank == 0) mbar_expect_tx(bar(G_FULL + st), 2 * L::kStage);
-          load_operand<true>(sa, &maps.a[0], a_mn, m0, kb, fb);
-          load_operand<true>(sb, &maps.b[0], b_mn, n0, kb, fb);
+          load_operand<true, 128>(sa, &maps.a[0], a_mn, m0, kb, fb);
+          load_operand<true, 128>(sb, &maps.b[0], b_mn, n0, kb, fb);
         }
       }
       // every stage is consumed (in both CTAs) before the CTA may end; after an abort the
@@ -844,20 +844,20 @@ bool use_pairs(const vsa_plan* p, int64_t M, int64_t N) {
   return cdiv64(M, 256) * cdiv64(N, 256) * 2 >= p->num_sms * 3 / 4;
 }
 
-bool add_product(GemmMaps& maps, GemmParams& prm, const Problem& q, int tile) {
+// tile_m x tile_n per unit; a CTA loads 128 rows of A and b_rows of B.
+bool add_product(GemmMaps& maps, GemmParams& prm, const Problem& q, int tile_m, int tile_n, int b_rows) {
   const int i = prm.n_prod++;
-  // either kernel's CTA loads 128 rows of each operand
   const bool ma = q.a_mn ? make_map2(&maps.a[i], q.a, q.K, q.M, q.ld_a, 64, 64)
                          : make_map2(&maps.a[i], q.a, q.M, q.K, q.ld_a, 64, 128);
   const bool mb = q.b_mn ? make_map2(&maps.b[i], q.b, q.K, q.N, q.ld_b, 64, 64)
-                         : make_map2(&maps.b[i], q.b, q.N, q.K, q.ld_b, 64, 128);
+                         : make_map2(&maps.b[i], q.b, q.N, q.K, q.ld_b, 64, b_rows);
   Product& r = prm.prod[i];
   r.ep = q.ep;
   r.M = int32_t(q.M);
   r.N = int32_t(q.N);
   r.kblocks = int32_t(cdiv64(q.K, 64));
-  r.tiles_m = int32_t(cdiv64(q.M, tile));
-  r.tiles_n = int32_t(cdiv64(q.N, tile));
+  r.tiles_m = int32_t(cdiv64(q.M, tile_m));
+  r.tiles_n = int32_t(cdiv64(q.N, tile_n));
   r.a_mn = q.a_mn;
   r.b_mn = q.b_mn;
   prm.units += r.tiles_m * r.tiles_n;
@@ -875,39 +875,44 @@ cudaError_t run_products(const vsa_plan* p, const Problem* q, int n, cudaStream_
     prm.group = kGroup;
     prm.splits = 1;
   };
-  bool single[2] = {};
+  const unsigned sms = unsigned(p->num_sms);
+  int64_t units128 = 0, units64 = 0, kb = 1 << 30;   // tiles of the single CTAs' products; k blocks of the shortest
   for (int i = 0; i < n; ++i) {
-    single[i] = !use_pairs(p, q[i].M, q[i].N);
-    if (single[i]) continue;
+    if (!use_pairs(p, q[i].M, q[i].N)) {
+      units128 += cdiv64(q[i].M, 128) * cdiv64(q[i].N, 128);
+      units64 += cdiv64(q[i].M, 128) * cdiv64(q[i].N, 64);
+      kb = cdiv64(q[i].K, 64) < kb ? cdiv64(q[i].K, 64) : kb;
+      continue;
+    }
     start();
-    if (!add_product(maps, prm, q[i], 256)) return cudaErrorInvalidValue;
-    const int smem = 1024 + int(PSmem::oEnd);
-    const int most = p->num_sms / 2;
-    const cudaError_t r = launch_after(gemm_pair_kernel, dim3(2 * unsigned(prm.units < most ? prm.units : most)), kGThreads,
-                                       size_t(smem), s, 1, maps, prm);
+    if (!add_product(maps, prm, q[i], 256, 256, 128)) return cudaErrorInvalidValue;
+    const unsigned pairs = unsigned(prm.units) < sms / 2 ? unsigned(prm.units) : sms / 2;
+    const cudaError_t r = launch_after(gemm_pair_kernel, dim3(2 * pairs), unsigned(kGThreads),
+                                       size_t(1024 + PSmem::oEnd), s, 1, maps, prm);
     if (r != cudaSuccess) return r;
   }
+  if (units128 == 0) return cudaSuccess;
+  // Tiles of 128 x 64 while those of 128 x 128 leave SMs without one, and K shared by clusters
+  // of 2, 4 or 8 while the clusters fit the SMs at once (clusters of 8 do not pack them all) and
+  // every CTA keeps two k blocks.
+  const bool narrow = units128 <= sms;
+  int splits = 1;
+  while (splits < 8 && units64 * splits * 2 <= sms * 9 / 10 && kb >= splits * 4) splits *= 2;
   start();
-  int kb = 1 << 30;                              // k blocks of the shortest product
-  for (int i = 0; i < n; ++i) {
-    if (!single[i]) continue;
-    if (!add_product(maps, prm, q[i], 128)) return cudaErrorInvalidValue;
-    const int k = prm.prod[prm.n_prod - 1].kblocks;
-    kb = k < kb ? k : kb;
-  }
-  if (prm.n_prod == 0) return cudaGetLastError();
-  // Few tiles: clusters of 2, 4 or 8 share a tile's K, while the clusters fill no more
-  // than three quarters of the SMs (clusters of 8 do not pack the rest) and each CTA
-  // has two k blocks at least.
-  while (prm.splits < 8 && int64_t(prm.units) * prm.splits * 2 <= p->num_sms * 3 / 4 && kb >= prm.splits * 4)
-    prm.splits *= 2;
-  const int smem = 1024 + int(GSmem::oEnd);
-  if (prm.splits == 1) {
-    return launch_after(gemm_kernel<false>, dim3(unsigned(prm.units < p->num_sms ? prm.units : p->num_sms)), kGThreads,
-                        size_t(smem), s, 1, maps, prm);
-  }
-  return launch_after(gemm_kernel<true>, dim3(unsigned(prm.units * prm.splits)), kGThreads, size_t(smem), s,
-                      unsigned(prm.splits), maps, prm);
+  prm.splits = splits;
+  for (int i = 0; i < n; ++i)
+    if (!use_pairs(p, q[i].M, q[i].N) &&
+        !add_product(maps, prm, q[i], 128, narrow ? 64 : 128, narrow ? 64 : 128))
+      return cudaErrorInvalidValue;
+  if (splits > 1)
+    return launch_after(gemm_kernel<true, 64>, dim3(unsigned(prm.units * splits)), unsigned(kGThreads),
+                        size_t(1024 + GSmem<true, 64>::oEnd), s, unsigned(splits), maps, prm);
+  const dim3 grid(unsigned(prm.units) < sms ? unsigned(prm.units) : sms);
+  if (narrow)
+    return launch_after(gemm_kernel<false, 64>, grid, unsigned(kGThreads), size_t(1024 + GSmem<false, 64>::oEnd), s, 1,
+                        maps, prm);
+  return launch_after(gemm_kernel<false, 128>, grid, unsigned(kGThreads), size_t(1024 + GSmem<false, 128>::oEnd), s, 1,
+                      maps, prm);
 }
 
 template <int R, int F>
@@ -965,8 +970,9 @@ GradPlan grad_plan(const vsa_plan* p, int64_t rows, int64_t N, int act, bool gat
 cudaError_t prepare_linear() {
   const auto at = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel, at, 1024 + int(PSmem::oEnd));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_kernel<false>, at, 1024 + int(GSmem::oEnd));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_kernel<true>, at, 1024 + int(GSmem::oEnd));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_kernel<false, 128>, at, 1024 + int(GSmem<false, 128>::oEnd));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_kernel<false, 64>, at, 1024 + int(GSmem<false, 64>::oEnd));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_kernel<true, 64>, at, 1024 + int(GSmem<true, 64>::oEnd));
   return e;
 }
 
