@@ -253,7 +253,11 @@ def _strided_addr(t, dtype, name, dev):
 
 def _matrix(t, cols, name, dev, rows=None):
     """(address, row stride, rows) of a bf16 [..., cols] tensor whose leading dimensions form one row axis."""
-    p = _strided_addr(t, _BF16, name, dev)
+    try:
+        ok = t.dtype is _BF16 and t.get_device() == dev
+    except AttributeError:
+        ok = False
+    p = t.data_ptr() if ok else _strided_addr(t, _BF16, name, dev)
     shape = t.shape
     if not shape or shape[-1] != cols:
         raise ValueError(f"{name} must be [..., {cols}], got {tuple(shape)}")
@@ -359,7 +363,7 @@ class Plan:
         self._tokens = (desc.batch, inf.n_tokens, desc.heads, desc.head_dim)
         self._pe, self._ws_bytes, self._lse, self._idx = (inf.packed_elems, inf.workspace_bytes, inf.lse_elems,
                                                           inf.index_elems)
-        self._bytes = {}               # workspace sizes of this plan, by call
+        self._bytes = {}               # workspace sizes of this plan, by call and sizes
 
     @classmethod
     def from_config(cls, cfg, sparsity: float, k_per_head=None):
@@ -631,9 +635,14 @@ class Plan:
         B, n, heads, d = want
         ptrs, strides, plain = [], [], True
         for name, t in views:
-            ptrs.append(_strided_addr(t, _BF16, name, dev))
-            if t.shape != want:
+            try:
+                ok = t.dtype is _BF16 and t.get_device() == dev and t.shape == want
+            except AttributeError:
+                ok = False
+            if not ok:
+                _strided_addr(t, _BF16, name, dev)
                 raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+            ptrs.append(t.data_ptr())
             if t.is_contiguous():
                 strides += (n * heads * d, heads * d)
                 continue
@@ -790,13 +799,19 @@ class Plan:
 
     def linear_bwd_workspace_bytes(self, rows, n_in, n_out, samples=0):
         """Workspace of :meth:`linear_bwd`; samples: rows of the gate, 0 without one."""
-        if samples and rows % samples:
-            raise ValueError(f"{rows} rows do not divide into {samples} samples")
-        n = ctypes.c_int64()
-        _check(self._lib.vsa_linear_bwd_workspace(self._h, int(rows), int(n_in), int(n_out),
-                                                  rows // samples if samples else 0, ctypes.byref(n)),
-               "vsa_linear_bwd_workspace")
-        return n.value
+        key = (rows, n_in, n_out, samples)
+        n = self._bytes.get(key)
+        if n is None:
+            if samples and rows % samples:
+                raise ValueError(f"{rows} rows do not divide into {samples} samples")
+            out = ctypes.c_int64()
+            _check(self._lib.vsa_linear_bwd_workspace(self._h, int(rows), int(n_in), int(n_out),
+                                                      rows // samples if samples else 0, ctypes.byref(out)),
+                   "vsa_linear_bwd_workspace")
+            if len(self._bytes) > 256:           # sizes that keep changing: do not keep them all
+                self._bytes.clear()
+            n = self._bytes[key] = out.value
+        return n
 
     def linear_bwd(self, dy, x, w, dx=None, dw=None, act="none", pre=None, gate=None, dbias=None, dgate=None,
                    workspace=None, stream=None):
