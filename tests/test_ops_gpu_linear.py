@@ -62,7 +62,8 @@ def check_forward(t, got, pre, act, use):
 SIZES = [(1, 8, 8), (1, 2048, 328), (2, 136, 1040), (3, 1480, 64), (8, 256, 2056), (9, 520, 200), (16, 64, 128),
          (17, 72, 264), (64, 128, 256), (77, 1480, 520), (127, 64, 136), (128, 128, 128), (129, 200, 72),
          (200, 2048, 96), (257, 512, 512), (515, 328, 1000), (1200, 192, 2304), (2500, 64, 640),
-         (3000, 136, 1304), (1100, 2600, 2904), (7201, 520, 520), (2, 72, 9480), (7, 1032, 9480), (4, 520, 1024)]
+         (3000, 136, 1304), (1100, 2600, 2904), (7201, 520, 520), (2, 72, 9480), (7, 1032, 9480), (4, 520, 1024),
+         (16, 2048, 9480), (13, 136, 40), (12, 1096, 1544), (5, 1560, 72), (1, 8, 16), (77, 2048, 1024)]
 
 
 @pytest.mark.parametrize("act", ["none", "gelu_tanh", "silu"])

@@ -618,79 +618,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// A few rows (a timestep's conditioning, single tokens): bound by reading W once, which
-// the tensor cores' 128-row tiles do with a few CTAs only. A warp takes F output
-// columns (rows of W) and strides over K, 16 bytes per lane and load, against R
-// rows of x; the products of neighbouring k are kept as packed pairs. KS = 8: the
-// block's eight warps share K instead, for few columns. fp32 throughout.
-template <int R, int F, int KS>
-__global__ void __launch_bounds__(256) skinny_kernel(const __nv_bfloat16* __restrict__ x, int64_t ld_x,
-                                                     const __nv_bfloat16* __restrict__ w, int rows, int K, int N,
-                                                     const __grid_constant__ Epilogue ep) {
-  __shared__ float part[KS > 1 ? 8 : 1][R * F];
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Up to sixteen rows (a timestep's conditioning, single tokens): bound by reading W once,
+// so no tile is staged. A block takes 8 T columns, its W warps every W-th chunk of 64 of
+// K; their sums are joined in shared memory in the warps' order and stored by the common
+// epilogue. T: eights of rows. A lane's 16-byte load holds eight k of one column of W, or
+// of one row of x, which is two steps of m16n8k16 fragments when the k within a chunk are
+// taken in the lanes' order, the same for both operands: nothing is shuffled, and 16 rows
+// cost no more arithmetic than one (the warp-level instruction takes its operands from
+// registers; its rate does not matter here). Each warp keeps U chunks of loads in flight.
+// Rows past the last are zeros in registers. fp32 products on the plain cores took 20.8 us
+// for 8 rows at 1,536 x 9,216, this takes 6.5 (4.3 at the copy rate) and 6.4 for one row;
+// the tiles of 128 rows take 15.
+template <int T, int W, int U>
+__global__ void __launch_bounds__(W * 32) few_rows_kernel(const __nv_bfloat16* __restrict__ x, int64_t ld_x,
+                                                          const __nv_bfloat16* __restrict__ w, int rows, int K, int N,
+                                                          const __grid_constant__ Epilogue ep) {
+  __shared__ float4 part[W][T * 8][T * 2];
   allow_successor();
   wait_predecessor();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n0 = (KS > 1 ? int(blockIdx.x) : int(blockIdx.x) * 8 + warp) * F;
-  uint64_t acc[F][R] = {};
-  if (n0 < N) {
-    const __nv_bfloat16* wp[F];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int n0 = int(blockIdx.x) * 8 * T;
+  const __nv_bfloat16 *wp[T], *xp[T];
+  bool w_in[T], x_in[T];
 #pragma unroll
-    for (int f = 0; f < F; ++f) wp[f] = w + int64_t(n0 + f < N ? n0 + f : n0) * K;
-    const __nv_bfloat16* xp[R];
+  for (int j = 0; j < T; ++j) {
+    w_in[j] = n0 + j * 8 < N;                      // N is a multiple of eight, and so is K
+    wp[j] = w + int64_t(w_in[j] ? n0 + j * 8 + g : 0) * K;
+    x_in[j] = g + j * 8 < rows;
+    xp[j] = x + int64_t(x_in[j] ? g + j * 8 : 0) * ld_x;
+  }
+  uint4 wv[U][2][T], xv[U][2][T];
+  auto load = [&](int d, int k0) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) xp[r] = x + int64_t(r < rows ? r : 0) * ld_x;
-#pragma unroll 2
-    for (int k = (KS > 1 ? warp * 32 + lane : lane) * 8; k < K; k += 256 * KS) {   // K is a multiple of eight
-      uint4 wv[F], xv[R];
+    for (int i = 0; i < 2; ++i) {
+      const int k = k0 + i * 32 + t * 8;
 #pragma unroll
-      for (int f = 0; f < F; ++f) wv[f] = __ldcs(reinterpret_cast<const uint4*>(wp[f] + k));
-#pragma unroll
-      for (int r = 0; r < R; ++r) xv[r] = __ldg(reinterpret_cast<const uint4*>(xp[r] + k));
-      float xf[R][8];
-#pragma unroll
-      for (int r = 0; r < R; ++r) bf16x8_to_f32(xv[r], xf[r]);
-#pragma unroll
-      for (int f = 0; f < F; ++f) {
-        float wf[8];
-        bf16x8_to_f32(wv[f], wf);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int i = 0; i < 8; i += 2)
-            acc[f][r] = ffma2(f2pack(wf[i], wf[i + 1]), f2pack(xf[r][i], xf[r][i + 1]), acc[f][r]);
+      for (int j = 0; j < T; ++j) {
+        wv[d][i][j] = k < K && w_in[j] ? __ldcs(reinterpret_cast<const uint4*>(wp[j] + k)) : make_uint4(0, 0, 0, 0);
+        xv[d][i][j] = k < K && x_in[j] ? __ldg(reinterpret_cast<const uint4*>(xp[j] + k)) : make_uint4(0, 0, 0, 0);
       }
     }
-  }
-  // lane f * R + r ends up with the sum of column f and row r
-  float mine = 0.f;
+  };
+  float acc[T][4] = {};
 #pragma unroll
-  for (int f = 0; f < F; ++f)
+  for (int d = 0; d < U; ++d) load(d, (d * W + warp) * 64);
+  for (int k0 = warp * 64; k0 < K; k0 += 64 * W * U) {     // the same steps for all lanes: a product is the whole warp's
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float lo, hi;
-      f2unpack(acc[f][r], lo, hi);
-      float s = lo + hi;
+    for (int d = 0; d < U; ++d) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == f * R + r) mine = s;
+      for (int i = 0; i < 2; ++i) {
+        const uint4 lo = xv[d][i][0], hi = T > 1 ? xv[d][i][T - 1] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+          mma_16x8x16(acc[j], lo.x, hi.x, lo.y, hi.y, wv[d][i][j].x, wv[d][i][j].y);
+          mma_16x8x16(acc[j], lo.z, hi.z, lo.w, hi.w, wv[d][i][j].z, wv[d][i][j].w);
+        }
+      }
+      load(d, k0 + 64 * W * (U + d));
     }
-  if constexpr (KS > 1) {
-    if (lane < R * F) part[warp][lane] = mine;
-    __syncthreads();
-    if (warp != 0) return;
-    mine = 0.f;
-    if (lane < R * F)
-      for (int i = 0; i < 8; ++i) mine += part[i][lane];
   }
-  const int col = n0 + lane / R, row = lane % R;
-  if (lane >= R * F || col >= N || row >= rows) return;
-  float v[8] = {mine + (ep.bias ? __ldg(ep.bias + col) : 0.f)};
-  if (ep.pre) ep.pre[row * ep.ld_pre + col] = __float2bfloat16_rn(v[0]);
-  act_fwd(v, ep.act);
-  if (ep.gate) v[0] *= __ldg(ep.gate + (row / ep.rows_per_gate) * ep.ld_gate + col);
-  if (ep.residual) v[0] += __bfloat162float(ep.residual[row * ep.ld_res + col]);
-  ep.out[row * ep.ld_out + col] = __float2bfloat16_rn(v[0]);
+#pragma unroll
+  for (int j = 0; j < T; ++j)
+#pragma unroll
+    for (int r = 0; r < T; ++r)
+      reinterpret_cast<float2*>(&part[warp][r * 8 + g][j * 2])[t] = make_float2(acc[j][2 * r], acc[j][2 * r + 1]);
+  __syncthreads();
+  const int row = int(threadIdx.x) / T, j = int(threadIdx.x) % T, col = n0 + j * 8;
+  if (row >= rows || col >= N) return;             // rows <= 8 T
+  float v[8] = {}, b[8];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float4 lo = part[i][row][j * 2], hi = part[i][row][j * 2 + 1];
+    v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+    v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+  }
+  load_bias(ep, col, b);
+  store8(ep, row, col, v, b, load_residual(ep, row, col), gate_row(ep, row));
 }
 
 // ----------------------------------------------------- gradient of the rest ----
@@ -838,10 +849,13 @@ struct Problem {
   Epilogue ep;
 };
 
-// Pairs of CTAs on 256 x 256 tiles from the point where those fill most of the SMs,
-// else single CTAs on 128 x 128 tiles.
+// Rounds of tiles over the SMs decide between pairs of CTAs on 256 x 256 tiles and single
+// CTAs on 128 x 128 ones: a round of pairs, four times a tile's work on two SMs, takes about 1.1
+// times as long (K 2,048, us, singles / pairs: 1,024 x 2,048 17.7 / 18.6, one round each; 512 x 5,120
+// 30.2 / 19.6, two and one; 3,584 x 2,048 56 / 31, four and two).
 bool use_pairs(const vsa_plan* p, int64_t M, int64_t N) {
-  return cdiv64(M, 256) * cdiv64(N, 256) * 2 >= p->num_sms * 3 / 4;
+  const int64_t pairs = cdiv64(cdiv64(M, 256) * cdiv64(N, 256), p->num_sms / 2);
+  return 11 * pairs < 10 * cdiv64(cdiv64(M, 128) * cdiv64(N, 128), p->num_sms);
 }
 
 // tile_m x tile_n per unit; a CTA loads 128 rows of A and b_rows of B.
@@ -892,12 +906,14 @@ cudaError_t run_products(const vsa_plan* p, const Problem* q, int n, cudaStream_
     if (r != cudaSuccess) return r;
   }
   if (units128 == 0) return cudaSuccess;
-  // Tiles of 128 x 64 while those of 128 x 128 leave SMs without one, and K shared by clusters
-  // of 2, 4 or 8 while the clusters fit the SMs at once (clusters of 8 do not pack them all) and
-  // every CTA keeps two k blocks.
-  const bool narrow = units128 <= sms;
+  // Tiles of 128 x 64 while one round of them covers the products (K 2,048, us: 128 tiles of 64
+  // columns 14.9, the 64 of 128 columns 17.2; 160 tiles of 64 columns 26.1, 80 of 128 17.6), and K
+  // shared by clusters of 2, 4 or 8 while the clusters fit the SMs at once and every CTA keeps two k
+  // blocks (32 tiles, shared by 1, 2, 4: 14.7, 10.7, 8.7). Clusters of 8 leave more SMs out (16 tiles of
+  // K 1,024, shared by 4 and 8: 7.4 and 12.0; 14 tiles: 6.4 and 6.3; 4 tiles of K 2,048: 6.6 and 5.9).
+  const bool narrow = units64 <= sms;
   int splits = 1;
-  while (splits < 8 && units64 * splits * 2 <= sms * 9 / 10 && kb >= splits * 4) splits *= 2;
+  while (splits < 8 && units64 * splits * 2 <= sms * (splits == 4 ? 8 : 9) / 10 && kb >= splits * 4) splits *= 2;
   start();
   prm.splits = splits;
   for (int i = 0; i < n; ++i)
@@ -915,29 +931,21 @@ cudaError_t run_products(const vsa_plan* p, const Problem* q, int n, cudaStream_
                       maps, prm);
 }
 
-template <int R, int F>
-cudaError_t run_skinny(const Problem& q, int ks, cudaStream_t s) {
+// Sixteen warps share a block's K where the blocks are few, four where they fill the SMs
+// several times over or K is short (one row, us, sixteen / four warps: K 2,048 by 512 columns
+// 2.3 / 2.5, by 2,048 3.3 / 4.3, by 8,192 9.8 / 7.0; K 512 by 1,536 2.1 / 1.8).
+cudaError_t run_few_rows(const vsa_plan* p, const Problem& q, cudaStream_t s) {
   auto* x = static_cast<const __nv_bfloat16*>(q.a);
   auto* w = static_cast<const __nv_bfloat16*>(q.b);
-  const unsigned cols = unsigned(cdiv64(q.N, F));
-  if (ks > 1)
-    return launch_after(skinny_kernel<R, F, 8>, dim3(cols), 256u, 0, s, 1, x, q.ld_a, w, int(q.M), int(q.K), int(q.N), q.ep);
-  return launch_after(skinny_kernel<R, F, 1>, dim3((cols + 7) / 8), 256u, 0, s, 1, x, q.ld_a, w, int(q.M), int(q.K),
-                      int(q.N), q.ep);
-}
-
-// Up to eight rows. Four columns per warp where that leaves sixteen warps for every SM, one
-// otherwise, and K shared by a block's warps where even that leaves fewer than eight.
-cudaError_t run_skinny(const vsa_plan* p, const Problem& q, cudaStream_t s) {
-  const int64_t sms = p->num_sms;
-  const bool wide = q.N >= sms * 64;
-  const int ks = q.N < sms * 8 && q.K >= 512 ? 8 : 1;
-#define VSA_SKINNY(R) (wide ? run_skinny<R, 4>(q, 1, s) : run_skinny<R, 1>(q, ks, s))
-  if (q.M == 1) return VSA_SKINNY(1);
-  if (q.M == 2) return VSA_SKINNY(2);
-  if (q.M <= 4) return VSA_SKINNY(4);
-  return VSA_SKINNY(8);
-#undef VSA_SKINNY
+  const int t = q.M <= 8 ? 1 : 2;
+  const int64_t blocks = cdiv64(q.N, 8 * t);
+  const bool few = blocks * t <= int64_t(p->num_sms) * 2 && q.K >= 1024;
+#define VSA_FEW(T, W, U)                                                                                             \
+  launch_after(few_rows_kernel<T, W, U>, dim3(unsigned(blocks)), unsigned(W * 32), 0, s, 1, x, q.ld_a, w, int(q.M), \
+               int(q.K), int(q.N), q.ep)
+  if (t == 1) return few ? VSA_FEW(1, 16, 2) : VSA_FEW(1, 4, 2);
+  return few ? VSA_FEW(2, 16, 2) : VSA_FEW(2, 4, 3);
+#undef VSA_FEW
 }
 
 struct GradPlan {
@@ -1003,7 +1011,7 @@ cudaError_t launch_linear(const vsa_plan* p, const vsa_linear_args& a, cudaStrea
   q.ep.pre = static_cast<__nv_bfloat16*>(a.pre);
   q.ep.ld_pre = a.ld_pre;
   q.ep.act = a.act;
-  return q.M <= 8 ? run_skinny(p, q, s) : run_products(p, &q, 1, s);
+  return q.M <= 16 ? run_few_rows(p, q, s) : run_products(p, &q, 1, s);
 }
 
 cudaError_t launch_linear_bwd(const vsa_plan* p, const vsa_linear_grad_args& a, void* workspace, cudaStream_t s) {
