@@ -401,7 +401,8 @@ VSA_API vsa_status vsa_layer_forward(vsa_plan* plan, const void* q, const void* 
 /* Element strides of a [B, N, heads, head_dim] view: heads and channels are
  * contiguous, tokens `token` and batches `batch` elements apart. token >=
  * heads * head_dim, both multiples of 8, batch >= 0. So q, k and v may be slices of one
- * projection's [B, N, 3, heads, head_dim] output. */
+ * projection's [B, N, 3, heads, head_dim] output. An input's batches may share
+ * rows (batch 0); an output whose rows would overlap is refused. */
 typedef struct {
   int64_t batch, token;
 } vsa_strides;
@@ -478,7 +479,7 @@ VSA_API vsa_status vsa_tile_norm_rope_bwd(vsa_plan* plan, const vsa_norm_rope* n
  * leaves them). dqp, dkp, dvp (packed bf16) are written in full: zero in
  * unused slots and in tiles past a head's own count. P and dS are rounded to
  * bf16 for their products, sums are fp32 in a fixed order: no atomics, the
- * same result on every call. A list that is out of range or not ascending
+ * same result on every call; outputs overlap nothing. A list that is out of range or not ascending
  * latches VSA_ERR_BAD_INDEX and its query tile takes no part. workspace:
  * vsa_attn_bwd_workspace bytes, 256-byte aligned. */
 VSA_API vsa_status vsa_attn_bwd_workspace(const vsa_plan* plan, int64_t* bytes);
@@ -502,8 +503,8 @@ typedef enum {
 /* y = residual + gate * act(x w^T + bias). x [rows, n_in], w [n_out, n_in]
  * (contiguous), y, residual and pre [rows, n_out] bf16, bias [n_out] fp32, gate
  * [rows / rows_per_gate, n_out] fp32: row r uses gate row r / rows_per_gate (a
- * sample's rows share one). n_in and n_out are multiples of 8, rows < 2^31, any
- * rows >= 0; leading dimensions (row strides in elements) are multiples of 8.
+ * sample's rows share one). n_in and n_out are multiples of 8 up to 2^20, any rows
+ * from 0 to 2^31 - 257; leading dimensions (row strides in elements) are multiples of 8.
  * NULL bias, gate, residual: left out. pre, if given, gets x w^T + bias for the
  * gradient. y may be residual (same pointer and stride); otherwise outputs
  * overlap nothing. fp32 accumulation and epilogue, one rounding. */
@@ -531,7 +532,8 @@ VSA_API vsa_status vsa_linear(vsa_plan* plan, const vsa_linear_args* args, void*
  * dy * act'(pre), dx = dz w (bf16), dw = dz^T x (bf16), dbias = sum of dz,
  * dgate = per sample the sum of dy act(pre) (fp32). Any of the four may be NULL.
  * pre is needed with an activation or for dgate. dz is rounded to bf16 for the
- * two products; dbias and dgate are summed unrounded, in a fixed order. */
+ * two products; dbias and dgate are summed unrounded, in a fixed order. Outputs
+ * overlap nothing. */
 typedef struct {
   int64_t rows;
   int32_t n_in, n_out;
@@ -557,8 +559,8 @@ VSA_API vsa_status vsa_linear_bwd_workspace(const vsa_plan* plan, int64_t rows, 
                                             int64_t rows_per_gate, int64_t* bytes);
 VSA_API vsa_status vsa_linear_bwd(vsa_plan* plan, const vsa_linear_grad_args* args, void* workspace, void* stream);
 
-/* Bound of every device-side wait of the plan's tcgen05 kernels (attention,
- * teacher map), in nanoseconds: 1,000 .. 60,000,000,000; 0 restores the
+/* Bound of every device-side wait of the plan's tcgen05 kernels (attention and
+ * its gradient, linear, teacher map), in nanoseconds: 1,000 .. 60,000,000,000; 0 restores the
  * default of two seconds. A kernel whose wait runs past it stops: it latches
  * VSA_ERR_DEVICE_TIMEOUT (returned by vsa_plan_check), lets its own copies and
  * tensor-core work finish, frees its tensor memory and returns, leaving the

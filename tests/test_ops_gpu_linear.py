@@ -258,3 +258,28 @@ def test_refusals(plan):
     with pytest.raises(ValueError):                                                # a workspace that is too small
         plan.linear_bwd(t["dy"], t["x"], t["w"], dbias=t["bias"], workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))
     plan.check()
+
+
+def test_widths_have_a_limit(plan):
+    import tile_sparse_video_pack_b200 as T
+    assert plan.linear_bwd_workspace_bytes(8, 64, 1 << 20) > 0
+    for n_in, n_out in ((64, (1 << 20) + 8), ((1 << 20) + 8, 64)):
+        with pytest.raises(T.VsaError):
+            plan.linear_bwd_workspace_bytes(8, n_in, n_out)
+
+
+def test_widest(plan):
+    """2^20 columns out with one row, and 2^20 in: offsets of the weights past 32 bits."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(3)
+    K, N = 2056, 1 << 20                         # 2.16e9 weights
+    w = torch.randn(N, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    for rows in (3, 20):                         # both kernels that read W by rows and by tiles
+        x = torch.randn(rows, K, generator=g, device="cuda").bfloat16()
+        y = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+        plan.linear(x, w, y)
+        plan.check()
+        for at in (0, N // 2 - 8, N - 16):
+            want = x.double() @ w[at:at + 16].double().T
+            terms = x.double().abs() @ w[at:at + 16].double().abs().T
+            assert bool(((y[:, at:at + 16].double() - want).abs() <= K * 2.0 ** -23 * terms + 2.0 ** -8 * want.abs()).all())

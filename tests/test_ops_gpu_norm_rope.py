@@ -26,6 +26,12 @@ def one_token_config():
                        tile_shapes=((4, 4, 4),), score_mode="meanpool_gate", proj_dim=128, sparsity=(0.0,), seed=9)
 
 
+def three_heads_config():
+    """No multiple of the four rows of 64 channels that a warp takes, 105 tokens."""
+    return LayerConfig(name="three", batch=1, heads=3, head_dim=64, T=3, H=5, W=7, segments=(),
+                       tile_shapes=((4, 4, 4),) * 3, score_mode="meanpool_gate", proj_dim=64, sparsity=(0.0,), seed=9)
+
+
 CONFIGS = {"ragged128": lambda: ragged_gpu_config(128, batch=2), "ragged64_trip": lambda: ragged_gpu_config(64, "tripool"),
            "noprefix": no_prefix_config, "tiny": lambda: get_config("tiny"), "one": one_token_config}
 
@@ -247,4 +253,72 @@ def test_refusals():
     wide = torch.empty(c.shape[0], c.shape[1], c.shape[2] * c.shape[3] + 4, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(T.VsaError):
         p.qk_norm_rope(wide[..., :-4].unflatten(2, c.shape[2:]), c.k, n, qo, ko)
+    p.check()
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("packed", [False, True])
+def test_backward_without_epsilon(packed, per_head, monkeypatch):
+    """Lanes without a row (an odd head count, the last tokens) hold zeros, whose norm has no value with eps 0: they
+    add nothing to dw."""
+    import sys
+    import torch
+    monkeypatch.setattr(sys.modules[__name__], "EPS", 0.0)
+    c = Case(three_heads_config(), "halves", per_head)
+    p, bf = c.plan, torch.bfloat16
+    dy = [torch.randn(*c.shape, generator=c.gen).to(bf).cuda() for _ in range(3)]
+    dw = [torch.empty_like(c.norm.w_q) for _ in range(2)]
+    ws = torch.empty(p.norm_bwd_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    dq, dk, dv = (torch.empty(c.shape, dtype=bf, device="cuda") for _ in range(3))
+    if packed:
+        pk = [torch.empty(p.info.packed_elems, dtype=bf, device="cuda") for _ in range(3)]
+        p.tile_pack(*dy, *pk)
+        p.tile_norm_rope_bwd(*pk, c.q, c.k, c.norm, dq, dk, dv, *dw, ws)
+    else:
+        p.qk_norm_rope_bwd(dy[0], dy[1], c.q, c.k, c.norm, dq, dk, *dw, ws)
+    p.check()
+    for i, dx in enumerate((dq, dk)):
+        check_backward(c, i, bf16_to_f64(dy[i]), dx, dw[i])
+
+
+def test_packed_backward_in_place():
+    import torch
+    c = Case(ragged_gpu_config(128, batch=2), "interleaved", False, strided=False)
+    p, bf = c.plan, torch.bfloat16
+    pk = [torch.empty(p.info.packed_elems, dtype=bf, device="cuda") for _ in range(3)]
+    p.tile_pack(*(torch.randn(*c.shape, generator=c.gen).to(bf).cuda() for _ in range(3)), *pk)
+    ws = torch.empty(p.norm_bwd_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    out = [torch.empty(c.shape, dtype=bf, device="cuda") for _ in range(3)]
+    p.tile_norm_rope_bwd(*pk, c.q, c.k, c.norm, *out, None, None, ws)
+    p.tile_norm_rope_bwd(*pk, c.q, c.k, c.norm, c.q, c.k, c.v, None, None, ws)
+    p.check()
+    assert all(torch.equal(a, b) for a, b in zip(out, (c.q, c.k, c.v)))
+
+
+def test_batches_inside_tokens_and_shared_inputs():
+    """[N, B, heads, d] outputs are taken, inputs may be one batch for all, outputs that overlap are refused."""
+    import torch
+    import tile_sparse_video_pack_b200 as T
+    c = Case(ragged_gpu_config(128, batch=2), "halves", False, strided=False)
+    p, (B, N, Hh, d) = c.plan, c.shape
+    new = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+    qo, ko = new(*c.shape), new(*c.shape)
+    p.qk_norm_rope(c.q, c.k, c.norm, qo, ko)
+    qt, kt = (new(N, B, Hh, d).transpose(0, 1) for _ in range(2))
+    p.qk_norm_rope(c.q, c.k, c.norm, qt, kt)
+    assert torch.equal(qt, qo) and torch.equal(kt, ko)
+    one = c.q[:1].expand(B, N, Hh, d)
+    p.qk_norm_rope(one, one, c.norm, qt, kt)
+    assert torch.equal(qt[0], qo[0]) and torch.equal(qt[1], qo[0])
+    ws = torch.empty(p.norm_bwd_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    shared = new(1, N, Hh, d).expand(B, N, Hh, d)
+    with pytest.raises(T.VsaError):
+        p.qk_norm_rope(c.q, c.k, c.norm, shared, ko)
+    with pytest.raises(T.VsaError):
+        p.qk_norm_rope(c.q, c.k, c.norm, qo, new(N * B + 1, Hh, d)[:N + 1].as_strided(c.shape, (Hh * d, Hh * d, d, 1)))
+    with pytest.raises(T.VsaError):
+        p.qk_norm_rope_bwd(qo, ko, c.q, c.k, c.norm, qt, shared, None, None, ws)
+    pk = [torch.empty(p.info.packed_elems, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    with pytest.raises(T.VsaError):
+        p.tile_norm_rope_bwd(*pk, c.q, c.k, c.norm, qt, kt, shared, None, None, ws)
     p.check()

@@ -646,8 +646,9 @@ __global__ void __launch_bounds__(256, 2) norm_rope_bwd_kernel(NormRopeArgs n, G
           turn = Turn{{cs.x, cs.y, cs.z, cs.w}, {sn.x, sn.y, sn.z, sn.w}};
         }
       }
-      const uint4 yq = norm_rope_grad_row<CPR, HALVES>(row(0), row(2), wq, turn, n.eps, tok_acc[0][0], tok_acc[0][1]);
-      const uint4 yk = norm_rope_grad_row<CPR, HALVES>(row(1), row(3), wk, turn, n.eps, tok_acc[1][0], tok_acc[1][1]);
+      const float eps = on(now) ? n.eps : 1.f;   // a lane without a row has zeros: with eps 0 they would be 0 * inf
+      const uint4 yq = norm_rope_grad_row<CPR, HALVES>(row(0), row(2), wq, turn, eps, tok_acc[0][0], tok_acc[0][1]);
+      const uint4 yk = norm_rope_grad_row<CPR, HALVES>(row(1), row(3), wk, turn, eps, tok_acc[1][0], tok_acc[1][1]);
       if (on(now)) {
         const int off = head_of(now) * D;
         store_row<HALVES>(dq + now.b * n.st[2].batch + now.tok * n.st[2].token + off, D, c, yq);

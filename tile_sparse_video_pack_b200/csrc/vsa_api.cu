@@ -56,10 +56,17 @@ bool on_plan_device(const vsa_plan* p) {
 
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
+// Whether a view's rows overlap nowhere: batches outside tokens, or tokens outside batches.
+bool rows_apart(const vsa_plan* p, const vsa_strides& v) {
+  const __int128 row = int64_t(p->geo.Hh) * p->geo.d, b = p->geo.B, n = p->geo.n_tokens;
+  return b == 1 || v.batch >= (n - 1) * v.token + row || (v.batch >= row && (n == 1 || v.token >= (b - 1) * v.batch + row));
+}
+
 // The arguments of one norm + rotation call: parameters and the views' strides
-// (null: contiguous), each view `n_views` long and mapped to NormRopeArgs::st by `at`.
-bool resolve_norm(const vsa_plan* p, const vsa_norm_rope* n, const vsa_strides* strides, int n_views, const int* at,
-                  vsa::NormRopeArgs* out) {
+// (null: contiguous), `n_views` views, the last `n_out` of them written, each mapped to
+// NormRopeArgs::st by `at`.
+bool resolve_norm(const vsa_plan* p, const vsa_norm_rope* n, const vsa_strides* strides, int n_views, int n_out,
+                  const int* at, vsa::NormRopeArgs* out) {
   if (!n) return false;
   if (!n->cos_table != !n->sin_table) return false;
   if (!aligned16(n->w_q) || !aligned16(n->w_k) || !aligned16(n->cos_table) || !aligned16(n->sin_table)) return false;
@@ -79,6 +86,7 @@ bool resolve_norm(const vsa_plan* p, const vsa_norm_rope* n, const vsa_strides* 
     vsa_strides v = {row * p->geo.n_tokens, row};
     if (strides) v = strides[i];
     if (v.token < row || v.token % 8 || v.batch < 0 || v.batch % 8) return false;
+    if (i >= n_views - n_out && !rows_apart(p, v)) return false;
     out->st[at[i]] = v;
   }
   return true;
@@ -87,7 +95,7 @@ bool resolve_norm(const vsa_plan* p, const vsa_norm_rope* n, const vsa_strides* 
 // rows, widths and leading dimensions of a linear call
 bool linear_sizes(int64_t rows, int32_t n_in, int32_t n_out) {
   return rows >= 0 && rows < (int64_t(1) << 31) - 256 && n_in >= 8 && n_out >= 8 && n_in % 8 == 0 && n_out % 8 == 0 &&
-         n_in <= (1 << 24) && n_out <= (1 << 24);
+         n_in <= (1 << 20) && n_out <= (1 << 20);   // column blocks are a grid's y
 }
 bool linear_view(const void* p, int64_t ld, int32_t cols) { return p && aligned16(p) && ld >= cols && ld % 8 == 0; }
 
@@ -654,7 +662,7 @@ vsa_status vsa_qk_norm_rope(vsa_plan* p, const vsa_norm_rope* norm, const void* 
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return fail(p, VSA_ERR_INVALID_ARG);
   vsa::NormRopeArgs n = {};
   const int at[4] = {0, 1, 2, 3};
-  if (!resolve_norm(p, norm, strides, 4, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!resolve_norm(p, norm, strides, 4, 2, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
   if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
   if (vsa::launch_norm_rope(p, n, q, k, q_out, k_out, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return fail(p, VSA_ERR_CUDA);
@@ -671,7 +679,7 @@ vsa_status vsa_tile_norm_rope_pack_pool(vsa_plan* p, const vsa_norm_rope* norm, 
     return fail(p, VSA_ERR_INVALID_ARG);
   vsa::NormRopeArgs n = {};
   const int at[3] = {0, 1, 2};
-  if (!resolve_norm(p, norm, strides, 3, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!resolve_norm(p, norm, strides, 3, 0, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
   if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
   p->stats.calls_pack++;
   float *pq, *pk;
@@ -703,7 +711,7 @@ vsa_status vsa_qk_norm_rope_bwd(vsa_plan* p, const vsa_norm_rope* norm, const vo
     return fail(p, VSA_ERR_INVALID_ARG);
   vsa::NormRopeArgs n = {};
   const int at[6] = {5, 6, 0, 1, 2, 3};
-  if (!resolve_norm(p, norm, strides, 6, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!resolve_norm(p, norm, strides, 6, 2, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
   if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
   if (vsa::launch_norm_rope_bwd(p, n, false, dq_out, dk_out, nullptr, q, k, dq, dk, nullptr, dw_q, dw_k, ws,
                                 static_cast<cudaStream_t>(stream)) != cudaSuccess)
@@ -721,7 +729,7 @@ vsa_status vsa_tile_norm_rope_bwd(vsa_plan* p, const vsa_norm_rope* norm, const 
     return fail(p, VSA_ERR_INVALID_ARG);
   vsa::NormRopeArgs n = {};
   const int at[5] = {0, 1, 2, 3, 4};
-  if (!resolve_norm(p, norm, strides, 5, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
+  if (!resolve_norm(p, norm, strides, 5, 3, at, &n)) return fail(p, VSA_ERR_INVALID_ARG);
   if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
   if (vsa::launch_norm_rope_bwd(p, n, true, dqp, dkp, dvp, q, k, dq, dk, dv, dw_q, dw_k, ws,
                                 static_cast<cudaStream_t>(stream)) != cudaSuccess)
@@ -746,7 +754,6 @@ static vsa_status attn_bwd(vsa_plan* p, const void* qp, const void* kp, const vo
   if (!aligned256(ws)) return fail(p, VSA_ERR_INVALID_ARG);
   int32_t k[VSA_MAX_HEADS];
   if (!resolve_k(p, k_per_head, k)) return fail(p, VSA_ERR_INVALID_ARG);
-  if (int64_t(p->geo.B) * p->geo.Hh > 65535) return fail(p, VSA_ERR_UNSUPPORTED);   // grid of the list kernel
   if (!on_plan_device(p)) return fail(p, VSA_ERR_INVALID_ARG);
   if (vsa::launch_attn_bwd(p, qp, kp, vp, op, lse, dop, idx, idx_ref, k, dqp, dkp, dvp, ws,
                            static_cast<cudaStream_t>(stream)) != cudaSuccess)
