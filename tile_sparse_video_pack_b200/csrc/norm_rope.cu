@@ -721,8 +721,8 @@ int bwd_blocks(const vsa_plan* p, bool per_head) {
   const int64_t tokens = int64_t(g.B) * g.n_tokens;
   const int tpb = per_head ? 8 * (32 / (g.d / 8)) : 8;
   const int64_t want = (tokens + tpb - 1) / tpb;
-  const int64_t cap = per_head ? (int64_t(p->num_sms) * 2 + g.Hh - 1) / g.Hh : int64_t(p->num_sms) * 2;
-  return int(want < cap ? want : cap);
+  const int64_t cap = int64_t(p->num_sms) * 2 / (per_head ? g.Hh : 1);
+  return int(want < cap ? want : cap < 1 ? 1 : cap);
 }
 
 }  // namespace
