@@ -42,20 +42,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-// One lane's eight channels of a row as loaded: four words of two channels.
+// One lane's eight channels of a row in shared memory: four words of two channels.
 // Interleaved: word j is pair j. Halves: words 0, 1 hold the first members of
 // pairs 0 .. 3, words 2, 3 the second.
 template <bool HALVES>
-__device__ __forceinline__ uint4 load_row(const __nv_bfloat16* row, int d, int c) {
-  if (HALVES) {
-    const uint2 a = __ldcs(reinterpret_cast<const uint2*>(row + 4 * c));
-    const uint2 b = __ldcs(reinterpret_cast<const uint2*>(row + d / 2 + 4 * c));
-    return make_uint4(a.x, a.y, b.x, b.y);
-  }
-  return __ldcs(reinterpret_cast<const uint4*>(row) + c);
-}
-template <bool HALVES>
-__device__ __forceinline__ uint4 row_of(const __nv_bfloat16* row, int d, int c) {   // the same of a row in shared memory
+__device__ __forceinline__ uint4 row_of(const __nv_bfloat16* row, int d, int c) {
   if (HALVES) {
     const uint2 a = *reinterpret_cast<const uint2*>(row + 4 * c);
     const uint2 b = *reinterpret_cast<const uint2*>(row + d / 2 + 4 * c);
@@ -101,14 +92,23 @@ __device__ __forceinline__ int channel_of(int d, int c, int j, int m) {
 struct Weights {
   float a[4], b[4];
 };
-// The lane's weights of one head (ones for a null table).
+// The lane's weights of one head (ones for a null table; rows are 16-byte aligned).
 template <bool HALVES>
 __device__ __forceinline__ Weights load_weights(const float* w, int d, int c) {
   Weights r;
+  if (!w) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    r.a[j] = w ? __ldg(w + channel_of<HALVES>(d, c, j, 0)) : 1.f;
-    r.b[j] = w ? __ldg(w + channel_of<HALVES>(d, c, j, 1)) : 1.f;
+    for (int j = 0; j < 4; ++j) r.a[j] = r.b[j] = 1.f;
+    return r;
+  }
+  const float4 x = __ldg(reinterpret_cast<const float4*>(w) + (HALVES ? c : 2 * c));
+  const float4 y = __ldg(reinterpret_cast<const float4*>(w) + (HALVES ? d / 8 + c : 2 * c + 1));
+  if (HALVES) {
+    r.a[0] = x.x; r.a[1] = x.y; r.a[2] = x.z; r.a[3] = x.w;
+    r.b[0] = y.x; r.b[1] = y.y; r.b[2] = y.z; r.b[3] = y.w;
+  } else {
+    r.a[0] = x.x; r.b[0] = x.y; r.a[1] = x.z; r.b[1] = x.w;
+    r.a[2] = y.x; r.b[2] = y.y; r.a[3] = y.z; r.b[3] = y.w;
   }
   return r;
 }
@@ -243,43 +243,89 @@ __device__ __forceinline__ void cp_wait() {
 
 // Token-major to token-major. One warp per token; its 32 / CPR lane groups
 // walk the heads, so the token's table row is loaded once for all heads.
-// Results may overwrite their inputs: a row is read before it is written, by
-// the lanes that write it.
+// Bound by HBM: a warp's next steps (32 / CPR rows of q and of k each) are
+// requested into shared memory ahead of the one at work, across tokens too, and
+// the next token's angles into registers. Sixteen rounds of blocks at most: the
+// SMs do not get the same share of HBM, and with one round, every warp's tokens
+// fixed, the last is 20 % behind (24 heads of 128, 112,512 tokens: 530 us; 2 rounds
+// 485, 4 455, 16 434 = 6.5 TB/s; direct loads, two in flight, 500 to 590). Results may
+// overwrite their inputs: a row is requested once, by the warp that writes it, and
+// written after it is read.
+constexpr int kFwdStages = 5, kFwdBlocks = 3;    // blocks per SM
 template <int CPR, bool HALVES>
-__global__ void __launch_bounds__(256) norm_rope_kernel(NormRopeArgs n, int B, int n_tok, int heads,
-                                                        const __nv_bfloat16* q, const __nv_bfloat16* k,
-                                                        __nv_bfloat16* qo, __nv_bfloat16* ko) {
+__global__ void __launch_bounds__(256, kFwdBlocks) norm_rope_kernel(NormRopeArgs n, int B, int n_tok, int heads,
+                                                                    const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                                                    __nv_bfloat16* qo, __nv_bfloat16* ko) {
   constexpr int D = CPR * 8, G = 32 / CPR;
+  __shared__ __align__(16) uint8_t sm[8][kFwdStages][2][512];
   tc::allow_successor();
   tc::wait_predecessor();
-  const int lane = threadIdx.x & 31, c = lane % CPR, grp = lane / CPR;
-  Weights wq = load_weights<HALVES>(n.w_q, D, c), wk = load_weights<HALVES>(n.w_k, D, c);
-  const int64_t total = int64_t(B) * n_tok;
-  for (int64_t tk = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); tk < total; tk += int64_t(gridDim.x) * 8) {
-    const int b = int(tk / n_tok), tok = int(tk - int64_t(b) * n_tok);
-    const Turn t = load_turn(n, tok, D, c);
-    const __nv_bfloat16* qr = q + b * n.st[0].batch + tok * n.st[0].token;
-    const __nv_bfloat16* kr = k + b * n.st[1].batch + tok * n.st[1].token;
-    __nv_bfloat16* qw = qo + b * n.st[2].batch + tok * n.st[2].token;
-    __nv_bfloat16* kw = ko + b * n.st[3].batch + tok * n.st[3].token;
-    for (int h0 = 0; h0 < heads; h0 += G) {      // the same trip count in every lane: the sums are warp-wide
-      const int h = h0 + grp;
+  const int lane = threadIdx.x & 31, c = lane % CPR, grp = lane / CPR, warp = threadIdx.x >> 5;
+  const int steps = (heads + G - 1) / G, dt = int(gridDim.x) * 8;
+  const int64_t first = int64_t(blockIdx.x) * 8 + warp, total = int64_t(B) * n_tok;
+  struct At {                                    // a place in the walk: alike in all lanes
+    int b, tok, step;
+    int64_t left;                                // tokens of the walk from here
+  };
+  auto next_token = [&](At& a) {                 // without a division
+    a.left -= dt;
+    a.tok += dt;
+    while (a.tok >= n_tok) {
+      a.tok -= n_tok;
+      ++a.b;
+    }
+  };
+  At now;
+  now.b = int(first / n_tok);
+  now.tok = int(first - int64_t(now.b) * n_tok);
+  now.step = 0;
+  now.left = total - first;
+  At ahead = now;                                // the step to request next
+  uint32_t issued = 0, done = 0;                 // steps, which take the stages in turn
+  auto request_next = [&] {                      // one group of copies for every step, past the end an empty one
+    if (ahead.left > 0) {
+      const int h = ahead.step * G + grp;
       const bool on = h < heads;
-      uint4 vq = make_uint4(0, 0, 0, 0), vk = vq;
-      if (on) {
-        vq = load_row<HALVES>(qr + h * D, D, c);
-        vk = load_row<HALVES>(kr + h * D, D, c);
-        if (n.per_head) {
-          wq = load_weights<HALVES>(n.w_q ? n.w_q + h * D : nullptr, D, c);
-          wk = load_weights<HALVES>(n.w_k ? n.w_k + h * D : nullptr, D, c);
-        }
+      const int64_t off = (on ? h : 0) * D + 8 * c;
+      const uint32_t dst = tc::smem_u32(sm[warp][issued % kFwdStages][0]) + lane * 16;
+      cp_async16(dst, q + ahead.b * n.st[0].batch + ahead.tok * n.st[0].token + off, on);
+      cp_async16(dst + 512, k + ahead.b * n.st[1].batch + ahead.tok * n.st[1].token + off, on);
+      if (++ahead.step == steps) {
+        ahead.step = 0;
+        next_token(ahead);
       }
-      vq = norm_rope_row<CPR, HALVES>(vq, wq, t, n.eps);
-      vk = norm_rope_row<CPR, HALVES>(vk, wk, t, n.eps);
-      if (on) {
-        store_row<HALVES>(qw + h * D, D, c, vq);
-        store_row<HALVES>(kw + h * D, D, c, vk);
+    }
+    cp_commit();
+    ++issued;
+  };
+#pragma unroll
+  for (int i = 0; i < kFwdStages - 1; ++i) request_next();
+  Weights wq = load_weights<HALVES>(n.w_q, D, c), wk = load_weights<HALVES>(n.w_k, D, c);
+  Turn next = load_turn(n, now.left > 0 ? now.tok : 0, D, c);
+  while (now.left > 0) {
+    const Turn t = next;
+    __nv_bfloat16* qw = qo + now.b * n.st[2].batch + now.tok * n.st[2].token;
+    __nv_bfloat16* kw = ko + now.b * n.st[3].batch + now.tok * n.st[3].token;
+    next_token(now);
+    if (now.left > 0) next = load_turn(n, now.tok, D, c);
+    for (int step = 0; step < steps; ++step, ++done) {
+      request_next();
+      cp_wait<kFwdStages - 1>();
+      __syncwarp();                              // a row's chunks were requested by the lanes that share it
+      const int h = step * G + grp;
+      const uint8_t* in = sm[warp][done % kFwdStages][0] + grp * CPR * 16;
+      if (n.per_head && h < heads) {
+        wq = load_weights<HALVES>(n.w_q ? n.w_q + h * D : nullptr, D, c);
+        wk = load_weights<HALVES>(n.w_k ? n.w_k + h * D : nullptr, D, c);
       }
+      const uint4 yq = norm_rope_row<CPR, HALVES>(row_of<HALVES>(reinterpret_cast<const __nv_bfloat16*>(in), D, c), wq, t, n.eps);
+      const uint4 yk =
+          norm_rope_row<CPR, HALVES>(row_of<HALVES>(reinterpret_cast<const __nv_bfloat16*>(in + 512), D, c), wk, t, n.eps);
+      if (h < heads) {
+        store_row<HALVES>(qw + h * D, D, c, yq);
+        store_row<HALVES>(kw + h * D, D, c, yk);
+      }
+      __syncwarp();                              // the stage may be filled again
     }
   }
 }
@@ -290,11 +336,12 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(NormRopeArgs n, int B, i
 // angles in registers for all heads of the run that share a tile shape. The rows
 // of a head (48 KB at d = 128) are requested at once into one of two buffers, the
 // next head's while this one is worked on, so that the bytes in flight do not
-// depend on registers. Unused slots arrive as zeros. Full clip: 0.78 ms with a
-// table read per head; one pass of loads per thread into registers took 1.20 ms. Lanes and rows as in the pack kernel;
-// the descriptors are pooled from the rounded rows in the same order as there, so
-// packed tiles and descriptors equal, bit for bit, those of the token-major pass
-// followed by the pack. Tiles past a head's own are zero, their descriptors too.
+// depend on registers. Unused slots arrive as zeros. Full clip (24 heads of 128, 112,512
+// tokens): 0.66 ms, 6.4 TB/s; 0.78 with a table read per head, 1.20 with one pass of
+// loads per thread into registers. Lanes and rows as in the pack kernel; the
+// descriptors are pooled from the rounded rows in the same order as there, so packed
+// tiles and descriptors equal, bit for bit, those of the token-major pass followed by
+// the pack. Tiles past a head's own are zero, their descriptors too.
 template <int CPR, bool TRIP>
 struct PackSmem {
   static constexpr int D = CPR * 8, NS = TRIP ? 3 : 1;
@@ -520,8 +567,9 @@ __device__ __forceinline__ uint4 norm_rope_grad_row(uint4 vy, uint4 vx, const We
 // partial sums of dw go to `part` [blockIdx.y][blockIdx.x][q, k][d], summed in
 // block order by the kernel below: no atomics, the same result every time.
 // Bound by HBM: a warp's next steps (32 / CPR rows of every input each) are
-// requested into shared memory ahead of the one at work, across tokens too; with
-// one step's loads in registers the clip took 1.08 ms. With PER_HEAD a step is a
+// requested into shared memory ahead of the one at work, across tokens too; the
+// clip takes 0.86 ms, 6.5 TB/s (weights per head 0.95), with one step's loads in
+// registers 1.08. With PER_HEAD a step is a
 // token, so its table rows are requested along with it.
 template <int CPR, bool PACKED, bool PER_HEAD>
 struct GradSmem {
@@ -715,13 +763,20 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
 
 // Blocks along x of the gradient kernel: one token for each of eight warps (or their
 // lane groups) at least, what is resident at once, two blocks per SM, at most
-// (weights per head: shared among the heads).
-int bwd_blocks(const vsa_plan* p, bool per_head) {
+// (weights per head: shared among the heads). From packed tiles and with shared
+// weights up to eight rounds of that, one for every 64 steps of a warp, so that SMs
+// with a smaller share of HBM get fewer blocks: 937 us with one round, 869 with eight
+// at 24 heads of 128 and 112,512 tokens (570 steps); 59 and 75 at 45 steps. From
+// token-major rows 677 and 682, with weights per head 952 and 1,053.
+int bwd_blocks(const vsa_plan* p, bool per_head, bool packed) {
   const Geometry& g = p->geo;
   const int64_t tokens = int64_t(g.B) * g.n_tokens;
   const int tpb = per_head ? 8 * (32 / (g.d / 8)) : 8;
   const int64_t want = (tokens + tpb - 1) / tpb;
-  const int64_t cap = int64_t(p->num_sms) * 2 / (per_head ? g.Hh : 1);
+  const int64_t resident = int64_t(p->num_sms) * 2, per_token = (g.Hh + 32 / (g.d / 8) - 1) / (32 / (g.d / 8));
+  int64_t rounds = per_head || !packed ? 1 : tokens * per_token / (resident * 8 * 64);
+  rounds = rounds < 1 ? 1 : rounds > 8 ? 8 : rounds;
+  const int64_t cap = resident * rounds / (per_head ? g.Hh : 1);
   return int(want < cap ? want : cap < 1 ? 1 : cap);
 }
 
@@ -751,7 +806,7 @@ cudaError_t prepare_norm_rope() {
 cudaError_t launch_norm_rope(const vsa_plan* p, const NormRopeArgs& n, const void* q, const void* k, void* qo, void* ko,
                              cudaStream_t s) {
   const Geometry& g = p->geo;
-  const int64_t want = (int64_t(g.B) * g.n_tokens + 7) / 8, cap = int64_t(p->num_sms) * 8;
+  const int64_t want = (int64_t(g.B) * g.n_tokens + 7) / 8, cap = int64_t(p->num_sms) * kFwdBlocks * 16;
   const unsigned grid = unsigned(want < cap ? want : cap);
   auto* q2 = static_cast<const __nv_bfloat16*>(q);
   auto* k2 = static_cast<const __nv_bfloat16*>(k);
@@ -804,7 +859,7 @@ cudaError_t launch_norm_rope_pack(const vsa_plan* p, const NormRopeArgs& n, cons
 }
 
 int64_t norm_bwd_workspace_bytes(const vsa_plan* p) {
-  const int64_t shared = bwd_blocks(p, false), per_head = int64_t(bwd_blocks(p, true)) * p->geo.Hh;
+  const int64_t shared = bwd_blocks(p, false, true), per_head = int64_t(bwd_blocks(p, true, true)) * p->geo.Hh;
   return (shared > per_head ? shared : per_head) * 2 * p->geo.d * int64_t(sizeof(float));
 }
 
@@ -812,7 +867,7 @@ cudaError_t launch_norm_rope_bwd(const vsa_plan* p, const NormRopeArgs& n, bool 
                                  const void* dyv, const void* q, const void* k, void* dq, void* dk, void* dv, float* dw_q,
                                  float* dw_k, void* workspace, cudaStream_t s) {
   const Geometry& g = p->geo;
-  const int nb = bwd_blocks(p, n.per_head);
+  const int nb = bwd_blocks(p, n.per_head, packed);
   const dim3 grid(nb, n.per_head ? g.Hh : 1);
   float* part = static_cast<float*>(workspace);
   cudaError_t e = cudaSuccess;
