@@ -283,3 +283,20 @@ def test_widest(plan):
             want = x.double() @ w[at:at + 16].double().T
             terms = x.double().abs() @ w[at:at + 16].double().abs().T
             assert bool(((y[:, at:at + 16].double() - want).abs() <= K * 2.0 ** -23 * terms + 2.0 ** -8 * want.abs()).all())
+
+
+def test_no_rows_with_a_gate(plan):
+    import torch
+    bf, K, N = torch.bfloat16, 64, 136
+    new = lambda *s, dtype=bf: torch.full(s, 7.0, dtype=dtype, device="cuda")
+    x, dx, y = new(2, 0, K), new(2, 0, K), new(2, 0, N)
+    w, dw, gate, dgate = new(N, K), new(N, K), new(2, N, dtype=torch.float32), new(2, N, dtype=torch.float32)
+    dbias = new(N, dtype=torch.float32)
+    plan.linear(x, w, y, gate=gate, residual=y)
+    for stream in (None, torch.cuda.Stream()):
+        for t in (dw, dbias, dgate):
+            t.fill_(7.0)
+        torch.cuda.synchronize()
+        plan.linear_bwd(y, x, w, dx=dx, dw=dw, pre=y, gate=gate, dbias=dbias, dgate=dgate, stream=stream)
+        plan.check()
+        assert not dw.any() and not dbias.any() and not dgate.any()

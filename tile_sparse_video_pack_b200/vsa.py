@@ -769,7 +769,7 @@ class Plan:
         if gate.dim() != 2 or gate.shape[1] != n_out or gate.shape[0] < 1 or rows % gate.shape[0]:
             raise ValueError(f"gate must be [samples, {n_out}] with samples dividing {rows} rows, "
                              f"got {tuple(gate.shape)}")
-        return _addr(gate, _F32, "gate", dev), rows // gate.shape[0]
+        return _addr(gate, _F32, "gate", dev), rows // gate.shape[0] or 1
 
     @staticmethod
     def _act(act):
@@ -845,6 +845,9 @@ class Plan:
                               _addr(dgate, f32, "dgate", dev))
         _check(self._lib.vsa_linear_bwd(self._h, a, _addr(workspace, _U8, "workspace", dev, need), s),
                "vsa_linear_bwd")
+        if rows == 0 and dgate is not None:      # samples without rows: the library sees none
+            with _torch.cuda.stream(stream):
+                dgate.zero_()
 
     def set_wait_limit(self, limit_ns: int = 0):
         """Bound of every device-side wait of the plan's tcgen05 kernels (0: the two-second default)."""
