@@ -271,3 +271,26 @@ def test_block_refusals():
         T.TileSparseBlock(c.layer, c.block.w_qkv, c.block.w_out[:, :-8], c.block.norm)
     with pytest.raises(ValueError):
         T.FeedForward(c.layer.plan, c.block.w_out, c.block.w_out)
+
+
+def test_output_over_the_input():
+    """Without save the residual's x may be written over; backward's x may not."""
+    import torch
+    import tile_sparse_video_pack_b200 as T
+    c = Block(get_config("tiny"))
+    x, channels = c.x, c.x.shape[2]
+    g = torch.Generator().manual_seed(6)
+    w_out = (torch.randn(channels, c.block.w_out.shape[1], generator=g) * 0.05).to(torch.bfloat16).cuda()
+    w_up = (torch.randn(264, channels, generator=g) * 0.05).to(torch.bfloat16).cuda()
+    block = T.TileSparseBlock(c.layer, c.block.w_qkv, w_out, c.block.norm)
+    for part in (block, T.FeedForward(c.layer.plan, w_up, w_up.t().contiguous())):
+        with pytest.raises(ValueError):
+            part(x, residual=x, out=x, save=True)
+        want = part(x, residual=x)
+        over = x.clone()
+        assert part(over, residual=over, out=over) is over
+        c.layer.plan.check()
+        assert torch.equal(over, want)
+        both = torch.empty(2, *x.shape, dtype=torch.bfloat16, device="cuda")   # neighbours in one buffer are taken
+        both[0].copy_(x)
+        assert torch.equal(part(both[0], residual=both[0], out=both[1], save=True), want)

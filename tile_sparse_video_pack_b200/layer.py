@@ -109,6 +109,16 @@ def _workspace(like, n):
     return torch.empty(n, dtype=torch.uint8, device=like.device)
 
 
+def _keeps(x, out, save):
+    """Refuses an output over the input that backward needs."""
+    if not save or out is None or x.numel() == 0 or out.numel() == 0:
+        return
+    lo = [t.data_ptr() for t in (x, out)]
+    hi = [a + (1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride()))) * t.element_size() for a, t in zip(lo, (x, out))]
+    if lo[0] < hi[1] and lo[1] < hi[0]:
+        raise ValueError("out overlaps x, which backward needs: save=True takes another output")
+
+
 class TileSparseBlock:
     """The attention half of a transformer block: y = residual + gate * (attention(norm, rotation(x w_qkv^T + b_qkv))
     w_out^T + b_out), with its gradient.
@@ -145,6 +155,7 @@ class TileSparseBlock:
         B, N, heads, d = p.shapes()["tokens"]
         if tuple(x.shape) != (B, N, self.w_qkv.shape[1]):
             raise ValueError(f"x must be {(B, N, self.w_qkv.shape[1])}, got {tuple(x.shape)}")
+        _keeps(x, out, save)
         if save and L.direct:
             raise ValueError("the direct path keeps no packed tiles: its gradient is not available")
         width = heads * d
@@ -235,6 +246,7 @@ class FeedForward:
             import torch
             with torch.cuda.stream(stream):
                 return self.forward(x, residual, gate, out, save)
+        _keeps(x, out, save)
         p, lead = self.plan, x.shape[:-1]
         h = _new(x, *lead, self.w_up.shape[0])
         hidden = _new(x, *lead, self.w_up.shape[0]) if save else None
