@@ -129,7 +129,8 @@ class TileSparseBlock:
     norm runs token-major. ``forward(..., save=True)`` keeps what :meth:`backward` needs (the gradient follows
     the selected tiles as given; not with ``layer.direct``). The packed tiles stay in the layer's buffers, which
     its next forward overwrites: backward refuses then, so blocks that are trained need a layer each. (A replayed
-    graph's forward is not noticed: capture a forward and its backward together.) With ``stream`` the whole call, its allocations too, is that stream's.
+    graph's forward is not noticed: capture a forward and its backward together.) With ``stream`` the whole call, its
+    allocations too, is that stream's.
     """
 
     def __init__(self, layer: TileSparseAttention, w_qkv, w_out, norm: NormRope, b_qkv=None, b_out=None):
