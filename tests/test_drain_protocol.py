@@ -1,0 +1,39 @@
+"""How the tcgen05 kernels end, on host-side models of their barriers (no GPU): usual ends, waits that run out early and
+waits that run out after the producer has left, with its last copies still on their way."""
+import random
+
+import pytest
+
+import drain_protocol_model as M
+
+WAYS = {"usual": dict(), "early": dict(timeout_p=0.02), "late": dict(timeout_p=0.3, late=True)}
+
+
+def outcomes(run, trials, seed):
+    rng = random.Random(seed)
+    seen = {"ok": 0, "aborted": 0, "hazard": 0}
+    for _ in range(trials):
+        try:
+            seen[run(rng)] += 1
+        except M.Hazard:
+            seen["hazard"] += 1
+    return seen
+
+
+@pytest.mark.parametrize("way", sorted(WAYS))
+def test_products_end_with_nothing_in_flight(way):
+    def run(rng):
+        kblocks, stages = M.random_gemm(rng)
+        return M.gemm(kblocks, stages, rng, **WAYS[way])
+    seen = outcomes(run, 300, 1)
+    assert seen["hazard"] == 0 and (seen["ok"] == 300) == (way == "usual"), seen
+
+
+def test_products_that_are_held_run_into_the_limit():
+    assert outcomes(lambda rng: M.gemm(*M.random_gemm(rng), rng, hold=True), 100, 2) == {"ok": 0, "aborted": 100, "hazard": 0}
+
+
+def test_a_producer_that_asks_the_flag_leaves_copies_behind():
+    """What the model is for: the flag is not up yet when the producer leaves, and the copies outlive the CTA."""
+    run = lambda drain: outcomes(lambda rng: M.gemm(*M.random_gemm(rng), rng, drain=drain, **WAYS["late"]), 200, 3)
+    assert run("flag")["hazard"] > 0 and run("never")["hazard"] > 0

@@ -450,7 +450,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
       if (u + du < prm.units) cluster_sync();
     }
   }
-  if (warp == 0 && lane == 0 && *abort_flag)     // let the copies land before shared memory is released
+  // Every copy lands before shared memory is released, whatever the abort flag says by now: a role that is
+  // still at work may give up after this one has left (at the usual end the last stages are on their way)
+  if (warp == 0 && lane == 0)
     for (uint32_t j = it >= uint32_t(L::kStages) ? it - L::kStages : 0; j < it; ++j)
       drain_wait(bar(G_FULL + int(j % L::kStages)), (j / L::kStages) & 1);
   if (warp == 1 && lane == 0) {                  // nothing of ours may run when TMEM is freed
