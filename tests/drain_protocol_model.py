@@ -1,4 +1,5 @@
-"""Host-side models of how the tcgen05 kernels end: nothing may be in flight when a CTA releases its memory.
+"""Host-side models of the tcgen05 products and attention gradient: what their waits cover, and how they end --
+nothing may be in flight when a CTA releases its memory.
 
 The warp roles of a kernel are Python generators that hand work to one another through mbarriers with the
 kernel's arrival counts and phase parities. TMA copies land in any order, the commits of one issuing thread in
@@ -198,3 +199,250 @@ def gemm(kblocks, stages, rng, timeout_p=0.0, late=False, drain="always", hold=F
 def random_gemm(rng):
     stages = rng.choice([2, 3, 6])
     return [rng.choice([1, 1, 2, 3, 5, 9]) for _ in range(rng.randint(1, 5))], stages
+
+
+def bwd_slot(d, key, g, is_x):
+    """Slot and use count of pair g's X or Y (attn_bwd.cu's slot_of)."""
+    if d == 64:
+        return 2 * (g % 4) + is_x, g // 4
+    if key:
+        n = 2 * g + (0 if is_x else 1)
+        return n % 5, n // 5
+    return (g % 3, g // 3) if is_x else (3 + g % 2, g // 2)
+
+
+def bwd_last_use(d, key, g, is_x, gx, gy):
+    """attn_bwd.cu's last_use."""
+    if d == 64:
+        return g + 4 >= (gx if is_x else gy)
+    if key:
+        return g + 2 >= gy if is_x else g + 3 >= gx
+    return g + 3 >= gx if is_x else g + 2 >= gy
+
+
+def bwd_pass(d, key, items, rng, timeout_p=0.0, late=False, drain="always", hold=False, first="free"):
+    """One pass of attn_bwd_kernel over items given as their numbers of streamed pairs: the producer warp with its
+    X and Y lanes, the issuers of S, dP, acc1 and (key pass) acc0, and the warps that turn S and dP into P and dS
+    (two here). drain: "always" (the kernel), "flag" (only if the abort flag is up when the producer leaves,
+    and for the last four loads of a lane whatever has used their slots since) or "never". first: what the issuers of
+    S and dP wait for first, "free" (the kernel: their buffer's release) or "full" (their tile)."""
+    s = Sim(rng, timeout_p, late)
+    B, n_wg, n_iss, bufs = s.bars, 2, 4 if key else 3, 1 if d == 128 else 2
+    for i in range(8):
+        s.bar(f"FULL{i}", 1)
+        s.bar(f"EMPTY{i}", 2 if d == 64 and key else 1)
+    for i in range(2):
+        for name, count in (("SFULL", 2), ("SFREE", n_wg), ("IFULL", 1), ("IEMPTY", n_iss + n_wg), ("PREADY", n_wg),
+                            ("PFREE", n_iss - 2)):
+            s.bar(f"{name}{i}", count)
+    for name, count in (("STATFULL", 1), ("STATEMPTY", 2), ("ACCFULL", n_iss - 2), ("ACCFREE", n_wg), ("COLS", n_wg),
+                        ("DRAIN", n_iss), ("HOLD", 1)):
+        s.bar(name, count)
+    info, pairs = [None, None], [None] * 4
+    held, stat = [None] * 8, [None]             # what the slots and the stationary tiles hold
+    g = {True: 0, False: 0}                      # pairs issued by the X and the Y lane
+    lanes = {"it": -1, True: None, False: None}  # the item at work; whether a lane is through (its ok)
+    sbuf, pbuf = [[None, None], [None, None]], [None, None]
+    done = {"S": -1, "dP": -1, "acc1": -1, "acc0": -1}       # last pair of each product that has completed
+    read = {"acc": -1, "s": [0, 0]}
+
+    def producer():
+        ok, stat_it = True, -1
+        for it in range(len(items) + 1):
+            slot = it & 1
+            if not (ok := (yield "wait", f"IEMPTY{slot}", ((it >> 1) & 1) ^ 1)):
+                break
+            info[slot] = (it, items[it]) if it < len(items) else (it, None)
+            B[f"IFULL{slot}"].arrive()
+            if it == len(items):
+                break
+            ok = yield "wait", "STATEMPTY", (it & 1) ^ 1
+            if ok:
+                if items[it] or drain != "flag":         # the flag form counted only the items with loads
+                    stat_it = it
+                if items[it]:
+                    def land(it=it):
+                        stat[0] = it
+                        B["STATFULL"].arrive()
+                    s.copy("stat", land)
+                else:
+                    B["STATFULL"].arrive()
+            lanes[True] = lanes[False] = None
+            lanes["ok"], lanes["it"] = ok, it
+            yield "until", lambda: lanes[True] is not None and lanes[False] is not None
+            ok = lanes[True] and lanes[False]
+            if not ok:
+                break
+        lanes["it"] = len(items)                          # the lanes leave
+        if drain == "never" or (drain == "flag" and not s.abort):
+            return
+        if stat_it >= 0:
+            yield "drain", "STATFULL", stat_it & 1
+        for x in (True, False):
+            for j in range(max(0, g[x] - 4), g[x]):
+                slot, use = bwd_slot(d, key, j, x)
+                if drain == "flag" or bwd_last_use(d, key, j, x, g[True], g[False]):
+                    yield "drain", f"FULL{slot}", use & 1
+
+    def lane(x):
+        for it in range(len(items)):
+            yield "until", lambda it=it: lanes["it"] >= it
+            if lanes["it"] == len(items):
+                return
+            ok = lanes["ok"]
+            for j in range(items[it]):
+                if not ok:
+                    break
+                slot, use = bwd_slot(d, key, g[x], x)
+                ok = yield "wait", f"EMPTY{slot}", (use & 1) ^ 1
+                if not ok:
+                    break
+                if held[slot] is not None:
+                    gg, xx = held[slot]
+                    users = [p for p in ("S" if xx else "dP", "acc1" if xx else "acc0")
+                             if p != "acc0" or key]
+                    if d == 64:
+                        users = ["acc1", "acc0"] if key else ["acc1"]
+                    check(all(done[p] >= gg for p in users), f"slot {slot} is filled before pair {gg} is used")
+                if x:
+                    pairs[g[x] & 3] = g[x]
+
+                def land(slot=slot, gg=g[x]):
+                    held[slot] = (gg, x)
+                    B[f"FULL{slot}"].arrive()
+                s.copy("x" if x else "y", land)
+                g[x] += 1
+            lanes[x] = ok
+
+    def issuer_s(name):
+        x, gi = name == "S", 0
+        for it in range(len(items) + 1):
+            slot = it & 1
+            if not (yield "wait", f"IFULL{slot}", (it >> 1) & 1):
+                break
+            got, n = info[slot]
+            check(got == it, f"{name} took item {got} for {it}")
+            B[f"IEMPTY{slot}"].arrive()
+            if n is None:
+                break
+            if not (yield "wait", "STATFULL", it & 1):
+                break
+            ok = True
+            for _ in range(n):
+                b, (sl, use) = gi & 1, bwd_slot(d, key, gi, x)
+                waits = [("wait", f"SFREE{b}", ((gi >> 1) & 1) ^ 1), ("wait", f"FULL{sl}", use & 1)]
+                for w in waits if first == "free" else waits[::-1]:
+                    ok = ok and (yield w)
+                if not ok:
+                    break
+                check(stat[0] == it and held[sl] == (gi, x), f"{name}({gi}) reads another tile")
+                check(gi < 2 or read["s"][b] == n_wg * (gi // 2), f"{name}({gi}) overwrites a buffer before it is read")
+
+                def land(gi=gi, b=b, sl=sl):
+                    sbuf[b][x], done[name] = gi, gi
+                    B[f"SFULL{b}"].arrive()
+                s.commit(name, land)
+                if not key and d == 128 and not x:
+                    s.commit(name, B[f"EMPTY{sl}"].arrive)
+                gi += 1
+            if not ok:
+                break
+            s.commit(name, B["STATEMPTY"].arrive)
+        s.commit(name, B["DRAIN"].arrive)
+        yield "drain", "DRAIN", 0
+
+    def issuer_acc(name):
+        x, gi = name == "acc1" and d == 128, 0
+        for it in range(len(items) + 1):
+            slot = it & 1
+            if not (yield "wait", f"IFULL{slot}", (it >> 1) & 1):
+                break
+            got, n = info[slot]
+            check(got == it, f"{name} took item {got} for {it}")
+            B[f"IEMPTY{slot}"].arrive()
+            if n is None:
+                break
+            if not (yield "wait", "ACCFREE", (it & 1) ^ 1):
+                break
+            check(read["acc"] >= it - 1, f"{name} overwrites gradients that are not read")
+            ok = True
+            for _ in range(n):
+                sl, use = bwd_slot(d, key, gi, x)
+                pb = gi % bufs
+                ok = yield "wait", f"FULL{sl}", use & 1
+                ok = ok and (yield "wait", f"PREADY{pb}", (gi // bufs) & 1)
+                if not ok:
+                    break
+                check(pbuf[pb] == gi and held[sl] == (gi, x), f"{name}({gi}) reads another pair")
+                check(d == 128 or held[sl + 1] == (gi, True), f"{name}({gi}) reads another X")
+
+                def land(gi=gi, pb=pb, sl=sl):
+                    done[name] = gi
+                    B[f"PFREE{pb}"].arrive()
+                    B[f"EMPTY{sl}"].arrive()
+                    if d == 64:
+                        B[f"EMPTY{sl + 1}"].arrive()
+                s.commit(name, land)
+                gi += 1
+            if not ok:
+                break
+            s.commit(name, B["ACCFULL"].arrive)
+        s.commit(name, B["DRAIN"].arrive)
+        yield "drain", "DRAIN", 0
+
+    finished, ready = {}, {}
+
+    def warp(w):
+        gi = 0
+        for it in range(len(items) + 1):
+            slot = it & 1
+            if not (yield "wait", f"IFULL{slot}", (it >> 1) & 1):
+                return
+            got, n = info[slot]
+            check(got == it, f"a warp took item {got} for {it}")
+            B[f"IEMPTY{slot}"].arrive()
+            if n is None:
+                return
+            if not key:
+                B["COLS"].arrive()
+                if not (yield "wait", "COLS", it & 1):
+                    return
+            for _ in range(n):
+                b, (sl, use), pb = gi & 1, bwd_slot(d, key, gi, True), gi % bufs
+                if not (yield "wait", f"FULL{sl}", use & 1):
+                    return
+                check(pairs[gi & 3] == gi, "a warp reads another pair's tiles")
+                if not (yield "wait", f"SFULL{b}", (gi >> 1) & 1):
+                    return
+                if hold and gi == 0 and not (yield "wait", "HOLD", 0):
+                    return
+                check(sbuf[b] == [gi, gi], f"a warp reads another pair's S or dP for {gi}")
+                read["s"][b] += 1
+                B[f"SFREE{b}"].arrive()
+                if not (yield "wait", f"PFREE{pb}", ((gi // bufs) & 1) ^ 1):
+                    return
+                check(min(done[a] for a in (("acc1", "acc0") if key else ("acc1",))) >= gi - bufs,
+                      "P is overwritten before its products have read it")
+                ready[gi] = ready.get(gi, 0) + 1
+                if ready[gi] == n_wg:
+                    pbuf[pb] = gi
+                B[f"PREADY{pb}"].arrive()
+                gi += 1
+            if not (yield "wait", "ACCFULL", it & 1):
+                return
+            check(n == 0 or min(done[a] for a in (("acc1", "acc0") if key else ("acc1",))) >= gi - 1,
+                  "gradients are read before they are complete")
+            finished[it] = finished.get(it, 0) + 1
+            if finished[it] == n_wg:
+                read["acc"] = it
+            B["ACCFREE"].arrive()
+
+    s.roles = {"producer": producer(), "lane x": lane(True), "lane y": lane(False), "S": issuer_s("S"), "dP": issuer_s("dP"),
+               "acc1": issuer_acc("acc1"), **({"acc0": issuer_acc("acc0")} if key else {}),
+               **{f"warp {w}": warp(w) for w in range(n_wg)}}
+    s.producers = {"producer", "lane x", "lane y"}
+    return s.run()
+
+
+def random_items(rng):
+    return [rng.choice([0, 1, 1, 2, 3, 5, 8]) for _ in range(rng.randint(1, 5))]

@@ -1,4 +1,5 @@
-"""How the tcgen05 kernels end, on host-side models of their barriers (no GPU): usual ends, waits that run out early and
+"""The barriers of the tcgen05 products and attention gradient on host-side models (no GPU): copies that land late, and
+how the kernels end: usual ends, waits that run out early and
 waits that run out after the producer has left, with its last copies still on their way."""
 import random
 
@@ -37,3 +38,21 @@ def test_a_producer_that_asks_the_flag_leaves_copies_behind():
     """What the model is for: the flag is not up yet when the producer leaves, and the copies outlive the CTA."""
     run = lambda drain: outcomes(lambda rng: M.gemm(*M.random_gemm(rng), rng, drain=drain, **WAYS["late"]), 200, 3)
     assert run("flag")["hazard"] > 0 and run("never")["hazard"] > 0
+
+
+PASSES = [(d, key) for d in (64, 128) for key in (False, True)]
+
+
+@pytest.mark.parametrize("late", [False, True])
+@pytest.mark.parametrize("d,key", PASSES)
+def test_attention_gradient_reads_its_own_tiles(d, key, late):
+    """Key and query passes, items without partners among them; late: copies land when nothing else can move, in any
+    order, so that an earlier load of a slot may still be on its way when a later one is waited for."""
+    assert outcomes(lambda rng: M.bwd_pass(d, key, M.random_items(rng), rng, late=late), 200, 4)["ok"] == 200
+
+
+def test_waiting_for_the_tile_before_the_buffer_reads_another_tile():
+    """Key pass at d = 128, five slots that X and Y share: a wait for Y of pair g passes on the parity of a phase two
+    back while X of pair g - 2 is on its way, so the buffer's release (which implies that load) comes first."""
+    run = lambda late: outcomes(lambda rng: M.bwd_pass(128, True, M.random_items(rng), rng, late=late, first="full"), 300, 4)
+    assert run(False)["hazard"] > 0 and run(True)["hazard"] > 0

@@ -412,9 +412,11 @@ __device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMa
         for (int j = 0; j < npairs; ++j, ++g) {
           const uint32_t b = g & 1;
           const SlotUse u = slot_of<D, KEY>(g, is_s);
-          if (!(ok = wait_bar(bar(Q_FULL + int(u.slot)), u.use & 1, abort_flag, gerr, prm.wait_ns))) break;
-          // the buffer's previous pair has been read
+          // The buffer's previous pair has been read: first, because it also says that the slot's previous load has
+          // landed. In the ring that X and Y share, Y of pair g follows X of pair g - 2, which this issuer has not
+          // waited for: with that load still on its way, the parity of Y's phase reads as if it had passed.
           if (!(ok = wait_bar(bar(Q_SFREE + int(b)), ((g >> 1) & 1) ^ 1, abort_flag, gerr, prm.wait_ns))) break;
+          if (!(ok = wait_bar(bar(Q_FULL + int(u.slot)), u.use & 1, abort_flag, gerr, prm.wait_ns))) break;
           tc_fence_after();
           const uint64_t da = da0 + u.slot * (L::kTensor >> 4);
 #pragma unroll
