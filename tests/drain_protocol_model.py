@@ -89,7 +89,7 @@ class Sim:
                     continue
             choices = [("role", k) for k in live if self._value(want[k]) is not None]
             copies = [i for i, (who, _) in enumerate(self.pending) if who.startswith("tma ")]
-            if not (self.late and not gone and choices):     # late: copies land last
+            if not (self.late and choices):      # late: copies land when nothing else can move
                 choices += [("land", i) for i in copies]
             firsts = {}
             for i, (who, _) in enumerate(self.pending):

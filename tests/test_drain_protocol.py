@@ -1,6 +1,6 @@
 """The barriers of the tcgen05 products and attention gradient on host-side models (no GPU): copies that land late, and
-how the kernels end: usual ends, waits that run out early and
-waits that run out after the producer has left, with its last copies still on their way."""
+how the kernels end: usual ends, waits that run out early and waits that run out after the producer has left, with
+its last copies still on their way."""
 import random
 
 import pytest
@@ -56,3 +56,38 @@ def test_waiting_for_the_tile_before_the_buffer_reads_another_tile():
     back while X of pair g - 2 is on its way, so the buffer's release (which implies that load) comes first."""
     run = lambda late: outcomes(lambda rng: M.bwd_pass(128, True, M.random_items(rng), rng, late=late, first="full"), 300, 4)
     assert run(False)["hazard"] > 0 and run(True)["hazard"] > 0
+
+
+
+@pytest.mark.parametrize("way", sorted(WAYS))
+@pytest.mark.parametrize("d,key", PASSES)
+def test_attention_gradient_ends_with_nothing_in_flight(d, key, way):
+    """Key and query passes, items without partners among them."""
+    seen = outcomes(lambda rng: M.bwd_pass(d, key, M.random_items(rng), rng, **WAYS[way]), 120, 4)
+    assert seen["hazard"] == 0 and (way != "usual" or seen["ok"] == 120) and (way == "usual" or seen["aborted"] > 0), seen
+
+
+@pytest.mark.parametrize("d,key", PASSES)
+def test_attention_gradient_that_is_held_runs_into_the_limit(d, key):
+    seen = outcomes(lambda rng: M.bwd_pass(d, key, [1] + M.random_items(rng), rng, hold=True), 40, 5)
+    assert seen == {"ok": 0, "aborted": 40, "hazard": 0}
+
+
+@pytest.mark.parametrize("d,key", PASSES)
+def test_an_attention_gradient_that_asks_the_flag_leaves_copies_behind(d, key):
+    for drain, way in (("flag", "late"), ("never", "late"), ("never", "early")):
+        run = lambda rng: M.bwd_pass(d, key, M.random_items(rng), rng, drain=drain, **WAYS[way])
+        assert outcomes(run, 200, 6)["hazard"] > 0, (drain, way)
+
+
+@pytest.mark.parametrize("d,key", [(128, False), (128, True)])
+def test_draining_a_slot_used_again_waits_for_nothing(d, key):
+    """The flag form's other fault: the parity of an earlier use of a slot, which does not come round again."""
+    for seed in range(400):
+        rng = random.Random(seed)
+        try:
+            M.bwd_pass(d, key, [8, 8], rng, drain="flag", timeout_p=0.02)
+        except M.Hazard as e:
+            if "waits for nothing" in str(e):
+                return
+    raise AssertionError("not met")

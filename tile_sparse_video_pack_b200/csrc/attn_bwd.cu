@@ -222,6 +222,13 @@ __device__ __forceinline__ SlotUse slot_of(uint32_t g, bool is_x) {
   }
   return is_x ? SlotUse{g % 3, g / 3} : SlotUse{3 + g % 2, g / 2};
 }
+// Whether pair g's X or Y is the last load into its slot, after gx loads of X and gy of Y.
+template <int D, bool KEY>
+__device__ __forceinline__ bool last_use(uint32_t g, bool is_x, uint32_t gx, uint32_t gy) {
+  if (D == 64) return g + 4 >= (is_x ? gx : gy);
+  if (KEY) return is_x ? g + 2 >= gy : g + 3 >= gx;   // five slots on: Y of pair g + 2, X of pair g + 3
+  return is_x ? g + 3 >= gx : g + 2 >= gy;
+}
 
 enum {
   Q_FULL = 0, Q_EMPTY = 8, Q_SFULL = 16, Q_SFREE = 18, Q_IFULL = 20, Q_IEMPTY = 22, Q_PREADY = 24, Q_PFREE = 26,
@@ -292,7 +299,7 @@ __device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMa
   if (warp == 0) {
     // ---------------------------------------------------------- producer ---
     uint32_t g = 0;                              // streamed pairs issued by this lane (0: X, 1: Y)
-    int stat_it = -1;                            // item of the last stationary load
+    int stat_it = -1;                            // last item whose stationary phase is under way or over
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
       const int slot = it & 1;
@@ -336,10 +343,10 @@ __device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMa
             tma_load_2d(sbase + L::oStat + c * kBox, &txs, 64 * c, y, bar(Q_STATFULL));
             tma_load_2d(sbase + L::oStat + L::kStat + c * kBox, &tys, 64 * c, y, bar(Q_STATFULL));
           }
-          stat_it = int(it);
         } else if (ok) {
           mbar_arrive(bar(Q_STATFULL));          // nothing to load: keep the phases in step with the items
         }
+        if (ok) stat_it = int(it);
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       // the streamed tiles, two at a time, in ascending order: lane 0 loads X, lane 1 Y, each
@@ -383,11 +390,15 @@ __device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMa
       __syncwarp();
       ok = __all_sync(0xffffffffu, ok);
     }
-    if (lane < 2 && *abort_flag) {               // let the copies land before shared memory is released
+    // Every copy lands before shared memory serves anything else, whatever the abort flag says by now: a role
+    // that is still at work may give up after this one has left. Each lane waits for the last use of its slots;
+    // a slot that has been used again since was empty before that.
+    const uint32_t gx = __shfl_sync(0xffffffffu, g, 0), gy = __shfl_sync(0xffffffffu, g, 1);
+    if (lane < 2) {
       if (lane == 0 && stat_it >= 0) drain_wait(bar(Q_STATFULL), uint32_t(stat_it) & 1);
-      for (uint32_t j = g >= 4 ? g - 4 : 0; j < g; ++j) {   // at most four loads of a lane are in flight
+      for (uint32_t j = g >= 4 ? g - 4 : 0; j < g; ++j) {
         const SlotUse u = slot_of<D, KEY>(j, lane == 0);
-        drain_wait(bar(Q_FULL + int(u.slot)), u.use & 1);
+        if (last_use<D, KEY>(j, lane == 0, gx, gy)) drain_wait(bar(Q_FULL + int(u.slot)), u.use & 1);
       }
     }
     __syncwarp();
