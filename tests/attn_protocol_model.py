@@ -23,7 +23,8 @@ eight softmax warps alone. `faults` plants protocol mistakes (the tests check
 that the model catches them): "s_skips_pv_done" (the S issuer reuses an S
 buffer without waiting for the PVs that read its P) and "softmax_parity" (the
 softmax waits on the wrong phase parity), "mma_no_drain" and "tma_no_drain"
-(the MMA issuers or the producer lanes leave without draining).
+(the MMA issuers or the producer lanes leave without draining), "tma_asks_flag" (the producer lanes drain only if
+the abort flag is up when they leave: the earlier kernel, which misses a role that gives up later).
 
 Bounded waits and the abort path: every wait of the kernel gives up after a
 time limit. When no role can move and nothing is in flight, the model lets one
@@ -149,7 +150,7 @@ def run(blocks_per_item, rng, slot_readers_release=True, starve=(), faults=(), h
                 break
             if slot_readers_release:
                 bars[f"LEMPTY{slot}"].arrive()
-        if flags["abort"] and "tma_no_drain" not in faults:
+        if "tma_no_drain" not in faults and (flags["abort"] or "tma_asks_flag" not in faults):
             yield drain_copies("tmaK" if is_k else "tmaV")
 
     def s_issuer():

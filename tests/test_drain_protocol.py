@@ -5,6 +5,7 @@ import random
 
 import pytest
 
+import attn_protocol_model as A
 import drain_protocol_model as M
 
 WAYS = {"usual": dict(), "early": dict(timeout_p=0.02), "late": dict(timeout_p=0.3, late=True)}
@@ -91,3 +92,22 @@ def test_draining_a_slot_used_again_waits_for_nothing(d, key):
             if "waits for nothing" in str(e):
                 return
     raise AssertionError("not met")
+
+
+def attention(rng, fault=None):
+    """The forward with copies that land when nothing else can move, and waits that run out meanwhile."""
+    items = A.random_items(rng, allow_empty=True)
+    try:
+        r = A.run(items, rng, starve=("tmaK", "tmaV"), timeout_p=0.01, faults=(fault,) if fault else ())
+    except A.Hazard as e:
+        raise M.Hazard(str(e)) from None
+    return r.split(":")[0]
+
+
+def test_attention_ends_with_nothing_in_flight_when_a_role_gives_up_late():
+    seen = outcomes(attention, 300, 7)
+    assert seen["hazard"] == 0 and seen["aborted"] > 0, seen
+
+
+def test_an_attention_that_asks_the_flag_leaves_copies_behind():
+    assert outcomes(lambda rng: attention(rng, "tma_asks_flag"), 300, 8)["hazard"] > 0

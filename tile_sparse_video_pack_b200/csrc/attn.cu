@@ -497,12 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         mbar_arrive(bar(B_LEMPTY0 + slot));   // this lane is done with the slot's list
       }
-      if (*abort_flag) {
-        // let every copy this thread issued land before shared memory is released
-        if (is_k && issuedQ) drain_wait(bar(B_QFULL), (issuedQ - 1) & 1);
-        for (uint32_t gg = (g >= uint32_t(nst) ? g - nst : 0); gg < g; ++gg)
-          drain_wait(bar(full0 + int(gg % nst)), (gg / nst) & 1);
-      }
+      // every copy this thread issued lands before shared memory is released, whatever the abort flag says by
+      // now: a role that is still at work may give up after this one has left
+      if (is_k && issuedQ) drain_wait(bar(B_QFULL), (issuedQ - 1) & 1);
+      for (uint32_t gg = (g >= uint32_t(nst) ? g - nst : 0); gg < g; ++gg)
+        drain_wait(bar(full0 + int(gg % nst)), (gg / nst) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {

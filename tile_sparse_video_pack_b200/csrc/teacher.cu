@@ -135,11 +135,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         ++issued;
       }
-      if (*abort_flag) {   // let this thread's copies land before shared memory is released
-        drain_wait(bar(T_QFULL), 0);
-        for (uint32_t j = issued >= 2 ? issued - 2 : 0; j < issued; ++j)
-          drain_wait(bar(T_KFULL0 + int(j & 1)), (j >> 1) & 1);
-      }
+      // this thread's copies land before shared memory is released, whatever the abort flag says by now: a role
+      // that is still at work may give up after this one has left
+      drain_wait(bar(T_QFULL), 0);
+      for (uint32_t j = issued >= 2 ? issued - 2 : 0; j < issued; ++j)
+        drain_wait(bar(T_KFULL0 + int(j & 1)), (j >> 1) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
