@@ -45,22 +45,32 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// SiLU has no cubic term: as GELU's with a coefficient of 0 it would be 0 times infinity from |z| = 2^64 on.
 __device__ __forceinline__ void act_fwd(float (&v)[8], int act) {
   if (act == VSA_ACT_NONE) return;
-  const bool gelu = act == VSA_ACT_GELU_TANH;
-  const float c1 = gelu ? -kGeluB * kLog2e : -kLog2e, c3 = gelu ? -0.044715f * kGeluB * kLog2e : 0.f;
-  const uint64_t c1p = f2pack(c1, c1), c3p = f2pack(c3, c3), one = f2pack(1.f, 1.f);
+  const uint64_t one = f2pack(1.f, 1.f);
+  auto apply = [&](auto exponent) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const uint64_t z = f2pack(v[i], v[i + 1]);
-    float x0, x1;
-    f2unpack(fmul2(z, ffma2(fmul2(z, z), c3p, c1p)), x0, x1);   // -2u log2 e (SiLU: -z log2 e)
-    f2unpack(fadd2(f2pack(ex2(x0), ex2(x1)), one), x0, x1);
-    f2unpack(fmul2(z, f2pack(rcp(x0), rcp(x1))), v[i], v[i + 1]);
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t z = f2pack(v[i], v[i + 1]);
+      float x0, x1;
+      f2unpack(exponent(z), x0, x1);
+      f2unpack(fadd2(f2pack(ex2(x0), ex2(x1)), one), x0, x1);
+      f2unpack(fmul2(z, f2pack(rcp(x0), rcp(x1))), v[i], v[i + 1]);
+    }
+  };
+  if (act == VSA_ACT_GELU_TANH) {
+    constexpr float c1 = -kGeluB * kLog2e, c3 = -0.044715f * kGeluB * kLog2e;
+    const uint64_t c1p = f2pack(c1, c1), c3p = f2pack(c3, c3);
+    apply([&](uint64_t z) { return fmul2(z, ffma2(fmul2(z, z), c3p, c1p)); });   // -2u log2 e
+  } else {
+    const uint64_t c1p = f2pack(-kLog2e, -kLog2e);
+    apply([&](uint64_t z) { return fmul2(z, c1p); });                            // -z log2 e
   }
 }
 // act(z) and act'(z) of two elements: with s = sigmoid(u), f = z s and
-// f' = s + f (1 - s) u' (SiLU: u = z; GELU: u the 2u above).
+// f' = s + f (1 - s) u' (SiLU: u = z; GELU: u the 2u above). Far out s is 0 or 1
+// exactly, and so is f': there f or u' may be infinite, and their factor 0.
 __device__ __forceinline__ void act_both(uint64_t z, int act, uint64_t& f, uint64_t& df) {
   const uint64_t one = f2pack(1.f, 1.f);
   if (act == VSA_ACT_NONE) {
@@ -68,16 +78,24 @@ __device__ __forceinline__ void act_both(uint64_t z, int act, uint64_t& f, uint6
     df = one;
     return;
   }
-  const bool gelu = act == VSA_ACT_GELU_TANH;
-  const float c1 = gelu ? kGeluB : 1.f, c3 = gelu ? 0.044715f * kGeluB : 0.f;
-  const uint64_t z2 = fmul2(z, z), l = f2pack(-kLog2e, -kLog2e);
-  float x0, x1;
-  f2unpack(fmul2(fmul2(z, l), ffma2(z2, f2pack(c3, c3), f2pack(c1, c1))), x0, x1);
+  uint64_t x = fmul2(z, f2pack(-kLog2e, -kLog2e)), du = one;
+  if (act == VSA_ACT_GELU_TANH) {
+    constexpr float c1 = kGeluB, c3 = 0.044715f * kGeluB;
+    const uint64_t z2 = fmul2(z, z);
+    x = fmul2(x, ffma2(z2, f2pack(c3, c3), f2pack(c1, c1)));
+    du = ffma2(z2, f2pack(3.f * c3, 3.f * c3), f2pack(c1, c1));
+  }
+  float x0, x1, s0, s1, z0, z1, d0, d1;
+  f2unpack(x, x0, x1);
   f2unpack(fadd2(f2pack(ex2(x0), ex2(x1)), one), x0, x1);
-  const uint64_t s = f2pack(rcp(x0), rcp(x1));
+  s0 = rcp(x0);
+  s1 = rcp(x1);
+  const uint64_t s = f2pack(s0, s1);
   f = fmul2(z, s);
-  const uint64_t du = ffma2(z2, f2pack(3.f * c3, 3.f * c3), f2pack(c1, c1));
-  df = ffma2(fmul2(f, ffma2(s, f2pack(-1.f, -1.f), one)), du, s);
+  f2unpack(ffma2(fmul2(f, ffma2(s, f2pack(-1.f, -1.f), one)), du, s), d0, d1);
+  f2unpack(z, z0, z1);
+  constexpr float kFar = 1e4f;
+  df = f2pack(fabsf(z0) > kFar ? s0 : d0, fabsf(z1) > kFar ? s1 : d1);
 }
 
 // -------------------------------------------------------------- epilogue ----
