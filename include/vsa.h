@@ -572,8 +572,10 @@ VSA_API vsa_status vsa_plan_set_wait_limit(vsa_plan* plan, uint64_t limit_ns);
  * on = 1, every later attention launch of this plan has its softmax warps,
  * after their first block of scores, wait on a barrier that nothing arrives
  * on, so each CTA runs into the wait limit and takes the abort path with
- * copies and tensor-core work in flight. on = 0 (the default) turns it off.
- * Not for production use. */
+ * copies and tensor-core work in flight; so do the attention's gradient (after
+ * a pass's first products) and linear calls that work in tiles (after the first
+ * tile's products; up to 16 rows have no waits). on = 0 (the default) turns it
+ * off. Not for production use. */
 VSA_API vsa_status vsa_plan_set_test_hold(vsa_plan* plan, int32_t on);
 
 /* Waits for the plan's device (cudaDeviceSynchronize), then returns and clears

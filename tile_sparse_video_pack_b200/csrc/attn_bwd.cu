@@ -232,7 +232,7 @@ __device__ __forceinline__ bool last_use(uint32_t g, bool is_x, uint32_t gx, uin
 
 enum {
   Q_FULL = 0, Q_EMPTY = 8, Q_SFULL = 16, Q_SFREE = 18, Q_IFULL = 20, Q_IEMPTY = 22, Q_PREADY = 24, Q_PFREE = 26,
-  Q_STATFULL = 28, Q_STATEMPTY, Q_ACCFULL, Q_ACCFREE, Q_COLS, Q_DRAIN, Q_COUNT
+  Q_STATFULL = 28, Q_STATEMPTY, Q_ACCFULL, Q_ACCFREE, Q_COLS, Q_DRAIN, Q_HOLD, Q_COUNT
 };
 static_assert(Q_COUNT <= 40, "barrier slots");
 
@@ -249,6 +249,7 @@ struct BwdCommon {
   const int32_t* counts;            // [heads][nt_max]
   int32_t heads, bh_total, nt_max, words, key_ctas, by_head;
   float scale_log2, scale;
+  int32_t hold;                     // test hook: the step to P waits, at its first pair, on a barrier nothing arrives on
 };
 struct BwdMaps {
   CUtensorMap q, k, v, dO;
@@ -291,6 +292,7 @@ __device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMa
     mbar_init(bar(Q_ACCFREE), 8);
     mbar_init(bar(Q_COLS), 8);
     mbar_init(bar(Q_DRAIN), kIssuers);
+    mbar_init(bar(Q_HOLD), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -541,6 +543,7 @@ __device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMa
         }
         const int b = int(g & 1);
         ok = wait_bar(bar(Q_SFULL + b), (g >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+        if (prm.hold && g == 0) ok = ok && wait_bar(bar(Q_HOLD), 0, abort_flag, gerr, prm.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[32], dp[32];
@@ -778,6 +781,7 @@ cudaError_t launch_attn_bwd(const vsa_plan* p, const void* qp, const void* kp, c
   BwdCommon prm;
   prm.state = p->d_state;
   prm.wait_ns = p->wait_ns;
+  prm.hold = p->test_hold;
   prm.n_items = int64_t(bh) * g.nt_max;
   prm.lse2 = lse2;
   prm.delta = delta;

@@ -241,6 +241,7 @@ struct GemmParams {
   int32_t n_prod, units;   // products and the tiles of all of them
   int32_t splits;          // CTAs of a cluster that share a tile's K
   int32_t group;           // row tiles per group of the tile order
+  int32_t hold;            // test hook: the epilogue waits, at its first tile, on a barrier nothing arrives on
 };
 struct GemmMaps {
   CUtensorMap a[2], b[2];
@@ -256,7 +257,7 @@ struct GSmem {
   static constexpr uint32_t oMisc = oBar + 24 * 8;
   static constexpr uint32_t oEnd = oMisc + 16;
 };
-enum { G_FULL = 0, G_EMPTY = 8, G_AFULL = 16, G_AEMPTY = 18, G_DRAIN = 20 };
+enum { G_FULL = 0, G_EMPTY = 8, G_AFULL = 16, G_AEMPTY = 18, G_DRAIN = 20, G_HOLD = 21 };
 
 // Tile u: tiles run down groups of `group` row tiles before the next column tile,
 // so that the CTAs at work share operand tiles in L2.
@@ -343,6 +344,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
       mbar_init(bar(G_AEMPTY + i), kEWarps);     // one arrival per epilogue warp
     }
     mbar_init(bar(G_DRAIN), 1);
+    mbar_init(bar(G_HOLD), 1);
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -408,6 +410,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
         next = load_chunk(pr.ep, rows, pr.N, t.n * BN + c0, lane);
       }
       ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+      if (prm.hold && n == 0) ok = ok && wait_bar(bar(G_HOLD), 0, abort_flag, gerr, prm.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after();
@@ -532,6 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       mbar_init(bar(G_AEMPTY + i), 2 * kEWarps); // the epilogue warps of both CTAs
     }
     mbar_init(bar(G_DRAIN), 1);
+    mbar_init(bar(G_HOLD), 1);
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -614,7 +618,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       // while the products run
       const StripRows rows = strip_rows(pr.ep, pr.M, int64_t(t.m) * 256 + rank * 128 + q4 * 32, lane);
       Chunk next = load_chunk(pr.ep, rows, pr.N, t.n * 256 + c0, lane);
-      const bool ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+      bool ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+      if (prm.hold && n == 0) ok = ok && wait_bar(bar(G_HOLD), 0, abort_flag, gerr, prm.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
 #pragma unroll 1
@@ -908,6 +913,7 @@ cudaError_t run_products(const vsa_plan* p, const Problem* q, int n, cudaStream_
     memset(&prm, 0, sizeof(prm));
     prm.state = p->d_state;
     prm.wait_ns = p->wait_ns;
+    prm.hold = p->test_hold;
     prm.group = kGroup;
     prm.splits = 1;
   };

@@ -854,7 +854,7 @@ class Plan:
         _check(library().vsa_plan_set_wait_limit(self._h, int(limit_ns)), "vsa_plan_set_wait_limit")
 
     def set_test_hold(self, on: bool):
-        """Test hook: attention's softmax waits for a release nothing gives, until the wait limit."""
+        """Test hook: attention, its gradient and linear wait for a release nothing gives, until the wait limit."""
         _check(library().vsa_plan_set_test_hold(self._h, 1 if on else 0), "vsa_plan_set_test_hold")
 
     def check(self):
