@@ -561,7 +561,8 @@ VSA_API vsa_status vsa_linear_bwd(vsa_plan* plan, const vsa_linear_grad_args* ar
 
 /* Bound of every device-side wait of the plan's tcgen05 kernels (attention and
  * its gradient, linear, teacher map), in nanoseconds: 1,000 .. 60,000,000,000; 0 restores the
- * default of two seconds. A kernel whose wait runs past it stops: it latches
+ * default of two seconds. (A linear call's wait for a whole tile has 10 us more for every 64 of
+ * the sum's length.) A kernel whose wait runs past it stops: it latches
  * VSA_ERR_DEVICE_TIMEOUT (returned by vsa_plan_check), lets its own copies and
  * tensor-core work finish, frees its tensor memory and returns, leaving the
  * CUDA context usable (fail loudly, never hang: "From 650 s to 72 s", "What

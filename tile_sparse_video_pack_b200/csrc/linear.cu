@@ -257,6 +257,11 @@ struct GSmem {
   static constexpr uint32_t oMisc = oBar + 24 * 8;
   static constexpr uint32_t oEnd = oMisc + 16;
 };
+// The bound of the epilogue's wait for a tile's products: the plan's limit and, because a sum over rows may have millions
+// of k blocks, 10 us for each (one takes 0.1 to 0.8, the latter with all SMs at HBM). A stall is found within the
+// limit all the same: producer and issuer wait for one k block at a time.
+__device__ __forceinline__ uint64_t tile_limit(uint64_t wait_ns, int kblocks) { return wait_ns + uint64_t(kblocks) * 10000u; }
+
 enum { G_FULL = 0, G_EMPTY = 8, G_AFULL = 16, G_AEMPTY = 18, G_DRAIN = 20, G_HOLD = 21 };
 
 // Tile u: tiles run down groups of `group` row tiles before the next column tile,
@@ -409,7 +414,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
         rows = strip_rows(pr.ep, pr.M, int64_t(t.m) * kBM + q4 * 32, lane);
         next = load_chunk(pr.ep, rows, pr.N, t.n * BN + c0, lane);
       }
-      ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+      ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, tile_limit(prm.wait_ns, k1 - k0));
       if (prm.hold && n == 0) ok = ok && wait_bar(bar(G_HOLD), 0, abort_flag, gerr, prm.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
@@ -618,7 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       // while the products run
       const StripRows rows = strip_rows(pr.ep, pr.M, int64_t(t.m) * 256 + rank * 128 + q4 * 32, lane);
       Chunk next = load_chunk(pr.ep, rows, pr.N, t.n * 256 + c0, lane);
-      bool ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, prm.wait_ns);
+      bool ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, tile_limit(prm.wait_ns, pr.kblocks));
       if (prm.hold && n == 0) ok = ok && wait_bar(bar(G_HOLD), 0, abort_flag, gerr, prm.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
