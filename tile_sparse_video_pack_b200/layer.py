@@ -119,6 +119,19 @@ def _keeps(x, out, save):
         raise ValueError("out overlaps x, which backward needs: save=True takes another output")
 
 
+def _saved_tensors(saved):
+    """What a forward kept, ready for backward on the current stream: another stream than the forward's, whose pool
+    the tensors go back to with the next forward, must have been waited for before they are used again."""
+    import torch
+    stream = torch.cuda.current_stream()
+    made_on, tensors = saved
+    if stream != made_on:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    return tensors
+
+
 class TileSparseBlock:
     """The attention half of a transformer block: y = residual + gate * (attention(norm, rotation(x w_qkv^T + b_qkv))
     w_out^T + b_out), with its gradient.
@@ -130,7 +143,8 @@ class TileSparseBlock:
     the selected tiles as given; not with ``layer.direct``). The packed tiles stay in the layer's buffers, which
     its next forward overwrites: backward refuses then, so blocks that are trained need a layer each. (A replayed
     graph's forward is not noticed: capture a forward and its backward together.) With ``stream`` the whole call, its
-    allocations too, is that stream's.
+    allocations too, is that stream's; a backward on another stream than its forward's waits for that one first, and
+    the next forward, which fills the layer's buffers anew, for the backward's (``wait_stream``).
     """
 
     def __init__(self, layer: TileSparseAttention, w_qkv, w_out, norm: NormRope, b_qkv=None, b_out=None):
@@ -180,7 +194,8 @@ class TileSparseBlock:
         y = _new(x, B, N, self.w_out.shape[0]) if out is None else out
         pre = _new(x, B, N, self.w_out.shape[0]) if save and gate is not None else None
         p.linear(o.view(B, N, width), self.w_out, y, bias=self.b_out, gate=gate, residual=residual, pre=pre)
-        self._saved = (x, qkv, o, gate, pre, L.runs) if save else None
+        self._saved = (torch.cuda.current_stream(), (x, qkv, o, gate, pre)) if save else None
+        self._run = L.runs
         return y
 
     __call__ = forward
@@ -194,10 +209,10 @@ class TileSparseBlock:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.backward(dy)
-        x, qkv, o, gate, pre, run = self._saved
         L, b = self.layer, self.layer.bufs
-        if L.runs != run:
+        if L.runs != self._run:
             raise ValueError("the layer has run again since this block's forward: its tiles are another's")
+        x, qkv, o, gate, pre = _saved_tensors(self._saved)
         p = L.plan
         B, N, heads, d = p.shapes()["tokens"]
         width, f32 = heads * d, torch.float32
@@ -233,7 +248,8 @@ class TileSparseBlock:
 
 class FeedForward:
     """The other half of the block: y = residual + gate * (act(x w_up^T + b_up) w_down^T + b_down), with its gradient.
-    ``plan`` names the device; weights bf16, biases and gate [samples, channels] fp32 (or None)."""
+    ``plan`` names the device; weights bf16, biases and gate [samples, channels] fp32 (or None). A backward on another
+    stream than its forward's waits for that one first (``wait_stream``); the next forward need not wait for it."""
 
     def __init__(self, plan: Plan, w_up, w_down, b_up=None, b_down=None, act="gelu_tanh"):
         if w_up.dim() != 2 or w_down.dim() != 2 or w_up.shape[0] != w_down.shape[1]:
@@ -243,8 +259,8 @@ class FeedForward:
         self._saved = None
 
     def forward(self, x, residual=None, gate=None, out=None, save=False, stream=None):
+        import torch
         if stream is not None:
-            import torch
             with torch.cuda.stream(stream):
                 return self.forward(x, residual, gate, out, save)
         _keeps(x, out, save)
@@ -255,7 +271,7 @@ class FeedForward:
         y = _new(x, *lead, self.w_down.shape[0]) if out is None else out
         pre = _new(x, *lead, self.w_down.shape[0]) if save and gate is not None else None
         p.linear(h, self.w_down, y, bias=self.b_down, gate=gate, residual=residual, pre=pre)
-        self._saved = (x, hidden, h, gate, pre) if save else None
+        self._saved = (torch.cuda.current_stream(), (x, hidden, h, gate, pre)) if save else None
         return y
 
     __call__ = forward
@@ -268,7 +284,7 @@ class FeedForward:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.backward(dy)
-        x, hidden, h, gate, pre = self._saved
+        x, hidden, h, gate, pre = _saved_tensors(self._saved)
         p = self.plan
         like = lambda t: None if t is None else torch.empty_like(t)
         g = {"x": torch.empty_like(x), "w_up": torch.empty_like(self.w_up), "w_down": torch.empty_like(self.w_down),
