@@ -72,3 +72,19 @@ def test_activation_and_gate_shapes():
         with pytest.raises(ValueError):
             T.Plan._gate(torch.zeros(shape), 8, 64, 0)
     assert T.Plan._gate(None, 8, 64, 0) == (None, 0)
+
+
+def test_an_output_beside_the_input_is_taken_and_one_over_it_refused():
+    from tile_sparse_video_pack_b200.layer import _keeps
+    wide = torch.zeros(2, 6, 96, dtype=torch.bfloat16)
+    x = wide[..., 16:48]
+    for out in (wide[..., 48:], wide[..., :16], wide[..., 72:80], torch.zeros(2, 6, 32, dtype=torch.bfloat16), None, wide[:0]):
+        _keeps(x, out, True)
+    _keeps(wide[:1, :, :32], wide[1:, :, :32], True)
+    for out in (x, wide[..., :24], wide[..., 40:72], wide[..., 47:48], wide[:1, 3:4, 16:24], wide.view(-1)[16:24],
+                wide[..., 0:96], wide.view(2, 12, 48)[:, ::2]):
+        _keeps(x, out, False)
+        with pytest.raises(ValueError):
+            _keeps(x, out, True)
+    with pytest.raises(ValueError):      # rows that wrap into the next one's columns
+        _keeps(wide.view(-1)[80:176].view(1, 96), wide.view(-1)[96:128].view(1, 32), True)

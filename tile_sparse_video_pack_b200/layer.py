@@ -109,6 +109,15 @@ def _workspace(like, n):
     return torch.empty(n, dtype=torch.uint8, device=like.device)
 
 
+def _row_bytes(t):
+    """Bytes from row to row of a [..., cols] view whose leading dimensions form one row axis, else None."""
+    try:
+        m = t.view(-1, t.shape[-1])
+    except RuntimeError:
+        return None
+    return m.stride(0) * t.element_size() if m.stride(1) == 1 else None
+
+
 def _keeps(x, out, save):
     """Refuses an output over the input that backward needs."""
     if not save or out is None or x.numel() == 0 or out.numel() == 0:
@@ -116,6 +125,11 @@ def _keeps(x, out, save):
     lo = [t.data_ptr() for t in (x, out)]
     hi = [a + (1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride()))) * t.element_size() for a, t in zip(lo, (x, out))]
     if lo[0] < hi[1] and lo[1] < hi[0]:
+        row = _row_bytes(x)
+        if row and row == _row_bytes(out):     # column slices of one buffer may lie side by side
+            at = (lo[1] - lo[0]) % row
+            if x.shape[-1] * x.element_size() <= at and at + out.shape[-1] * out.element_size() <= row:
+                return
         raise ValueError("out overlaps x, which backward needs: save=True takes another output")
 
 
