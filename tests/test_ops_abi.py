@@ -88,3 +88,22 @@ def test_an_output_beside_the_input_is_taken_and_one_over_it_refused():
             _keeps(x, out, True)
     with pytest.raises(ValueError):      # rows that wrap into the next one's columns
         _keeps(wide.view(-1)[80:176].view(1, 96), wide.view(-1)[96:128].view(1, 32), True)
+
+
+def test_blocks_refuse_biases_of_another_length():
+    """The direct path slices b_qkv: a longer one would have been taken without a word."""
+    from types import SimpleNamespace as NS
+    layer = NS(plan=NS(desc=NS(heads=2, head_dim=64)))
+    w_qkv, w_out, norm = torch.zeros(384, 96), torch.zeros(80, 128), T.NormRope()
+    T.TileSparseBlock(layer, w_qkv, w_out, norm, torch.zeros(384), torch.zeros(80))
+    T.FeedForward(None, w_qkv, torch.zeros(96, 384), torch.zeros(384), torch.zeros(96))
+    for b in (torch.zeros(392), torch.zeros(376), torch.zeros(1, 384)):
+        with pytest.raises(ValueError):
+            T.TileSparseBlock(layer, w_qkv, w_out, norm, b)
+        with pytest.raises(ValueError):
+            T.FeedForward(None, w_qkv, torch.zeros(96, 384), b)
+    for b in (torch.zeros(128), torch.zeros(80, 1)):
+        with pytest.raises(ValueError):
+            T.TileSparseBlock(layer, w_qkv, w_out, norm, None, b)
+        with pytest.raises(ValueError):
+            T.FeedForward(None, w_qkv, torch.zeros(96, 384), None, b)

@@ -109,6 +109,11 @@ def _workspace(like, n):
     return torch.empty(n, dtype=torch.uint8, device=like.device)
 
 
+def _check_bias(name, b, n):
+    if b is not None and tuple(b.shape) != (n,):
+        raise ValueError(f"{name} must be [{n}], got {tuple(b.shape)}")
+
+
 def _row_bytes(t):
     """Bytes from row to row of a [..., cols] view whose leading dimensions form one row axis, else None."""
     try:
@@ -169,6 +174,8 @@ class TileSparseBlock:
             raise ValueError(f"w_qkv must be [{3 * width}, channels], got {tuple(w_qkv.shape)}")
         if w_out.dim() != 2 or w_out.shape[1] != width:
             raise ValueError(f"w_out must be [channels, {width}], got {tuple(w_out.shape)}")
+        _check_bias("b_qkv", b_qkv, 3 * width)
+        _check_bias("b_out", b_out, w_out.shape[0])
         self.layer, self.norm = layer, norm
         self.w_qkv, self.b_qkv, self.w_out, self.b_out = w_qkv, b_qkv, w_out, b_out
         self._saved = None
@@ -268,6 +275,8 @@ class FeedForward:
     def __init__(self, plan: Plan, w_up, w_down, b_up=None, b_down=None, act="gelu_tanh"):
         if w_up.dim() != 2 or w_down.dim() != 2 or w_up.shape[0] != w_down.shape[1]:
             raise ValueError(f"w_up {tuple(w_up.shape)} and w_down {tuple(w_down.shape)} do not follow each other")
+        _check_bias("b_up", b_up, w_up.shape[0])
+        _check_bias("b_down", b_down, w_down.shape[0])
         self.plan, self.act = plan, act
         self.w_up, self.b_up, self.w_down, self.b_down = w_up, b_up, w_down, b_down
         self._saved = None
