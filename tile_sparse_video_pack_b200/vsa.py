@@ -413,24 +413,26 @@ class Plan:
         """Device buffers for every intermediate of the layer (torch is only the allocator).
 
         packed=False leaves out the packed tiles (qp, kp, vp, op: None), which a plan with
-        info.direct_attn does not need."""
+        info.direct_attn does not need. Where heads differ in their number of tiles, the calls leave the
+        entries past a head's own unwritten: they are zero here."""
         import torch
         dev = torch.device("cuda") if device is None else torch.device(device)
         s = self.shapes()
-        pk = (lambda: torch.empty(s["packed"], dtype=torch.bfloat16, device=dev)) if packed else (lambda: None)
-        bufs = {
-            "qp": pk(),
-            "kp": pk(),
-            "vp": pk(),
-            "op": pk(),
-            "scores": torch.empty(s["scores"], dtype=torch.float32, device=dev),
-            "idx": torch.empty(s["idx"], dtype=torch.int32, device=dev),
-            "workspace": torch.empty(s["workspace"], dtype=torch.uint8, device=dev),
-            "lse": torch.empty(s["lse"], dtype=torch.float32, device=dev) if with_lse else None,
-        }
+        ragged = any(self.info.ntv[h] != self.info.ntv_max for h in range(self.desc.heads))
+
+        def new(name, dtype, written=False):
+            return (torch.zeros if ragged and not written else torch.empty)(s[name], dtype=dtype, device=dev)
+
+        bufs = {x: new("packed", torch.bfloat16, x != "op") if packed else None for x in ("qp", "kp", "vp", "op")}
+        bufs.update({
+            "scores": new("scores", torch.float32),
+            "idx": new("idx", torch.int32),
+            "workspace": new("workspace", torch.uint8, True),
+            "lse": new("lse", torch.float32) if with_lse else None,
+        })
         if self.info.n_ref_tiles:
-            bufs["scores_ref"] = torch.empty(s["scores_ref"], dtype=torch.float32, device=dev)
-            bufs["idx_ref"] = torch.empty(s["idx_ref"], dtype=torch.int32, device=dev)
+            bufs["scores_ref"] = new("scores_ref", torch.float32)
+            bufs["idx_ref"] = new("idx_ref", torch.int32)
         return bufs
 
     # ---- the five calls (same names as the C ABI) ------------------------------
