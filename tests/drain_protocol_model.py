@@ -114,17 +114,16 @@ class Sim:
 def gemm(kblocks, stages, rng, timeout_p=0.0, late=False, drain="always", hold=False):
     """gemm_kernel<false, BN>: tiles of kblocks[n] k blocks through `stages` stages and two accumulators, with a
     producer, an MMA issuer and epilogue warps (two here). drain: "always" (the kernel), "flag" (only if the
-    abort flag is up when the producer leaves) or "never". hold: the epilogue waits for a release nothing gives."""
+    abort flag is up when the producer leaves) or "never". hold: the epilogue waits for an arrival nothing makes."""
     s = Sim(rng, timeout_p, late)
     n_ep = 2
     for i in range(stages):
         s.bar(f"FULL{i}", 1)
         s.bar(f"EMPTY{i}", 1)
     for i in range(2):
-        s.bar(f"AFULL{i}", 1)
+        s.bar(f"AFULL{i}", 2 if hold else 1)
         s.bar(f"AEMPTY{i}", n_ep)
     s.bar("DRAIN", 1)
-    s.bar("HOLD", 1)
     held, used, acc, stored = [None] * stages, [-1], [None, None], [0, 0]
     B = s.bars
 
@@ -185,8 +184,6 @@ def gemm(kblocks, stages, rng, timeout_p=0.0, late=False, drain="always", hold=F
             ab = n & 1
             if not (yield "wait", f"AFULL{ab}", (n >> 1) & 1):
                 return
-            if hold and n == 0 and not (yield "wait", "HOLD", 0):
-                return
             check(acc[ab] == n, "the epilogue reads another tile's accumulator")
             stored[ab] += 1
             B[f"AEMPTY{ab}"].arrive()
@@ -232,11 +229,11 @@ def bwd_pass(d, key, items, rng, timeout_p=0.0, late=False, drain="always", hold
         s.bar(f"FULL{i}", 1)
         s.bar(f"EMPTY{i}", 2 if d == 64 and key else 1)
     for i in range(2):
-        for name, count in (("SFULL", 2), ("SFREE", n_wg), ("IFULL", 1), ("IEMPTY", n_iss + n_wg), ("PREADY", n_wg),
+        for name, count in (("SFULL", 3 if hold else 2), ("SFREE", n_wg), ("IFULL", 1), ("IEMPTY", n_iss + n_wg), ("PREADY", n_wg),
                             ("PFREE", n_iss - 2)):
             s.bar(f"{name}{i}", count)
     for name, count in (("STATFULL", 1), ("STATEMPTY", 2), ("ACCFULL", n_iss - 2), ("ACCFREE", n_wg), ("COLS", n_wg),
-                        ("DRAIN", n_iss), ("HOLD", 1)):
+                        ("DRAIN", n_iss)):
         s.bar(name, count)
     info, pairs = [None, None], [None] * 4
     held, stat = [None] * 8, [None]             # what the slots and the stationary tiles hold
@@ -413,8 +410,6 @@ def bwd_pass(d, key, items, rng, timeout_p=0.0, late=False, drain="always", hold
                     return
                 check(pairs[gi & 3] == gi, "a warp reads another pair's tiles")
                 if not (yield "wait", f"SFULL{b}", (gi >> 1) & 1):
-                    return
-                if hold and gi == 0 and not (yield "wait", "HOLD", 0):
                     return
                 check(sbuf[b] == [gi, gi], f"a warp reads another pair's S or dP for {gi}")
                 read["s"][b] += 1

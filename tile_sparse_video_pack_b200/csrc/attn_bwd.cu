@@ -232,7 +232,7 @@ __device__ __forceinline__ bool last_use(uint32_t g, bool is_x, uint32_t gx, uin
 
 enum {
   Q_FULL = 0, Q_EMPTY = 8, Q_SFULL = 16, Q_SFREE = 18, Q_IFULL = 20, Q_IEMPTY = 22, Q_PREADY = 24, Q_PFREE = 26,
-  Q_STATFULL = 28, Q_STATEMPTY, Q_ACCFULL, Q_ACCFREE, Q_COLS, Q_DRAIN, Q_HOLD, Q_COUNT
+  Q_STATFULL = 28, Q_STATEMPTY, Q_ACCFULL, Q_ACCFREE, Q_COLS, Q_DRAIN, Q_COUNT
 };
 static_assert(Q_COUNT <= 40, "barrier slots");
 
@@ -249,7 +249,7 @@ struct BwdCommon {
   const int32_t* counts;            // [heads][nt_max]
   int32_t heads, bh_total, nt_max, words, key_ctas, by_head;
   float scale_log2, scale;
-  int32_t hold;                     // test hook: the step to P waits, at its first pair, on a barrier nothing arrives on
+  int32_t hold;                     // test hook: the step to P waits for a third arrival, which nothing makes
 };
 struct BwdMaps {
   CUtensorMap q, k, v, dO;
@@ -277,7 +277,7 @@ __device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMa
       mbar_init(bar(Q_EMPTY + i), D == 64 && KEY ? 2 : 1);   // d = 64: acc0 and acc1 read both of [Y; X]
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(Q_SFULL + i), 2);            // S and dP
+      mbar_init(bar(Q_SFULL + i), prm.hold ? 3 : 2);   // S and dP
       mbar_init(bar(Q_SFREE + i), 8);            // one arrival per warp of the warpgroups
       mbar_init(bar(Q_IFULL + i), 1);
       mbar_init(bar(Q_IEMPTY + i), kIssuers + 8);
@@ -292,7 +292,6 @@ __device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMa
     mbar_init(bar(Q_ACCFREE), 8);
     mbar_init(bar(Q_COLS), 8);
     mbar_init(bar(Q_DRAIN), kIssuers);
-    mbar_init(bar(Q_HOLD), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -543,7 +542,6 @@ __device__ __forceinline__ void bwd_pass(const CUtensorMap& tx, const CUtensorMa
         }
         const int b = int(g & 1);
         ok = wait_bar(bar(Q_SFULL + b), (g >> 1) & 1, abort_flag, gerr, prm.wait_ns);
-        if (prm.hold && g == 0) ok = ok && wait_bar(bar(Q_HOLD), 0, abort_flag, gerr, prm.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[32], dp[32];

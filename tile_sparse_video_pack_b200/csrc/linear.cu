@@ -241,7 +241,7 @@ struct GemmParams {
   int32_t n_prod, units;   // products and the tiles of all of them
   int32_t splits;          // CTAs of a cluster that share a tile's K
   int32_t group;           // row tiles per group of the tile order
-  int32_t hold;            // test hook: the epilogue waits, at its first tile, on a barrier nothing arrives on
+  int32_t hold;            // test hook: the epilogue waits for a second arrival, which nothing makes
 };
 struct GemmMaps {
   CUtensorMap a[2], b[2];
@@ -262,7 +262,7 @@ struct GSmem {
 // limit all the same: producer and issuer wait for one k block at a time.
 __device__ __forceinline__ uint64_t tile_limit(uint64_t wait_ns, int kblocks) { return wait_ns + uint64_t(kblocks) * 10000u; }
 
-enum { G_FULL = 0, G_EMPTY = 8, G_AFULL = 16, G_AEMPTY = 18, G_DRAIN = 20, G_HOLD = 21 };
+enum { G_FULL = 0, G_EMPTY = 8, G_AFULL = 16, G_AEMPTY = 18, G_DRAIN = 20 };
 
 // Tile u: tiles run down groups of `group` row tiles before the next column tile,
 // so that the CTAs at work share operand tiles in L2.
@@ -345,11 +345,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
       mbar_init(bar(G_EMPTY + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(G_AFULL + i), 1);
+      mbar_init(bar(G_AFULL + i), prm.hold ? 2 : 1);
       mbar_init(bar(G_AEMPTY + i), kEWarps);     // one arrival per epilogue warp
     }
     mbar_init(bar(G_DRAIN), 1);
-    mbar_init(bar(G_HOLD), 1);
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -415,7 +414,6 @@ __global__ void __launch_bounds__(kGThreads, 1)
         next = load_chunk(pr.ep, rows, pr.N, t.n * BN + c0, lane);
       }
       ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, tile_limit(prm.wait_ns, k1 - k0));
-      if (prm.hold && n == 0) ok = ok && wait_bar(bar(G_HOLD), 0, abort_flag, gerr, prm.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after();
@@ -536,11 +534,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       mbar_init(bar(G_EMPTY + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(G_AFULL + i), 1);
+      mbar_init(bar(G_AFULL + i), prm.hold ? 2 : 1);
       mbar_init(bar(G_AEMPTY + i), 2 * kEWarps); // the epilogue warps of both CTAs
     }
     mbar_init(bar(G_DRAIN), 1);
-    mbar_init(bar(G_HOLD), 1);
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -624,7 +621,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const StripRows rows = strip_rows(pr.ep, pr.M, int64_t(t.m) * 256 + rank * 128 + q4 * 32, lane);
       Chunk next = load_chunk(pr.ep, rows, pr.N, t.n * 256 + c0, lane);
       bool ok = wait_bar(bar(G_AFULL + ab), (n >> 1) & 1, abort_flag, gerr, tile_limit(prm.wait_ns, pr.kblocks));
-      if (prm.hold && n == 0) ok = ok && wait_bar(bar(G_HOLD), 0, abort_flag, gerr, prm.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
 #pragma unroll 1
