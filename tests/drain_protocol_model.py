@@ -46,7 +46,13 @@ class Sim:
 
     def __init__(self, rng, timeout_p=0.0, late=False):
         self.rng, self.timeout_p, self.late = rng, timeout_p, late
-        self.bars, self.roles, self.pending, self.abort, self.producers = {}, {}, [], False, set()
+        self.bars, self.roles, self.pending, self.producers = {}, {}, [], set()
+        self.flags = {0: False}          # abort flags by CTA
+        self.cta = {}                    # a role's CTA, 0 unless named
+
+    @property
+    def abort(self):
+        return any(self.flags.values())
 
     def bar(self, name, count):
         self.bars[name] = Bar(count)
@@ -57,13 +63,13 @@ class Sim:
     def commit(self, issuer, fn):        # an MMA issuer's commit: in order
         self.pending.append(("mma " + issuer, fn))
 
-    def _value(self, want):
+    def _value(self, role, want):
         kind = want[0]
         if kind == "until":
             return True if want[1]() else None
         if self.bars[want[1]].passed(want[2]):
             return True
-        return False if kind == "wait" and self.abort else None
+        return False if kind == "wait" and self.flags[self.cta.get(role, 0)] else None
 
     def run(self, max_steps=200_000):
         want = {}
@@ -82,12 +88,11 @@ class Sim:
                 check(not self.pending, "the CTA ends with work in flight: " + ", ".join(i for i, _ in self.pending))
                 return "aborted" if self.abort else "ok"
             gone = all(want[p] is None or want[p][0] == "drain" for p in self.producers)
-            if not self.abort and (gone or not self.late) and self.rng.random() < self.timeout_p:
-                blocked = [k for k in live if want[k][0] == "wait" and self._value(want[k]) is None]
-                if blocked:
-                    self.abort = True
-                    continue
-            choices = [("role", k) for k in live if self._value(want[k]) is not None]
+            blocked = [k for k in live if want[k][0] == "wait" and self._value(k, want[k]) is None]
+            if blocked and (gone or not self.late) and self.rng.random() < self.timeout_p:
+                self.flags[self.cta.get(self.rng.choice(blocked), 0)] = True
+                continue
+            choices = [("role", k) for k in live if self._value(k, want[k]) is not None]
             copies = [i for i, (who, _) in enumerate(self.pending) if who.startswith("tma ")]
             if not (self.late and choices):      # late: copies land when nothing else can move
                 choices += [("land", i) for i in copies]
@@ -98,14 +103,13 @@ class Sim:
             choices += [("land", i) for i in firsts.values()]
             if not choices:
                 stuck = "; ".join(f"{k}: {want[k][0]} {want[k][1:]}" for k in live)
-                if all(want[k][0] != "wait" for k in live):
+                if not blocked:
                     raise Hazard("a wait on the way out waits for nothing: " + stuck)
-                check(not self.abort, "stuck after the abort: " + stuck)
-                self.abort = True                            # a bounded wait runs out
+                self.flags[self.cta.get(self.rng.choice(blocked), 0)] = True     # a bounded wait runs out
                 continue
             kind, who = self.rng.choice(choices)
             if kind == "role":
-                step(who, self._value(want[who]))
+                step(who, self._value(who, want[who]))
             else:
                 self.pending.pop(who)[1]()
         raise Hazard("step limit")
@@ -190,6 +194,92 @@ def gemm(kblocks, stages, rng, timeout_p=0.0, late=False, drain="always", hold=F
 
     s.roles = {"producer": producer(), "mma": mma(), **{f"epilogue {i}": epilogue() for i in range(n_ep)}}
     s.producers = {"producer"}
+    return s.run()
+
+
+def gemm_pair(kblocks, rng, stages=3, timeout_p=0.0, late=False, hold=False):
+    """gemm_pair_kernel: two CTAs, each with a producer and epilogue warps (two here); CTA 0 issues. Both CTAs' loads
+    count on CTA 0's full barriers, its commits arrive in both CTAs. A producer stays until its last stages have
+    been used or, after a wait that ran out, until its copies have landed (the kernel: a time far above theirs)."""
+    s = Sim(rng, timeout_p, late)
+    s.flags = {0: False, 1: False}
+    n_ep, B = 2, s.bars
+    for i in range(stages):
+        s.bar(f"FULL{i}", 3)                     # the announcement of the bytes, and each CTA's copies
+        for r in range(2):
+            s.bar(f"EMPTY{r}{i}", 1)
+    for i in range(2):
+        s.bar(f"AEMPTY{i}", 2 * n_ep)
+        for r in range(2):
+            s.bar(f"AFULL{r}{i}", 2 if hold else 1)
+    s.bar("DRAIN", 1)
+    held, used, acc, stored = [[None] * stages for _ in range(2)], [-1], [None, None], [0, 0]
+
+    def producer(r):
+        it, ok = 0, True
+        for n in range(len(kblocks)):
+            for _ in range(kblocks[n]):
+                st = it % stages
+                ok = ok and (yield "wait", f"EMPTY{r}{st}", ((it // stages) & 1) ^ 1)
+                if not ok:
+                    break
+                check(used[0] >= it - stages, "a stage is filled before its products have read it")
+                if r == 0:
+                    B[f"FULL{st}"].arrive()
+
+                def land(st=st, it=it):
+                    held[r][st] = it
+                    B[f"FULL{st}"].arrive()
+                s.copy(f"p{r}", land)
+                it += 1
+        for j in range(max(0, it - stages), it):
+            ok = ok and (yield "wait", f"EMPTY{r}{j % stages}", (j // stages) & 1)
+        if not ok:
+            yield "until", lambda: not any(who == f"tma p{r}" for who, _ in s.pending)
+
+    def mma():
+        it, ok = 0, True
+        for n in range(len(kblocks)):
+            ab = n & 1
+            ok = ok and (yield "wait", f"AEMPTY{ab}", ((n >> 1) & 1) ^ 1)
+            if not ok:
+                break
+            check(n < 2 or stored[ab] == 2 * n_ep * (n // 2), "an accumulator is overwritten before it is read")
+            for _ in range(kblocks[n]):
+                st = it % stages
+                ok = yield "wait", f"FULL{st}", (it // stages) & 1
+                if not ok:
+                    break
+                check(held[0][st] == it and held[1][st] == it, "a product reads a stage that holds something else")
+
+                def done(st=st, it=it):
+                    used[0] = it
+                    B[f"EMPTY0{st}"].arrive()
+                    B[f"EMPTY1{st}"].arrive()
+                s.commit("m", done)
+                it += 1
+            if ok:
+                def full(ab=ab, n=n):
+                    acc[ab] = n
+                    B[f"AFULL0{ab}"].arrive()
+                    B[f"AFULL1{ab}"].arrive()
+                s.commit("m", full)
+        s.commit("m", B["DRAIN"].arrive)
+        yield "drain", "DRAIN", 0
+
+    def epilogue(r):
+        for n in range(len(kblocks)):
+            ab = n & 1
+            if not (yield "wait", f"AFULL{r}{ab}", (n >> 1) & 1):
+                return
+            check(acc[ab] == n, "the epilogue reads another tile's accumulator")
+            stored[ab] += 1
+            B[f"AEMPTY{ab}"].arrive()
+
+    s.roles = {"mma": mma(), **{f"producer {r}": producer(r) for r in range(2)},
+               **{f"epilogue {r}.{i}": epilogue(r) for r in range(2) for i in range(n_ep)}}
+    s.cta = {name: 1 for name in s.roles if name.startswith(("producer 1", "epilogue 1"))}
+    s.producers = {"producer 0", "producer 1"}
     return s.run()
 
 

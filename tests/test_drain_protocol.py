@@ -111,3 +111,14 @@ def test_attention_ends_with_nothing_in_flight_when_a_role_gives_up_late():
 
 def test_an_attention_that_asks_the_flag_leaves_copies_behind():
     assert outcomes(lambda rng: attention(rng, "tma_asks_flag"), 300, 8)["hazard"] > 0
+
+
+@pytest.mark.parametrize("hold", [False, True])
+@pytest.mark.parametrize("way", sorted(WAYS))
+def test_pairs_of_ctas(way, hold):
+    """Products on CTA pairs, an abort flag in each CTA."""
+    def run(rng):
+        kblocks, stages = M.random_gemm(rng)
+        return M.gemm_pair(kblocks, rng, stages, hold=hold, **WAYS[way])
+    seen = outcomes(run, 300, 9)
+    assert seen["hazard"] == 0 and (seen["ok"] == 300) == (way == "usual" and not hold), seen
