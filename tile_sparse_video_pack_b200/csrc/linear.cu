@@ -23,6 +23,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "tc_sm100.h"
 #include "tile_map.h"
 #include "vsa_internal.h"
@@ -69,8 +71,10 @@ __device__ __forceinline__ void act_fwd(float (&v)[8], int act) {
   }
 }
 // act(z) and act'(z) of two elements: with s = sigmoid(u), f = z s and
-// f' = s + f (1 - s) u' (SiLU: u = z; GELU: u the 2u above). Far out s is 0 or 1
-// exactly, and so is f': there f or u' may be infinite, and their factor 0.
+// f' = s + f (1 - s) u' (SiLU: u = z; GELU: u the 2u above), one polynomial for both.
+// Far out s is 0 or 1 exactly and so is f', but with |z| past 2^64 the polynomial (SiLU: 0
+// times infinity) and f' (0 times an infinite f or u') are NaN: FAR has their values.
+template <bool FAR>
 __device__ __forceinline__ void act_both(uint64_t z, int act, uint64_t& f, uint64_t& df) {
   const uint64_t one = f2pack(1.f, 1.f);
   if (act == VSA_ACT_NONE) {
@@ -78,24 +82,26 @@ __device__ __forceinline__ void act_both(uint64_t z, int act, uint64_t& f, uint6
     df = one;
     return;
   }
-  uint64_t x = fmul2(z, f2pack(-kLog2e, -kLog2e)), du = one;
-  if (act == VSA_ACT_GELU_TANH) {
-    constexpr float c1 = kGeluB, c3 = 0.044715f * kGeluB;
-    const uint64_t z2 = fmul2(z, z);
-    x = fmul2(x, ffma2(z2, f2pack(c3, c3), f2pack(c1, c1)));
-    du = ffma2(z2, f2pack(3.f * c3, 3.f * c3), f2pack(c1, c1));
-  }
-  float x0, x1, s0, s1, z0, z1, d0, d1;
+  const bool gelu = act == VSA_ACT_GELU_TANH;
+  const float c1 = gelu ? kGeluB : 1.f, c3 = gelu ? 0.044715f * kGeluB : 0.f;
+  const uint64_t z2 = fmul2(z, z);
+  uint64_t x = fmul2(z, f2pack(-kLog2e, -kLog2e));
+  if (!FAR || gelu) x = fmul2(x, ffma2(z2, f2pack(c3, c3), f2pack(c1, c1)));
+  float x0, x1;
   f2unpack(x, x0, x1);
   f2unpack(fadd2(f2pack(ex2(x0), ex2(x1)), one), x0, x1);
-  s0 = rcp(x0);
-  s1 = rcp(x1);
-  const uint64_t s = f2pack(s0, s1);
+  const uint64_t s = f2pack(rcp(x0), rcp(x1));
   f = fmul2(z, s);
-  f2unpack(ffma2(fmul2(f, ffma2(s, f2pack(-1.f, -1.f), one)), du, s), d0, d1);
-  f2unpack(z, z0, z1);
-  constexpr float kFar = 1e4f;
-  df = f2pack(fabsf(z0) > kFar ? s0 : d0, fabsf(z1) > kFar ? s1 : d1);
+  const uint64_t du = ffma2(z2, f2pack(3.f * c3, 3.f * c3), f2pack(c1, c1));
+  df = ffma2(fmul2(f, ffma2(s, f2pack(-1.f, -1.f), one)), du, s);
+  if constexpr (FAR) {
+    constexpr float kFar = 1e4f;
+    float z0, z1, s0, s1, d0, d1;
+    f2unpack(z, z0, z1);
+    f2unpack(s, s0, s1);
+    f2unpack(df, d0, d1);
+    df = f2pack(fabsf(z0) > kFar ? s0 : d0, fabsf(z1) > kFar ? s1 : d1);
+  }
 }
 
 // -------------------------------------------------------------- epilogue ----
@@ -760,7 +766,7 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
   int64_t r1 = r0 + p.chunk;
   if (r1 > end) r1 = end;
   if (r1 > p.rows) r1 = p.rows;
-  uint64_t sz[4] = {}, sg[4] = {}, gt[4];
+  uint64_t sz[4], sg[4], gt[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) gt[i] = f2pack(1.f, 1.f);
   const bool on = col < p.N;
@@ -770,8 +776,12 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < 4; ++i) gt[i] = f2pack(g[2 * i], g[2 * i + 1]);
   }
-  if (on) {
+  // this thread's columns of its rows
+  auto walk = [&](auto far) {
     constexpr int U = 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sz[i] = sg[i] = 0ull;
+    if (!on) return;
     for (int64_t r = r0 + warp; r < r1; r += 8 * U) {
       uint4 vy[U], vz[U];
 #pragma unroll
@@ -793,7 +803,7 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
         for (int i = 0; i < 4; ++i) {
           uint64_t d = f2pack(dy[2 * i], dy[2 * i + 1]), f, df;
           if (p.pre) {
-            act_both(f2pack(z[2 * i], z[2 * i + 1]), p.act, f, df);
+            act_both<decltype(far)::value>(f2pack(z[2 * i], z[2 * i + 1]), p.act, f, df);
             sg[i] = ffma2(d, f, sg[i]);
             d = fmul2(fmul2(d, gt[i]), df);
           } else {
@@ -805,7 +815,14 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
         if (p.dz) *reinterpret_cast<uint4*>(p.dz + rr * p.N + col) = to_bf16x8(dy);
       }
     }
-  }
+  };
+  walk(std::false_type{});
+  // A pre-activation too far out for the common polynomial has made its column's sum NaN: once more, with care. (The
+  // two comparisons that this takes cost 8 % when every element makes them.)
+  uint64_t all = fadd2(fadd2(sz[0], sz[1]), fadd2(sz[2], sz[3]));
+  float all0, all1;
+  f2unpack(all, all0, all1);
+  if (p.pre && isnan(all0 + all1)) walk(std::true_type{});
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f2unpack(sz[i], red[0][warp][lane * 8 + 2 * i], red[0][warp][lane * 8 + 2 * i + 1]);
