@@ -504,8 +504,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
 // loads of both CTAs count on the leader's full barrier, the products' completion
 // arrives in both CTAs. Two 256-column accumulators fill TMEM: a tile's epilogue
 // runs under the next tile's products.
-// 18,944 x 2,048 with K 8,192: 457 us, 1,390 TFLOP/s (395 on zeros: the rest is power);
-// K 2,048 with gate and residual 126 us, 1,240.
+// 18,944 x 2,048 with K 8,192: 468 us, 1,360 TFLOP/s at 1,965 MHz, 554 us once the power cap holds (1,400 MHz), 380 on
+// zeros; K 2,048 with gate and residual (18,560 rows) 126 to 131 us, 147 to 153 with the cap. The tensor pipe is
+// active 66 to 71 % of the time (K 2,048).
 constexpr int kPStages = 6;
 struct PSmem {
   static constexpr uint32_t kA = 128 * 128, kB = 128 * 128, kStage = kA + kB;
@@ -753,7 +754,7 @@ struct GradParams {
 // eight) of one chunk of rows, which lies in one sample; its eight warps take
 // every eighth row, four at a time so that enough loads are in flight (one row at a time
 // and the library's exponential and division: 238 us at 9,280 x 8,192, where the bytes take 70;
-// now 75), and meet in shared memory.
+// now 89), and meet in shared memory.
 __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ GradParams p) {
   __shared__ float red[2][8][256];
   allow_successor();
