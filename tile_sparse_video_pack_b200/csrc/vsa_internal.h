@@ -75,7 +75,7 @@ struct vsa_plan {
   int attn_smem_bytes;
   int list_cap;            // entries of one key-list buffer in the attention kernel
   uint64_t wait_ns;        // bound of every device-side wait of the tcgen05 kernels
-  int32_t test_hold;       // test hook: the attention softmax waits for a release nothing gives
+  int32_t test_hold;       // test hook: attention, its gradient and the products wait for what nothing gives
 };
 
 namespace vsa {
